@@ -359,6 +359,213 @@ int muon_adamw_step(const muon_adamw_tensor_t* tensors, int64_t n_tensors, float
                     float beta2, float eps, float wd, void* workspace, size_t workspace_bytes,
                     hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Training operators beside the optimizer step: what makes the gradients
+ * that muon_step and muon_adamw_step take, from activations kept in 8 bits.
+ *
+ *   muon_rmsnorm_act8 / _grad   RMS norm with the residual's addition; keeps
+ *                               the normalised rows in 8 bits
+ *   muon_swiglu_act8 / _grad    gated unit silu(gate) * up; keeps both in 8 bits
+ *   muon_act8_pack / _unpack    the 8-bit form of any matrix, and back
+ *   muon_act8_wgrad             weight gradient dY^T X from an 8-bit X
+ *   muon_embed / _grad          embedding lookup and its gradient
+ *
+ * Matrices are row-major with unit column stride; each has its own row
+ * stride ("ld", in elements, >= the row's length; not read where there is one
+ * row).  Rows may start anywhere (aligned to their element).  rows and tokens
+ * are 0 .. 2^31 - 1 (0: nothing is written, except that gradients summed over
+ * rows are zero then), cols 1 .. MUON_MAX_DIM.
+ *
+ * These calls stage nothing through host memory: their arguments travel with
+ * the launches.  They may be captured into a graph, and the structs are read
+ * during the call only.  Outputs must not overlap each other or an input
+ * (MUON_EALIAS; column slices of one buffer with one row stride do not).
+ * Sums run in fp32 in an order that depends on the shapes alone: the same
+ * call on the same values gives the same bits.  Errors, the stream's device
+ * and MUON_DEBUG are as for muon_step (under MUON_DEBUG a workspace is filled
+ * with NaN first; on a capturing stream the variable is ignored).  Phase
+ * timing does not record them.
+ * ------------------------------------------------------------------------ */
+
+/* A matrix in 8 bits.  Each group of 32 consecutive columns of a row (the
+ * last one may be shorter) shares a power of two s = 2^e, the smallest with
+ * max |v| <= 448 s and -117 <= e <= 119; each value is v / s rounded to the
+ * nearest 8-bit float of 4 exponent and 3 mantissa bits (finite, largest 448;
+ * ties to even; 0x7F and 0xFF are NaN).  |v - value| <= max(2^-4 |v|, 2^-10 s),
+ * and the value is exact in bf16.  Infinities and NaN become NaN and do not
+ * count in the maximum, so they leave the rest of their group as it is;
+ * finite values beyond 448 * 2^119 saturate.
+ *   codes   rows x ld_codes bytes
+ *   scales  rows x ld_scales bytes, e + 127 of each group (10 .. 246; the
+ *           calls that read them take any byte, b as 2^(b - 127), but their
+ *           results are defined for 10 .. 246 only) */
+#define MUON_ACT8_GROUP 32
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t  ld_codes;    /* >= cols */
+  int64_t  ld_scales;   /* >= (cols + 31) / 32 */
+} muon_act8_t;
+
+/* x (fp32 or bf16) -> its 8-bit form; and the values it stands for. */
+int muon_act8_pack(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t cols,
+                   const muon_act8_t* out, hipStream_t stream);
+int muon_act8_unpack(const muon_act8_t* in, int64_t rows, int64_t cols, void* out, int64_t ld_out,
+                     int32_t dtype, hipStream_t stream);
+
+/* RMS norm of h = x + residual, row by row, in fp32 from the unrounded sum:
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  n = h rstd,  y = n gain.
+ * cols <= MUON_NORM_MAX_COLS (a row stays in one workgroup's registers).
+ *   x, residual  dtype; residual may be NULL (h = x)
+ *   gain         fp32 [cols], NULL: 1
+ *   h, y         dtype, each rounded once; either may be NULL
+ *   n            8-bit form of n (before the gain); codes NULL: not kept
+ *   rstd         fp32 [rows]; may be NULL
+ * n and rstd are all that the backward pass needs: x, residual and h may go. */
+#define MUON_NORM_MAX_COLS 16384
+typedef struct {
+  const void*  x;
+  const void*  residual;
+  const float* gain;
+  void*        h;
+  void*        y;
+  muon_act8_t  n;
+  float*       rstd;
+  int64_t      rows, cols;
+  int64_t      ld_x, ld_residual, ld_h, ld_y;
+  float        eps;       /* >= 0 */
+  int32_t      dtype;     /* MUON_F32 or MUON_BF16: x, residual, h, y */
+} muon_rmsnorm_t;
+int muon_rmsnorm_act8(const muon_rmsnorm_t* op, hipStream_t stream);
+
+/* Backward pass of the norm, with n read from its 8-bit form:
+ *   dx    = rstd (gain dy - n mean(gain dy n)) + dres
+ *   dgain = sum over rows of dy n
+ * dx is the gradient of x and of residual alike (h is their sum).
+ *   dy, dres  dtype; dres (the gradient that reaches h on its own path, the
+ *             residual stream's) may be NULL
+ *   dx        dtype;  dgain  fp32 [cols], may be NULL
+ *   workspace muon_rmsnorm_act8_grad_workspace_bytes(rows, cols), 256-byte
+ *             aligned; not needed where dgain is NULL */
+typedef struct {
+  const void*  dy;
+  const void*  dres;
+  const float* gain;
+  const float* rstd;
+  muon_act8_t  n;
+  void*        dx;
+  float*       dgain;
+  int64_t      rows, cols;
+  int64_t      ld_dy, ld_dres, ld_dx;
+  int32_t      dtype;
+  int32_t      reserved;  /* must be 0 */
+} muon_rmsnorm_grad_t;
+size_t muon_rmsnorm_act8_grad_workspace_bytes(int64_t rows, int64_t cols);
+int muon_rmsnorm_act8_grad(const muon_rmsnorm_grad_t* op, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* Gated unit: a = silu(gate) up = gate / (1 + exp(-gate)) up, in fp32.
+ *   gate, up       dtype
+ *   a              dtype; may be NULL
+ *   gate8, up8     8-bit forms of gate and up, for the backward pass; codes
+ *                  NULL (both): not kept */
+typedef struct {
+  const void* gate;
+  const void* up;
+  void*       a;
+  muon_act8_t gate8, up8;
+  int64_t     rows, cols;
+  int64_t     ld_gate, ld_up, ld_a;
+  int32_t     dtype;
+  int32_t     reserved;   /* must be 0 */
+} muon_swiglu_t;
+int muon_swiglu_act8(const muon_swiglu_t* op, hipStream_t stream);
+
+/* Its backward pass from the 8-bit gate and up, with s = 1 / (1 + exp(-gate)):
+ *   dgate = da up s (1 + gate (1 - s)),   dup = da gate s
+ *   a8    8-bit form of a = gate s up, recomputed: the activation that the next
+ *         product's weight gradient needs (codes NULL: not made)
+ * da, dgate, dup: dtype. */
+typedef struct {
+  const void* da;
+  muon_act8_t gate8, up8;
+  void*       dgate;
+  void*       dup;
+  muon_act8_t a8;
+  int64_t     rows, cols;
+  int64_t     ld_da, ld_dgate, ld_dup;
+  int32_t     dtype;
+  int32_t     reserved;   /* must be 0 */
+} muon_swiglu_grad_t;
+int muon_swiglu_act8_grad(const muon_swiglu_grad_t* op, hipStream_t stream);
+
+/* Weight gradient of y = x W^T (W: n x k, as muon_step holds it) from the
+ * 8-bit form of x:
+ *   dw[i][j] (+)= col_gain[j] sum_t dy[t][i] x[t][j]
+ * Products of bf16 with the exact values of x8, summed in fp32; the total is
+ * rounded once to dw's type.
+ *   dy        bf16, tokens x n
+ *   x8        tokens x k
+ *   col_gain  fp32 [k], NULL: 1.  With x8 the norm's n this folds the norm's
+ *             gain in: x = n gain
+ *   dw        n x k, dw_dtype (MUON_F32 or MUON_BF16), 1 <= n, k; accumulate
+ *             != 0 adds to what it holds, else it is overwritten
+ *   workspace muon_act8_wgrad_workspace_bytes(op) bytes, 256-byte aligned
+ *             (may be 0, and NULL then).  Depends on the sizes, strides and
+ *             alignments. */
+typedef struct {
+  const void*  dy;
+  muon_act8_t  x8;
+  const float* col_gain;
+  void*        dw;
+  int64_t      tokens, n, k;
+  int64_t      ld_dy, ld_dw;
+  int32_t      dw_dtype;
+  int32_t      accumulate;
+} muon_act8_wgrad_t;
+size_t muon_act8_wgrad_workspace_bytes(const muon_act8_wgrad_t* op);
+int muon_act8_wgrad(const muon_act8_wgrad_t* op, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
+/* Embedding lookup: out[t] = scale * table[ids[t]], the product in fp32,
+ * rounded to out_dtype.  A token whose id is outside 0 .. vocab - 1 (-1 for padding, say)
+ * gets a row of zeros, and no gradient below.
+ *   table  vocab x cols, table_dtype;  ids  int32 or int64 (id_bytes 4 or 8)
+ *   out    tokens x cols, out_dtype */
+typedef struct {
+  const void* table;
+  const void* ids;
+  void*       out;
+  int64_t     tokens, vocab, cols;   /* vocab 1 .. 2^31 - 2 */
+  int64_t     ld_table, ld_out;
+  float       scale;                 /* finite */
+  int32_t     table_dtype, out_dtype;
+  int32_t     id_bytes;
+} muon_embed_t;
+int muon_embed(const muon_embed_t* op, hipStream_t stream);
+
+/* Its gradient, from the tokens sorted by id:
+ *   dtable[v] (+)= scale * sum over t with ids[t] == v of dy[t]
+ * every row is written (zeros where no token has its id) unless accumulate.
+ *   dy        tokens x cols, dy_dtype;  dtable  vocab x cols, table_dtype
+ *   workspace muon_embed_grad_workspace_bytes(tokens, vocab, cols) bytes,
+ *             256-byte aligned */
+typedef struct {
+  const void* dy;
+  const void* ids;
+  void*       dtable;
+  int64_t     tokens, vocab, cols;
+  int64_t     ld_dy, ld_dtable;
+  float       scale;
+  int32_t     dy_dtype, table_dtype;
+  int32_t     id_bytes;
+  int32_t     accumulate;
+  int32_t     reserved;              /* must be 0 */
+} muon_embed_grad_t;
+size_t muon_embed_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols);
+int muon_embed_grad(const muon_embed_grad_t* op, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
 /* Phase timing with HIP events, for benchmarks.  When enabled, every launch
  * is bracketed by a pair of events on the call's stream, and a step keeps
  * all its launches on that stream (no side-stream overlap, so that each

@@ -328,3 +328,18 @@ def timing_read() -> dict:
     cnt = (ctypes.c_int64 * _lib.MUON_PHASES)()
     _lib.check(_lib.load().muon_timing_read(ms, cnt), "muon_timing_read")
     return {name: {"ms": ms[k], "launches": cnt[k]} for k, name in enumerate(PHASE_NAMES)}
+
+
+# Training operators that make the gradients of a step (ops.py); resolved on
+# first use, so that importing the package does not import torch.
+_OPS = ("Act8", "act8_pack", "act8_unpack", "act8_wgrad", "rmsnorm_act8", "rmsnorm_act8_grad",
+        "swiglu_act8", "swiglu_act8_grad", "embed", "embed_grad")
+
+
+def __getattr__(name):
+    if name in _OPS:
+        from . import ops
+        for n in _OPS:
+            globals()[n] = getattr(ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

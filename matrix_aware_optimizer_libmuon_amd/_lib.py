@@ -41,7 +41,12 @@ EXPORTED = ("muon_workspace_bytes", "muon_step", "muon_step_ex", "muon_plan_crea
             "muon_workspace_view",
             "muon_adamw_workspace_bytes", "muon_adamw_step",
             "muon_timing_enable", "muon_timing_read", "muon_status_string", "muon_version",
-            "muon_step_noalloc", "muon_noalloc_scratch")
+            "muon_step_noalloc", "muon_noalloc_scratch",
+            "muon_act8_pack", "muon_act8_unpack",
+            "muon_rmsnorm_act8", "muon_rmsnorm_act8_grad_workspace_bytes", "muon_rmsnorm_act8_grad",
+            "muon_swiglu_act8", "muon_swiglu_act8_grad",
+            "muon_act8_wgrad_workspace_bytes", "muon_act8_wgrad",
+            "muon_embed", "muon_embed_grad_workspace_bytes", "muon_embed_grad")
 
 
 class MuonMatrix(ctypes.Structure):
@@ -77,6 +82,67 @@ class MuonWorkspaceView(ctypes.Structure):
                 ("nrm2_off", ctypes.c_size_t), ("rows_pad", ctypes.c_int64),
                 ("cols_pad", ctypes.c_int64), ("m_pad", ctypes.c_int64),
                 ("transposed", ctypes.c_int32), ("tile", ctypes.c_int32)]
+
+
+# Training operators (ops.py)
+class MuonAct8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("ld_codes", ctypes.c_int64), ("ld_scales", ctypes.c_int64)]
+
+
+def _int64s(*names):
+    return [(n, ctypes.c_int64) for n in names]
+
+
+class MuonRmsnorm(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("gain", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("y", ctypes.c_void_p), ("n", MuonAct8),
+                ("rstd", ctypes.c_void_p),
+                *_int64s("rows", "cols", "ld_x", "ld_residual", "ld_h", "ld_y"),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class MuonRmsnormGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("dres", ctypes.c_void_p), ("gain", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("n", MuonAct8), ("dx", ctypes.c_void_p),
+                ("dgain", ctypes.c_void_p),
+                *_int64s("rows", "cols", "ld_dy", "ld_dres", "ld_dx"),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MuonSwiglu(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("a", ctypes.c_void_p),
+                ("gate8", MuonAct8), ("up8", MuonAct8),
+                *_int64s("rows", "cols", "ld_gate", "ld_up", "ld_a"),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MuonSwigluGrad(ctypes.Structure):
+    _fields_ = [("da", ctypes.c_void_p), ("gate8", MuonAct8), ("up8", MuonAct8),
+                ("dgate", ctypes.c_void_p), ("dup", ctypes.c_void_p), ("a8", MuonAct8),
+                *_int64s("rows", "cols", "ld_da", "ld_dgate", "ld_dup"),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MuonAct8Wgrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("x8", MuonAct8), ("col_gain", ctypes.c_void_p),
+                ("dw", ctypes.c_void_p), *_int64s("tokens", "n", "k", "ld_dy", "ld_dw"),
+                ("dw_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class MuonEmbed(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                *_int64s("tokens", "vocab", "cols", "ld_table", "ld_out"),
+                ("scale", ctypes.c_float), ("table_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("id_bytes", ctypes.c_int32)]
+
+
+class MuonEmbedGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("dtable", ctypes.c_void_p),
+                *_int64s("tokens", "vocab", "cols", "ld_dy", "ld_dtable"),
+                ("scale", ctypes.c_float), ("dy_dtype", ctypes.c_int32),
+                ("table_dtype", ctypes.c_int32), ("id_bytes", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -143,6 +209,22 @@ def load() -> ctypes.CDLL:
     lib.muon_step_noalloc.restype = ctypes.c_int
     lib.muon_noalloc_scratch.argtypes = []
     lib.muon_noalloc_scratch.restype = ctypes.c_void_p
+    i32, i64, size_t, ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+    for name, res, args in (
+            ("muon_act8_pack", ctypes.c_int, [ptr, i64, i32, i64, i64, P(MuonAct8), ptr]),
+            ("muon_act8_unpack", ctypes.c_int, [P(MuonAct8), i64, i64, ptr, i64, i32, ptr]),
+            ("muon_rmsnorm_act8", ctypes.c_int, [P(MuonRmsnorm), ptr]),
+            ("muon_rmsnorm_act8_grad_workspace_bytes", size_t, [i64, i64]),
+            ("muon_rmsnorm_act8_grad", ctypes.c_int, [P(MuonRmsnormGrad), ptr, size_t, ptr]),
+            ("muon_swiglu_act8", ctypes.c_int, [P(MuonSwiglu), ptr]),
+            ("muon_swiglu_act8_grad", ctypes.c_int, [P(MuonSwigluGrad), ptr]),
+            ("muon_act8_wgrad_workspace_bytes", size_t, [P(MuonAct8Wgrad)]),
+            ("muon_act8_wgrad", ctypes.c_int, [P(MuonAct8Wgrad), ptr, size_t, ptr]),
+            ("muon_embed", ctypes.c_int, [P(MuonEmbed), ptr]),
+            ("muon_embed_grad_workspace_bytes", size_t, [i64, i64, i64]),
+            ("muon_embed_grad", ctypes.c_int, [P(MuonEmbedGrad), ptr, size_t, ptr])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = res, args
     lib.muon_version.argtypes = []
     lib.muon_version.restype = ctypes.c_char_p
     _lib = lib

@@ -31,7 +31,12 @@ SOURCES = [
     ("muon_gemm128.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]),
     ("muon_fused.hip", []),
     ("muon_noalloc.hip", []),
+    ("muon_act8.hip", []),
+    ("muon_norm.hip", []),
+    ("muon_embed.hip", []),
+    ("muon_wgrad.hip", []),
     ("muon_api.cpp", []),
+    ("muon_ops.cpp", []),
 ]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -77,8 +82,8 @@ def _marshal_cmd(out):
             f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-DTORCH_EXTENSION_NAME=_marshal",
             "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include",
             *[f"-I{p}" for p in ce.include_paths()], f"-I{sysconfig.get_paths()['include']}",
-            os.path.join(CSRC, "marshal.cpp"), "-o", out,
-            f"-L{libdir}", "-lc10", "-ltorch", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libdir}"]
+            os.path.join(CSRC, "marshal.cpp"), os.path.join(CSRC, "marshal_ops.cpp"), "-o", out,
+            f"-L{libdir}", "-lc10", "-lc10_hip", "-ltorch", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libdir}"]
 
 
 def build(verbose: bool = False) -> str:
@@ -123,7 +128,7 @@ def build_asan(out_dir: str, verbose: bool = False) -> str:
     jobs, objs = [], []
     for src, extra in SOURCES:
         obj = os.path.join(out_dir, os.path.splitext(src)[0] + ".o")
-        if src == "muon_api.cpp":
+        if src.endswith(".cpp"):
             extra = [*extra, "-Xarch_host", "-fsanitize=address", "-fno-omit-frame-pointer", "-g"]
         jobs.append(_start([HIPCC, *FLAGS, *extra, "-c", "-o", obj, os.path.join(CSRC, src)], verbose))
         objs.append(obj)

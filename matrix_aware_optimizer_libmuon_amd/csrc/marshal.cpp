@@ -166,6 +166,8 @@ void fill_adamw(const std::vector<at::Tensor>& params, const std::vector<OptTens
 
 }  // namespace
 
+void register_ops(py::module_& mod);  // marshal_ops.cpp
+
 PYBIND11_MODULE(_marshal, mod) {
   mod.doc() = "libmuon argument marshalling (fills C-ABI descriptor arrays from tensors)";
   mod.def("fill_matrices", &fill_matrices);
@@ -174,4 +176,5 @@ PYBIND11_MODULE(_marshal, mod) {
   mod.attr("MATRIX_BYTES") = sizeof(muon_matrix_t);
   mod.attr("ORTHO_BYTES") = sizeof(muon_ortho_t);
   mod.attr("ADAMW_BYTES") = sizeof(muon_adamw_tensor_t);
+  register_ops(mod);
 }

@@ -18,6 +18,7 @@
 
 #include "muon.h"
 #include "muon_internal.h"
+#include "muon_ops.h"
 
 using namespace muon;
 
@@ -793,6 +794,12 @@ struct muon_plan {
   SidePair side;  // own fork / join pair, when the step forks
   ~muon_plan() { free_side(side); }
 };
+
+namespace muon {
+int host_hip_fail(int hip_error, const char* what) { return hip_fail(static_cast<hipError_t>(hip_error), what); }
+bool host_debug() { return debug_env(); }
+bool host_stream_on_device(void* stream, int dev) { return stream_on_device(static_cast<hipStream_t>(stream), dev); }
+}  // namespace muon
 
 extern "C" {
 

@@ -1,0 +1,58 @@
+// What the host side of the training operators (muon_ops.cpp) shares with their
+// kernels and with muon_api.cpp.  Each launcher returns hipError_t as int; its
+// arguments have been checked.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include "muon.h"
+
+namespace muon {
+
+// Host helpers of muon_api.cpp: keep the HIP error text for
+// muon_status_string (returns MUON_EHIP); whether MUON_DEBUG is set; whether
+// `stream` (a hipStream_t) can belong to device `dev`.
+int host_hip_fail(int hip_error, const char* what);
+bool host_debug();
+bool host_stream_on_device(void* stream, int dev);
+
+// muon_act8.hip
+int launch_act8_pack(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t cols,
+                     const muon_act8_t& out, void* stream);
+int launch_act8_unpack(const muon_act8_t& in, int64_t rows, int64_t cols, void* out, int64_t ld_out,
+                       int32_t dtype, void* stream);
+int launch_swiglu(const muon_swiglu_t& op, void* stream);
+int launch_swiglu_grad(const muon_swiglu_grad_t& op, void* stream);
+
+// muon_norm.hip
+int launch_rmsnorm(const muon_rmsnorm_t& op, void* stream);
+// blocks of the backward pass, each with its own partial dgain (one: none needed)
+int64_t rmsnorm_grad_blocks(int64_t rows, int64_t cols);
+int launch_rmsnorm_grad(const muon_rmsnorm_grad_t& op, float* partial, void* stream);
+int launch_rmsnorm_dgain(const float* partial, int64_t blocks, int64_t cols, float* dgain, void* stream);
+
+// muon_wgrad.hip
+struct WgradPlan {
+  int64_t tiles_n, tiles_k;   // output tiles
+  int64_t splits, split_rows; // token ranges of split_rows (the last one may be shorter)
+  size_t bytes;               // workspace: splits partial outputs where splits > 1
+};
+WgradPlan wgrad_plan(const muon_act8_wgrad_t& op);
+int launch_wgrad(const muon_act8_wgrad_t& op, const WgradPlan& p, void* workspace, void* stream);
+int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const void* workspace, void* stream);
+
+// muon_embed.hip
+struct EmbedSortPlan {
+  int passes;                 // 8-bit digits of the keys 0 .. vocab
+  int64_t blocks;             // blocks of a pass, block_tokens tokens each
+  int64_t block_tokens;
+  size_t keys_off[2], toks_off[2], count_off;
+  size_t bytes;
+};
+EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols);
+int launch_embed(const muon_embed_t& op, void* stream);
+int launch_embed_count(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream);
+int launch_embed_scatter(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream);
+int launch_embed_rows(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
+
+}  // namespace muon

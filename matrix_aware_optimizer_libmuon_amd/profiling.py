@@ -34,12 +34,17 @@ ROOT = os.path.dirname(PKG)
 _COMMON = ("muon_device.h", "muon_internal.h")
 _ELEMENTWISE = _COMMON + ("muon_kernels.hip",)
 _GEMM = _COMMON + ("muon_gemm.h", "muon_gemm256.hip", "muon_gemm128.hip")
+_OPS = ("muon_ops.h", "muon_act8.h")
 # the sources each bench phase's kernel is compiled from
 SOURCES_OF = {"momentum_norm": _ELEMENTWISE, "normalize_cast": _ELEMENTWISE, "apply": _ELEMENTWISE,
               "adamw": _ELEMENTWISE, "gram": _GEMM, "gram2_epilogue": _GEMM, "x_update": _GEMM,
               "ns_fused": _COMMON + ("muon_fused.hip",),
               # the descriptor-table writer of the no-allocation step (no bench phase)
-              "noalloc_table": _COMMON + ("muon_noalloc.hip",)}
+              "noalloc_table": _COMMON + ("muon_noalloc.hip",),
+              # the training operators (no bench phase)
+              "act8": _COMMON + _OPS + ("muon_act8.hip",), "norm": _COMMON + _OPS + ("muon_norm.hip",),
+              "embed": _COMMON + _OPS + ("muon_embed.hip",),
+              "wgrad": _COMMON + _OPS + ("muon_gemm.h", "muon_wgrad.hip")}
 KERNEL_SOURCES = tuple(sorted({f for files in SOURCES_OF.values() for f in files}))
 TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "muon_step_transformer_d4096_hbm_traffic.md")
 MFMA_PROFILE = os.path.join(ROOT, "profiles", "muon_step_transformer_d4096_mfma_util.md")

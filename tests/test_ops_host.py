@@ -1,0 +1,221 @@
+"""Host-side checks of the training operators' C entries and of their binding
+that need no GPU: bad arguments are refused before anything is launched."""
+import ctypes
+import os
+import random
+
+import pytest
+
+import matrix_aware_optimizer_libmuon_amd as muon
+from matrix_aware_optimizer_libmuon_amd import _lib as L
+
+torch = pytest.importorskip("torch")
+EINVAL, EALIAS, EWORKSPACE = muon.MUON_EINVAL, muon.MUON_EALIAS, muon.MUON_EWORKSPACE
+BF16, F32 = muon.MUON_BF16, muon.MUON_F32
+WS = ctypes.c_void_p(1 << 42)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(L.LIB_PATH):
+        from matrix_aware_optimizer_libmuon_amd import build
+        build.build()
+    return L.load()
+
+
+_next = [1 << 36]
+
+
+def ptr():
+    """A fresh address, far from every other (never read: the calls below fail on the host)."""
+    _next[0] += 1 << 28
+    return _next[0]
+
+
+def act8(cols=64, **kw):
+    a = L.MuonAct8(ptr(), ptr(), cols, (cols + 31) // 32)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def with_(s, **kw):
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def norm(**kw):
+    return with_(L.MuonRmsnorm(x=ptr(), residual=ptr(), gain=ptr(), h=ptr(), y=ptr(), n=act8(), rstd=ptr(), rows=8, cols=64,
+                               ld_x=64, ld_residual=64, ld_h=64, ld_y=64, eps=1e-6, dtype=BF16), **kw)
+
+
+def norm_grad(**kw):
+    return with_(L.MuonRmsnormGrad(dy=ptr(), dres=ptr(), gain=ptr(), rstd=ptr(), n=act8(), dx=ptr(), dgain=ptr(), rows=4000,
+                                   cols=64, ld_dy=64, ld_dres=64, ld_dx=64, dtype=BF16), **kw)
+
+
+def gate(**kw):
+    return with_(L.MuonSwiglu(gate=ptr(), up=ptr(), a=ptr(), gate8=act8(), up8=act8(), rows=8, cols=64, ld_gate=64, ld_up=64,
+                              ld_a=64, dtype=BF16), **kw)
+
+
+def gate_grad(**kw):
+    return with_(L.MuonSwigluGrad(da=ptr(), gate8=act8(), up8=act8(), dgate=ptr(), dup=ptr(), a8=act8(), rows=8, cols=64,
+                                  ld_da=64, ld_dgate=64, ld_dup=64, dtype=BF16), **kw)
+
+
+def wgrad(**kw):
+    return with_(L.MuonAct8Wgrad(dy=ptr(), x8=act8(), col_gain=ptr(), dw=ptr(), tokens=5000, n=64, k=64, ld_dy=64, ld_dw=64,
+                                 dw_dtype=F32, accumulate=0), **kw)
+
+
+def embed(**kw):
+    return with_(L.MuonEmbed(table=ptr(), ids=ptr(), out=ptr(), tokens=9, vocab=100, cols=64, ld_table=64, ld_out=64, scale=1.0,
+                             table_dtype=F32, out_dtype=BF16, id_bytes=8), **kw)
+
+
+def embed_grad(**kw):
+    return with_(L.MuonEmbedGrad(dy=ptr(), ids=ptr(), dtable=ptr(), tokens=900, vocab=100, cols=64, ld_dy=64, ld_dtable=64,
+                                 scale=1.0, dy_dtype=BF16, table_dtype=F32, id_bytes=8), **kw)
+
+
+def test_struct_layouts_match_header(lib):
+    sizes = muon._marshaller().OP_BYTES
+    for name, cls in (("muon_act8_t", L.MuonAct8), ("muon_rmsnorm_t", L.MuonRmsnorm),
+                      ("muon_rmsnorm_grad_t", L.MuonRmsnormGrad), ("muon_swiglu_t", L.MuonSwiglu),
+                      ("muon_swiglu_grad_t", L.MuonSwigluGrad), ("muon_act8_wgrad_t", L.MuonAct8Wgrad),
+                      ("muon_embed_t", L.MuonEmbed), ("muon_embed_grad_t", L.MuonEmbedGrad)):
+        assert sizes[name] == ctypes.sizeof(cls), name
+
+
+def test_pack_and_unpack_refuse(lib):
+    def pack(x=ptr(), ld=64, dtype=BF16, rows=8, cols=64, out=act8()):
+        return lib.muon_act8_pack(x, ld, dtype, rows, cols, ctypes.byref(out) if out else None, None)
+
+    def unpack(src=act8(), rows=8, cols=64, out=ptr(), ld=64, dtype=BF16):
+        return lib.muon_act8_unpack(ctypes.byref(src) if src else None, rows, cols, out, ld, dtype, None)
+
+    for bad in (dict(x=0), dict(x=ptr() + 1), dict(ld=63), dict(dtype=7), dict(rows=-1), dict(rows=1 << 31), dict(cols=0),
+                dict(cols=(1 << 20) + 1), dict(out=None), dict(out=act8(codes=0)), dict(out=act8(scales=0)),
+                dict(out=act8(ld_codes=63)), dict(out=act8(ld_scales=1)), dict(ld=1 << 60)):
+        assert pack(**bad) == EINVAL, bad
+    for bad in (dict(src=None), dict(src=act8(ld_codes=5)), dict(out=0), dict(ld=7), dict(dtype=-1), dict(cols=-3)):
+        assert unpack(**bad) == EINVAL, bad
+    p = ptr()
+    assert pack(x=p, out=act8(codes=p + 64)) == EALIAS
+    assert pack(out=act8(codes=p, scales=p + 3)) == EALIAS
+    assert unpack(src=act8(codes=p), out=p + 512 - 64) == EALIAS
+    # no rows: nothing is read, nothing launched
+    assert pack(x=0, rows=0, out=act8(codes=0, scales=0)) == 0 and unpack(rows=0, out=0) == 0
+
+
+def test_norm_refuses(lib):
+    def call(**kw):
+        return lib.muon_rmsnorm_act8(ctypes.byref(norm(**kw)), None)
+
+    assert lib.muon_rmsnorm_act8(None, None) == EINVAL
+    for bad in (dict(x=0), dict(dtype=3), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(cols=16385),
+                dict(cols=0), dict(ld_x=63), dict(ld_residual=0), dict(ld_h=1), dict(ld_y=1), dict(gain=ptr() + 2),
+                dict(rstd=ptr() + 1), dict(n=act8(scales=0)), dict(n=act8(ld_codes=3)), dict(rows=-1), dict(y=ptr() + 1)):
+        assert call(**bad) == EINVAL, bad
+    p = ptr()
+    assert call(x=p, y=p) == EALIAS and call(h=p, y=p + 2) == EALIAS and call(gain=p, rstd=p + 64) == EALIAS
+    assert call(rows=0, x=0) == 0
+
+
+def test_norm_gradient_refuses(lib):
+    need = lib.muon_rmsnorm_act8_grad_workspace_bytes(4000, 64)
+    assert need > 0 and lib.muon_rmsnorm_act8_grad_workspace_bytes(1, 64) == 0
+    assert lib.muon_rmsnorm_act8_grad_workspace_bytes(10, 1 << 15) == 0 and lib.muon_rmsnorm_act8_grad_workspace_bytes(-1, 8) == 0
+
+    def call(ws=WS, ws_bytes=need, **kw):
+        return lib.muon_rmsnorm_act8_grad(ctypes.byref(norm_grad(**kw)), ws, ws_bytes, None)
+
+    for bad in (dict(dy=0), dict(n=act8(codes=0)), dict(rstd=0), dict(dx=0), dict(reserved=1), dict(dtype=2), dict(ld_dx=9),
+                dict(cols=1 << 15), dict(ld_dres=3)):
+        assert call(**bad) == EINVAL, bad
+    assert call(ws=None) == EWORKSPACE and call(ws_bytes=need - 1) == EWORKSPACE
+    assert call(ws=ctypes.c_void_p((1 << 42) + 8)) == EWORKSPACE
+    p = ptr()
+    assert call(dy=p, dx=p) == EALIAS and call(dgain=1 << 42) == EALIAS
+
+
+def test_gate_refuses_and_takes_halves_of_one_buffer(lib):
+    def fwd(**kw):
+        return lib.muon_swiglu_act8(ctypes.byref(gate(**kw)), None)
+
+    def bwd(**kw):
+        return lib.muon_swiglu_act8_grad(ctypes.byref(gate_grad(**kw)), None)
+
+    for bad in (dict(gate=0), dict(up=0), dict(gate8=act8(codes=0)), dict(reserved=1), dict(dtype=9), dict(ld_a=1)):
+        assert fwd(**bad) == EINVAL, bad
+    for bad in (dict(da=0), dict(dup=0), dict(dgate=0), dict(gate8=act8(codes=0)), dict(up8=act8(scales=0)), dict(reserved=2)):
+        assert bwd(**bad) == EINVAL, bad
+    p = ptr()
+    # column slices that touch overlap nothing; shifted by one element they do
+    assert bwd(dgate=p, dup=p + 126, ld_dgate=128, ld_dup=128) == EALIAS
+    assert bwd(dgate=p + 126, dup=p, ld_dgate=128, ld_dup=128) == EALIAS
+    assert bwd(dgate=p, dup=p + 130, ld_dgate=128, ld_dup=128) == EALIAS      # runs into the next row
+    assert bwd(rows=1, dgate=p, dup=p + 100) == EALIAS
+    assert fwd(rows=0) == 0 and bwd(rows=0) == 0
+
+
+def test_wgrad_refuses(lib):
+    def call(ws=WS, ws_bytes=1 << 40, **kw):
+        return lib.muon_act8_wgrad(ctypes.byref(wgrad(**kw)), ws, ws_bytes, None)
+
+    for bad in (dict(dy=0), dict(dw=0), dict(x8=act8(codes=0)), dict(n=0), dict(k=0), dict(tokens=-1), dict(n=(1 << 20) + 1),
+                dict(dw_dtype=4), dict(accumulate=2), dict(ld_dy=63), dict(ld_dw=63), dict(dy=ptr() + 1), dict(dw=ptr() + 2)):
+        assert call(**bad) == EINVAL, bad
+    op = wgrad()
+    need = lib.muon_act8_wgrad_workspace_bytes(ctypes.byref(op))
+    assert need > 0 and lib.muon_act8_wgrad_workspace_bytes(ctypes.byref(wgrad(n=0))) == 0
+    assert call(ws_bytes=need - 1) == EWORKSPACE and call(ws=None) == EWORKSPACE
+    assert call(ws=ctypes.c_void_p((1 << 42) + 4)) == EWORKSPACE
+    p = ptr()
+    assert call(dy=p, dw=p) == EALIAS and call(dw=1 << 42) == EALIAS and call(dw=p, col_gain=p) == EALIAS
+    assert call(tokens=0, accumulate=1) == 0                          # nothing to add
+
+
+def test_embed_refuses(lib):
+    def fwd(**kw):
+        return lib.muon_embed(ctypes.byref(embed(**kw)), None)
+
+    def bwd(ws=WS, ws_bytes=1 << 40, **kw):
+        return lib.muon_embed_grad(ctypes.byref(embed_grad(**kw)), ws, ws_bytes, None)
+
+    for bad in (dict(table=0), dict(ids=0), dict(out=0), dict(vocab=0), dict(vocab=(1 << 31) - 1), dict(tokens=-1), dict(cols=0),
+                dict(scale=float("nan")), dict(id_bytes=2), dict(out_dtype=5), dict(table_dtype=-1), dict(ids=ptr() + 4)):
+        assert fwd(**bad) == EINVAL, bad
+    for bad in (dict(dy=0), dict(ids=0), dict(dtable=0), dict(vocab=0), dict(reserved=1), dict(accumulate=-1), dict(id_bytes=1),
+                dict(scale=float("inf")), dict(ld_dtable=63)):
+        assert bwd(**bad) == EINVAL, bad
+    need = lib.muon_embed_grad_workspace_bytes(900, 100, 64)
+    assert need > 0 and lib.muon_embed_grad_workspace_bytes(900, 0, 64) == 0
+    assert bwd(ws_bytes=need - 1) == EWORKSPACE and bwd(ws=None) == EWORKSPACE
+    p = ptr()
+    assert fwd(table=p, out=p) == EALIAS and bwd(dy=p, dtable=p) == EALIAS and bwd(dtable=1 << 42) == EALIAS
+    assert fwd(tokens=0, ids=0, out=0) == 0 and bwd(tokens=0, accumulate=1) == 0
+
+
+def test_workspaces_grow_with_the_work(lib):
+    rng = random.Random(5)
+    for _ in range(200):
+        t, v, c = rng.randint(0, 1 << 20), rng.randint(1, 1 << 20), rng.randint(1, 1 << 14)
+        a = lib.muon_embed_grad_workspace_bytes(t, v, c)
+        assert a >= 16 * t                                            # keys and tokens, twice
+        assert lib.muon_rmsnorm_act8_grad_workspace_bytes(t, c) % (4 * c) == 0
+
+
+def test_binding_refuses_cpu_tensors(lib):
+    x, v = torch.zeros(4, 64), torch.zeros(4, dtype=torch.int64)
+    x8 = muon.Act8(x.to(torch.float8_e4m3fn), torch.zeros(4, 2, dtype=torch.uint8))
+    for call in (lambda: muon.act8_pack(x), lambda: muon.act8_unpack(x8), lambda: muon.rmsnorm_act8(x),
+                 lambda: muon.rmsnorm_act8_grad(x, x8, x[:, 0]), lambda: muon.swiglu_act8(x, x),
+                 lambda: muon.swiglu_act8_grad(x, x8, x8), lambda: muon.act8_wgrad(x.bfloat16(), x8),
+                 lambda: muon.embed(x, v), lambda: muon.embed_grad(x, v, 9)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    with pytest.raises(AttributeError):
+        muon.no_such_operator
