@@ -1,10 +1,23 @@
 // Embedding lookup and its gradient (gfx950).
 //
-// The gradient adds the rows of dy by id without atomics: the tokens are sorted
-// by id with a stable radix sort (8-bit digits, least significant first), so
-// each row of the table finds its tokens side by side and in their own order,
-// and its sum does not depend on scheduling.  Tokens whose id is outside the
-// table take the key `vocab` and end up past every row.
+// The gradient adds the rows of dy by id without atomics, so that its sums do
+// not depend on scheduling.  The tokens are sorted by id with a stable radix
+// sort (9-bit digits, least significant first: two passes up to 262143 rows),
+// which puts each row's tokens side by side and in their own order; k_starts
+// then notes where each row's begin.  Tokens whose id is outside the table take
+// the key `vocab` and end up past every row.
+//
+// Ids are as frequent as words: a few have thousands of tokens, most none.
+//   Rows of up to kRun tokens (and empty ones, which are written as zeros) go to
+//   k_rows, a wave or a block per 4 rows.
+//   Longer runs are cut where the sorted order passes a multiple of kRun:
+//   k_pieces sums each piece into the workspace, k_join adds a run's pieces in
+//   order.  A piece lies in one chunk of kRun places; a chunk can hold two of
+//   them, the end of one run and the beginning of another.
+// Up to kDirect tokens none of that is needed: each wave of k_rows finds its
+// rows' tokens by comparing all ids.
+//
+// Bound by memory: dy is read once, the table's gradient written once.
 #include <algorithm>
 
 #include "muon_act8.h"
@@ -14,12 +27,14 @@ namespace muon {
 
 namespace {
 
-constexpr int kDigits = 256;
-constexpr int kSortThreads = 1024;
+constexpr int kDigitBits = 9;
+constexpr int kDigits = 1 << kDigitBits;
+constexpr int kSortThreads = 1024;                  // tokens of a block per step
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kPerWave = 256;                       // tokens of a wave per step
-constexpr int kStep = kSortWaves * kPerWave;        // tokens of a block per step
 constexpr int kRowThreads = 256;
+constexpr int kRun = 64;                            // longest run that one wave adds up
+constexpr int kDirect = 256;                        // tokens that are not sorted
+constexpr int kRowsEach = 4;                        // rows of a wave (or block) of k_rows
 
 __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_t i) {
   return id_bytes == 8 ? gld<int64_t>(static_cast<const char*>(ids) + 8 * i)
@@ -67,10 +82,12 @@ struct SortArgs {
   uint32_t* count;            // [block][digit]
 };
 
-__device__ __forceinline__ uint32_t key_of(const SortArgs& a, int64_t i) {
-  if (a.keys_in) return gld<uint32_t>(a.keys_in + i);
-  const int64_t id = load_id(a.ids, a.id_bytes, i);
-  return static_cast<uint32_t>(id >= 0 && id < a.vocab ? id : a.vocab);
+__device__ __forceinline__ uint32_t key_of(const void* ids, int id_bytes, int64_t vocab, int64_t i) {
+  const int64_t id = load_id(ids, id_bytes, i);
+  return static_cast<uint32_t>(id >= 0 && id < vocab ? id : vocab);
+}
+__device__ __forceinline__ uint32_t key_in(const SortArgs& a, int64_t i) {
+  return a.keys_in ? gld<uint32_t>(a.keys_in + i) : key_of(a.ids, a.id_bytes, a.vocab, i);
 }
 
 // Tokens of each digit in each block's share.
@@ -79,9 +96,9 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_count(SortArgs a) {
   if (threadIdx.x < kDigits) hist[threadIdx.x] = 0;
   __syncthreads();
   const int64_t begin = blockIdx.x * a.block_tokens;
-  const int64_t end = begin + a.block_tokens < a.tokens ? begin + a.block_tokens : a.tokens;
+  const int64_t end = min(begin + a.block_tokens, a.tokens);
   for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads)
-    atomicAdd(&hist[(key_of(a, i) >> a.shift) & (kDigits - 1)], 1u);
+    atomicAdd(&hist[(key_in(a, i) >> a.shift) & (kDigits - 1)], 1u);
   __syncthreads();
   if (threadIdx.x < kDigits) gst<uint32_t>(a.count + blockIdx.x * kDigits + threadIdx.x, hist[threadIdx.x]);
 }
@@ -91,57 +108,65 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_count(SortArgs a) {
 // lanes with one digit find each other by a ballot per digit bit.
 __global__ __launch_bounds__(kSortThreads) void k_embed_scatter(SortArgs a) {
   __shared__ uint32_t base[kDigits];                // next place of each digit
-  __shared__ uint32_t part[kDigits];
-  __shared__ uint32_t wcnt[kSortWaves][kDigits];
+  __shared__ uint32_t wcnt[kSortWaves][kDigits];    // a step's tokens by wave, then their places
+  __shared__ uint32_t half[2][kDigits], wsum[kSortWaves];
   const int t = static_cast<int>(threadIdx.x), lane = t & 63, w = t >> 6;
-  uint32_t before = 0, total = 0;
-  if (t < kDigits) {
-    for (unsigned b = 0; b < gridDim.x; ++b) {
-      const uint32_t n = gld<uint32_t>(a.count + b * kDigits + t);
-      if (b < blockIdx.x) before += n;
+  // tokens of digit d in the blocks before this one, and in all: two halves of
+  // the threads take every other block
+  {
+    const int d = t & (kDigits - 1), h = t / kDigits;
+    uint32_t before = 0, total = 0;
+#pragma unroll 4
+    for (unsigned b = h; b < gridDim.x; b += 2) {
+      const uint32_t n = gld<uint32_t>(a.count + b * kDigits + d);
+      before += b < blockIdx.x ? n : 0u;
       total += n;
     }
-    part[t] = total;
-  }
-  __syncthreads();
-  for (int o = 1; o < kDigits; o <<= 1) {           // inclusive scan over the digits
-    uint32_t v = 0;
-    if (t < kDigits && t >= o) v = part[t - o];
+    half[h][d] = total;
+    if (h == 1) base[d] = before;
     __syncthreads();
-    if (t < kDigits) part[t] += v;
+    uint32_t sum = 0;
+    if (t < kDigits) {
+      sum = half[0][t] + half[1][t];
+      before += base[t];
+    }
+    // exclusive scan of the totals over the digits
+    uint32_t scan = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t v = __shfl_up(scan, o, 64);
+      scan += lane >= o ? v : 0u;
+    }
+    if (lane == 63) wsum[w] = scan;
     __syncthreads();
+    if (t < kDigits) {
+      uint32_t first = scan - sum;
+      for (int k = 0; k < w; ++k) first += wsum[k];
+      base[t] = first + before;
+    }
   }
-  if (t < kDigits) base[t] = part[t] - total + before;
   const int64_t begin = blockIdx.x * a.block_tokens;
-  const int64_t end = begin + a.block_tokens < a.tokens ? begin + a.block_tokens : a.tokens;
-  for (int64_t at = begin; at < end; at += kStep) {
+  const int64_t end = min(begin + a.block_tokens, a.tokens);
+  for (int64_t at = begin; at < end; at += kSortThreads) {
+#pragma unroll
     for (int i = t; i < kSortWaves * kDigits; i += kSortThreads) (&wcnt[0][0])[i] = 0;
     __syncthreads();
-    uint32_t key[kPerWave / 64], tok[kPerWave / 64], rank[kPerWave / 64];
-#pragma unroll
-    for (int r = 0; r < kPerWave / 64; ++r) {
-      const int64_t i = at + w * kPerWave + r * 64 + lane;
-      key[r] = i < end ? key_of(a, i) : 0u;
-      tok[r] = i < end ? (a.toks_in ? gld<uint32_t>(a.toks_in + i) : static_cast<uint32_t>(i)) : 0u;
+    const int64_t i = at + t;
+    const bool valid = i < end;
+    uint32_t key = 0, tok = 0;
+    if (valid) {
+      key = key_in(a, i);
+      tok = a.toks_in ? gld<uint32_t>(a.toks_in + i) : static_cast<uint32_t>(i);
     }
+    const uint32_t d = (key >> a.shift) & (kDigits - 1);
+    uint64_t same = __ballot(valid);
 #pragma unroll
-    for (int r = 0; r < kPerWave / 64; ++r) {
-      const bool valid = at + w * kPerWave + r * 64 + lane < end;
-      const uint32_t d = (key[r] >> a.shift) & (kDigits - 1);
-      uint64_t same = __ballot(valid);
-#pragma unroll
-      for (int bit = 0; bit < 8; ++bit) {
-        const uint64_t on = __ballot((d >> bit) & 1);
-        same &= (d >> bit) & 1 ? on : ~on;
-      }
-      const uint32_t seen = wcnt[w][d];
-      rank[r] = seen + __popcll(same & ((uint64_t(1) << lane) - 1));
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      if (valid && (same >> lane) == 1) wcnt[w][d] = rank[r] + 1;   // the digit's last lane
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+    for (int bit = 0; bit < kDigitBits; ++bit) {
+      const uint64_t on = __ballot((d >> bit) & 1);
+      same &= (d >> bit) & 1 ? on : ~on;
     }
+    const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    if (valid && (same >> lane) == 1) wcnt[w][d] = rank + 1;   // the digit's last lane
     __syncthreads();
     if (t < kDigits) {
       uint32_t run = base[t];
@@ -154,61 +179,216 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_scatter(SortArgs a) {
       base[t] = run;
     }
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kPerWave / 64; ++r) {
-      if (at + w * kPerWave + r * 64 + lane < end) {
-        const uint32_t p = wcnt[w][(key[r] >> a.shift) & (kDigits - 1)] + rank[r];
-        gst<uint32_t>(a.keys_out + p, key[r]);
-        gst<uint32_t>(a.toks_out + p, tok[r]);
-      }
+    if (valid) {
+      const uint32_t p = wcnt[w][d] + rank;
+      gst<uint32_t>(a.keys_out + p, key);
+      gst<uint32_t>(a.toks_out + p, tok);
     }
     __syncthreads();
   }
 }
 
-// -------------------------------------------------------------------- rows ----
-// First place whose key is >= v, by a whole wave: 64 probes a step.  (c probes
-// below v: the place is past the c-th and at most at the next one.)
-__device__ __forceinline__ uint32_t lower_bound(const uint32_t* keys, uint32_t n, uint32_t v, int lane) {
-  uint32_t lo = 0, hi = n;
+// start[v] = first place whose key is >= v, for v = 0 .. vocab.
+__global__ __launch_bounds__(kRowThreads) void k_starts(const uint32_t* keys, uint32_t tokens, uint32_t vocab, uint32_t* start) {
+  const uint32_t v = blockIdx.x * kRowThreads + threadIdx.x;
+  if (v > vocab) return;
+  uint32_t lo = 0, hi = tokens;
   while (lo < hi) {
-    const uint32_t step = (hi - lo + 63) >> 6;
-    const uint32_t p = lo + (lane + 1) * step - 1;
-    bool less = false;
-    if (p < hi) less = gld<uint32_t>(keys + p) < v;
-    lo += static_cast<uint32_t>(__popcll(__ballot(less))) * step;
-    hi = min(hi, lo + step - 1);
+    const uint32_t mid = (lo + hi) >> 1;
+    if (gld<uint32_t>(keys + mid) < v) lo = mid + 1;
+    else hi = mid;
   }
-  return lo;
+  gst<uint32_t>(start + v, lo);
 }
 
-// One wave per row of the table.
-template <class S, class T>
-__global__ __launch_bounds__(kRowThreads) void k_embed_rows(muon_embed_grad_t op, const uint32_t* keys, const uint32_t* toks) {
+// ------------------------------------------------------------------ sums ----
+// s += dy[token] for the tokens held by lanes first .. first + n - 1 of the wave
+// (all lanes active), in order; this thread's columns c .. c + 7.
+template <class S>
+__device__ __forceinline__ void add_rows(const muon_embed_grad_t& op, uint32_t held, int first, int n, int c, float (&s)[8]) {
+  const int valid = static_cast<int>(op.cols) - c;
+  const S* dy = static_cast<const S*>(op.dy) + c;
+  auto row = [&](int i) { return dy + static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(held, i))) * op.ld_dy; };
+  int i = first;
+  const int end = first + n;
+  for (; i + 8 <= end; i += 8) {
+    Vec8<S> v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) load8(v[k], row(i + k), valid);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += v[k].get(j);
+  }
+  for (; i + 2 <= end; i += 2) {
+    Vec8<S> v[2];
+    load8(v[0], row(i), valid);
+    load8(v[1], row(i + 1), valid);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = s[j] + v[0].get(j) + v[1].get(j);
+  }
+  if (i < end) {
+    Vec8<S> v;
+    load8(v, row(i), valid);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += v.get(j);
+  }
+}
+
+// dtable[row] (+)= scale s, columns c .. c + 7.
+template <class T>
+__device__ __forceinline__ void put_row(const muon_embed_grad_t& op, int64_t row, int c, float (&s)[8]) {
+  const int n = static_cast<int>(op.cols) - c;
+  T* out = static_cast<T*>(op.dtable) + row * op.ld_dtable + c;
+  Vec8<T> old;
+  if (op.accumulate) load8(old, out, n);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = op.accumulate ? fmaf(op.scale, s[j], old.get(j)) : op.scale * s[j];
+  Vec8<T>::store(out, n, s);
+}
+
+// kRowsEach rows for each group of TPR threads (a wave, or the block).
+template <class S, class T, int TPR, bool DIRECT>
+__global__ __launch_bounds__(kRowThreads) void k_rows(muon_embed_grad_t op, const uint32_t* start, const uint32_t* toks) {
+  const int lane = threadIdx.x & 63;
+  // uniform over a wave: taken from its first lane
+  const int group = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / TPR);
+  const int t = static_cast<int>(threadIdx.x) % TPR;
+  const int cols = static_cast<int>(op.cols);
+  for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kRowThreads / TPR) + group) * kRowsEach; row0 < op.vocab;
+       row0 += static_cast<int64_t>(gridDim.x) * (kRowThreads / TPR) * kRowsEach) {
+    if constexpr (DIRECT) {
+      uint32_t key[kDirect / 64];
+#pragma unroll
+      for (int q = 0; q < kDirect / 64; ++q) {
+        const int64_t i = q * 64 + lane;
+        key[q] = i < op.tokens ? key_of(op.ids, op.id_bytes, op.vocab, i) : 0xffffffffu;
+      }
+      for (int r = 0; r < kRowsEach && row0 + r < op.vocab; ++r)
+        for (int c0 = 0; c0 < cols; c0 += TPR * 8) {
+          const int c = c0 + t * 8;
+          float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < kDirect / 64; ++q)
+            for (uint64_t m = __ballot(key[q] == static_cast<uint32_t>(row0 + r)); m; m &= m - 1) {
+              Vec8<S> v;
+              load8(v, static_cast<const S*>(op.dy) + (q * 64 + __builtin_ctzll(m)) * op.ld_dy + c, cols - c);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) s[j] += v.get(j);
+            }
+          put_row<T>(op, row0 + r, c, s);
+        }
+    } else {
+      uint32_t first[kRowsEach], held[kRowsEach];
+      int len[kRowsEach];
+#pragma unroll
+      for (int r = 0; r < kRowsEach; ++r) {
+        const bool in = row0 + r < op.vocab;
+        first[r] = in ? gld<uint32_t>(start + row0 + r) : 0u;
+        len[r] = in ? static_cast<int>(gld<uint32_t>(start + row0 + r + 1) - first[r]) : kRun + 1;
+      }
+#pragma unroll
+      for (int r = 0; r < kRowsEach; ++r)
+        held[r] = len[r] <= kRun && lane < len[r] ? gld<uint32_t>(toks + first[r] + lane) : 0u;
+#pragma unroll
+      for (int r = 0; r < kRowsEach; ++r) {
+        if (len[r] > kRun) continue;                // k_join's, or past the table
+        for (int c0 = 0; c0 < cols; c0 += TPR * 8) {
+          float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          add_rows<S>(op, held[r], 0, len[r], c0 + t * 8, s);
+          put_row<T>(op, row0 + r, c0 + t * 8, s);
+        }
+      }
+    }
+  }
+}
+
+// The long runs that touch chunk `chunk` of the sorted order, one place per
+// lane: `left`, lanes of a run that began in an earlier chunk, and `right`, lanes
+// of one that begins here (it goes on in the next chunk).
+struct Chunk {
+  uint64_t left, right;
+  uint32_t key, begin, end;     // of this lane's run
+};
+__device__ __forceinline__ Chunk chunk_runs(const uint32_t* keys, const uint32_t* start, int64_t tokens, int64_t vocab,
+                                            int64_t chunk, int lane) {
+  const int64_t i = chunk * kRun + lane;
+  Chunk c;
+  c.key = i < tokens ? gld<uint32_t>(keys + i) : static_cast<uint32_t>(vocab);
+  c.begin = c.end = 0;
+  if (c.key < vocab) {
+    c.begin = gld<uint32_t>(start + c.key);
+    c.end = gld<uint32_t>(start + c.key + 1);
+  }
+  const bool is_long = c.end - c.begin > kRun;
+  c.left = __ballot(is_long && c.begin < chunk * kRun);
+  c.right = __ballot(is_long && c.begin >= chunk * kRun);
+  return c;
+}
+
+// Sums of the pieces of each chunk, columns of a wave: 512 from
+// (4 blockIdx.y + wave) * 512.  pieces: [chunk][left, right][cols].
+template <class S>
+__global__ __launch_bounds__(kRowThreads) void k_pieces(muon_embed_grad_t op, int64_t chunks, const uint32_t* keys,
+                                                        const uint32_t* toks, const uint32_t* start, float* pieces) {
   const int lane = threadIdx.x & 63;
   const int cols = static_cast<int>(op.cols);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); row < op.vocab;
-       row += static_cast<int64_t>(gridDim.x) * 4) {
-    const uint32_t v = static_cast<uint32_t>(row);
-    const uint32_t first = lower_bound(keys, static_cast<uint32_t>(op.tokens), v, lane);
-    for (int c = lane * 8; c < cols; c += 512) {
-      const int n = cols - c;
-      float s[8];
+  const int c = (static_cast<int>(blockIdx.y) * 4 + (threadIdx.x >> 6)) * 512 + lane * 8;
+  if (c - lane * 8 >= cols) return;
+  for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    const Chunk r = chunk_runs(keys, start, op.tokens, op.vocab, chunk, lane);
+    if (!(r.left | r.right)) continue;
+    const int64_t i = chunk * kRun + lane;
+    const uint32_t held = i < op.tokens ? gld<uint32_t>(toks + i) : 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = 0.f;
-      for (int64_t i = first; i < op.tokens && gld<uint32_t>(keys + i) == v; ++i) {
-        Vec8<S> raw;
-        load8(raw, static_cast<const S*>(op.dy) + static_cast<int64_t>(gld<uint32_t>(toks + i)) * op.ld_dy + c, n);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[k] += raw.get(k);
-      }
-      T* out = static_cast<T*>(op.dtable) + row * op.ld_dtable + c;
-      Vec8<T> old;
-      if (op.accumulate) load8(old, out, n);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = op.accumulate ? fmaf(op.scale, s[i], old.get(i)) : op.scale * s[i];
-      Vec8<T>::store(out, n, s);
+    for (int side = 0; side < 2; ++side) {
+      const uint64_t m = side ? r.right : r.left;
+      if (!m) continue;
+      float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      add_rows<S>(op, held, __builtin_ctzll(m), __popcll(m), c, s);
+      Vec8<float>::store(pieces + (chunk * 2 + side) * cols + c, cols - c, s);
     }
+  }
+}
+
+// The run that begins in a chunk: its pieces, 512 columns from 512 blockIdx.y.
+// The waves take consecutive shares of them, which are added in order.
+constexpr int kJoinWaves = 16;
+template <class T>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, int64_t chunks, const uint32_t* keys,
+                                                          const uint32_t* start, const float* pieces) {
+  __shared__ float red[kJoinWaves][512];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int cols = static_cast<int>(op.cols);
+  const int c = static_cast<int>(blockIdx.y) * 512 + lane * 8;
+  for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    const Chunk r = chunk_runs(keys, start, op.tokens, op.vocab, chunk, lane);
+    if (!r.right) continue;                          // the whole block
+    const int src = __builtin_ctzll(r.right);
+    const int64_t row = static_cast<uint32_t>(__builtin_amdgcn_readlane(r.key, src));
+    const int64_t last = (static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(r.end, src))) - 1) / kRun;
+    const int n = static_cast<int>(last - chunk + 1), per = (n + kJoinWaves - 1) / kJoinWaves;
+    const int end = min((w + 1) * per, n);
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = w * per; k < end; ++k) {
+      Vec8<float> v;
+      load8(v, pieces + ((chunk + k) * 2 + (k == 0)) * cols + c, cols - c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += v.get(j);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[w][j * 64 + lane] = s[j];
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[j] = 0.f;
+        for (int k = 0; k < kJoinWaves; ++k) s[j] += red[k][j * 64 + lane];
+      }
+      put_row<T>(op, row, c, s);
+    }
+    __syncthreads();                                 // before red is used again
   }
 }
 
@@ -223,7 +403,7 @@ SortArgs sort_args(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass
   a.tokens = op.tokens;
   a.vocab = op.vocab;
   a.block_tokens = p.block_tokens;
-  a.shift = 8 * pass;
+  a.shift = kDigitBits * pass;
   const int in = (pass + 1) & 1, out = pass & 1;
   a.keys_in = pass ? reinterpret_cast<const uint32_t*>(ws + p.keys_off[in]) : nullptr;
   a.toks_in = pass ? reinterpret_cast<const uint32_t*>(ws + p.toks_off[in]) : nullptr;
@@ -243,23 +423,27 @@ int by_types(int32_t in, int32_t out, F&& f) {
 }  // namespace
 
 EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols) {
-  EmbedSortPlan p;
-  p.passes = 0;
-  for (int64_t top = vocab; top > 0; top >>= 8) ++p.passes;
+  EmbedSortPlan p{};
+  if (tokens <= kDirect) return p;
+  for (int64_t top = vocab; top > 0; top >>= kDigitBits) ++p.passes;
   // at most 256 blocks, whole steps each
-  p.block_tokens = kStep * std::max<int64_t>(1, (tokens + kStep * 256 - 1) / (kStep * 256));
+  p.block_tokens = kSortThreads * ((tokens + kSortThreads * 256 - 1) / (kSortThreads * 256));
   p.blocks = (tokens + p.block_tokens - 1) / p.block_tokens;
+  p.chunks = (tokens + kRun - 1) / kRun;
   size_t off = 0;
+  auto take = [&](int64_t n) {
+    const size_t at = off;
+    off = up256(off + static_cast<size_t>(n) * 4);
+    return at;
+  };
   for (int k = 0; k < 2; ++k) {
-    p.keys_off[k] = off;
-    off = up256(off + static_cast<size_t>(tokens) * 4);
-    p.toks_off[k] = off;
-    off = up256(off + static_cast<size_t>(tokens) * 4);
+    p.keys_off[k] = take(tokens);
+    p.toks_off[k] = take(tokens);
   }
-  p.count_off = off;
-  off = up256(off + static_cast<size_t>(p.blocks) * kDigits * 4);
+  p.count_off = take(p.blocks * kDigits);
+  p.start_off = take(vocab + 1);
+  p.pieces_off = take(p.chunks * 2 * cols);
   p.bytes = off;
-  (void)cols;
   return p;
 }
 
@@ -284,14 +468,44 @@ int launch_embed_scatter(const muon_embed_grad_t& op, const EmbedSortPlan& p, in
   return static_cast<int>(hipGetLastError());
 }
 
+int launch_embed_starts(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
+  hipLaunchKernelGGL(k_starts, dim3(static_cast<unsigned>((op.vocab + kRowThreads) / kRowThreads)), dim3(kRowThreads), 0,
+                     static_cast<hipStream_t>(stream), p.keys(ws), static_cast<uint32_t>(op.tokens),
+                     static_cast<uint32_t>(op.vocab), p.starts(ws));
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_embed_pieces(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
+  const dim3 grid(static_cast<unsigned>(std::min(p.chunks, kMaxGrid)), static_cast<unsigned>((op.cols + 2047) / 2048));
+  return by_types(op.dy_dtype, op.table_dtype, [&](auto s, auto) {
+    hipLaunchKernelGGL((k_pieces<decltype(s)>), grid, dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), op,
+                       p.chunks, p.keys(ws), p.toks(ws), p.starts(ws), p.pieces(ws));
+    return static_cast<int>(hipGetLastError());
+  });
+}
+
 int launch_embed_rows(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
-  const int last = (p.passes - 1) & 1;
-  const uint32_t* keys = reinterpret_cast<const uint32_t*>(ws + p.keys_off[last]);
-  const uint32_t* toks = reinterpret_cast<const uint32_t*>(ws + p.toks_off[last]);
-  const int64_t blocks = (op.vocab + 3) / 4;
+  const bool direct = op.tokens <= kDirect, wide = op.cols > 512;
+  const int64_t per_block = (wide ? 1 : 4) * kRowsEach, blocks = (op.vocab + per_block - 1) / per_block;
+  const dim3 grid(static_cast<unsigned>(std::min(blocks, kMaxGrid)));
   return by_types(op.dy_dtype, op.table_dtype, [&](auto s, auto t) {
-    hipLaunchKernelGGL((k_embed_rows<decltype(s), decltype(t)>), dim3(static_cast<unsigned>(std::min(blocks, kMaxGrid))),
-                       dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), op, keys, toks);
+    using S = decltype(s);
+    using T = decltype(t);
+    auto go = [&](auto k) {
+      hipLaunchKernelGGL(k, grid, dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), op,
+                         direct ? nullptr : p.starts(ws), direct ? nullptr : p.toks(ws));
+      return static_cast<int>(hipGetLastError());
+    };
+    if (direct) return wide ? go(k_rows<S, T, 256, true>) : go(k_rows<S, T, 64, true>);
+    return wide ? go(k_rows<S, T, 256, false>) : go(k_rows<S, T, 64, false>);
+  });
+}
+
+int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
+  const dim3 grid(static_cast<unsigned>(std::min(p.chunks, kMaxGrid / 4)), static_cast<unsigned>((op.cols + 511) / 512));
+  return by_types(op.dy_dtype, op.table_dtype, [&](auto, auto t) {
+    hipLaunchKernelGGL((k_join<decltype(t)>), grid, dim3(64 * kJoinWaves), 0, static_cast<hipStream_t>(stream), op,
+                       p.chunks, p.keys(ws), p.starts(ws), p.pieces(ws));
     return static_cast<int>(hipGetLastError());
   });
 }

@@ -42,17 +42,29 @@ int launch_wgrad(const muon_act8_wgrad_t& op, const WgradPlan& p, void* workspac
 int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const void* workspace, void* stream);
 
 // muon_embed.hip
+// Workspace of the gradient (nothing for few tokens, which are not sorted):
+// keys and tokens before and after a pass, each block's digit counts, each
+// row's first place, the sums of the long runs' pieces.
 struct EmbedSortPlan {
-  int passes;                 // 8-bit digits of the keys 0 .. vocab
+  int passes;                 // digits of the keys 0 .. vocab
   int64_t blocks;             // blocks of a pass, block_tokens tokens each
   int64_t block_tokens;
-  size_t keys_off[2], toks_off[2], count_off;
+  int64_t chunks;             // pieces of long runs lie in one chunk
+  size_t keys_off[2], toks_off[2], count_off, start_off, pieces_off;
   size_t bytes;
+  // after the last pass
+  uint32_t* keys(char* ws) const { return reinterpret_cast<uint32_t*>(ws + keys_off[(passes - 1) & 1]); }
+  uint32_t* toks(char* ws) const { return reinterpret_cast<uint32_t*>(ws + toks_off[(passes - 1) & 1]); }
+  uint32_t* starts(char* ws) const { return reinterpret_cast<uint32_t*>(ws + start_off); }
+  float* pieces(char* ws) const { return reinterpret_cast<float*>(ws + pieces_off); }
 };
 EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols);
 int launch_embed(const muon_embed_t& op, void* stream);
 int launch_embed_count(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream);
 int launch_embed_scatter(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream);
+int launch_embed_starts(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
+int launch_embed_pieces(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
 int launch_embed_rows(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
+int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
 
 }  // namespace muon
