@@ -261,10 +261,14 @@ int muon_act8_wgrad(const muon_act8_wgrad_t* op, void* workspace, size_t workspa
   Launcher l(stream);
   if (int rc = l.open()) return rc;
   if (int rc = l.poison(workspace, p.bytes)) return rc;
+  char* ws = static_cast<char*>(workspace);
+  muon_act8_wgrad_t in = *op;
+  if (p.copy_dy || p.copy_x)
+    if (int rc = l.run("weight gradient, aligned copies", [&](void* st) { return launch_wgrad_copy(in, p, ws, st); })) return rc;
   if (op->tokens > 0)
-    if (int rc = l.run("weight gradient", [&](void* st) { return launch_wgrad(*op, p, workspace, st); })) return rc;
+    if (int rc = l.run("weight gradient", [&](void* st) { return launch_wgrad(in, p, ws, st); })) return rc;
   if (p.splits != 1)
-    return l.run("weight gradient join", [&](void* st) { return launch_wgrad_join(*op, p, workspace, st); });
+    return l.run("weight gradient, join", [&](void* st) { return launch_wgrad_join(in, p, ws, st); });
   return MUON_OK;
 }
 

@@ -32,14 +32,20 @@ int launch_rmsnorm_grad(const muon_rmsnorm_grad_t& op, float* partial, void* str
 int launch_rmsnorm_dgain(const float* partial, int64_t blocks, int64_t cols, float* dgain, void* stream);
 
 // muon_wgrad.hip
+// Workspace: the token ranges' partial outputs where there are several, and
+// aligned copies of a dy or x8 that the kernel's loads cannot take as they are.
 struct WgradPlan {
+  int tile;                   // 256 or 128
   int64_t tiles_n, tiles_k;   // output tiles
   int64_t splits, split_rows; // token ranges of split_rows (the last one may be shorter)
-  size_t bytes;               // workspace: splits partial outputs where splits > 1
+  bool copy_dy, copy_x;
+  size_t partial_off, dy_off, x_off, s_off;
+  size_t bytes;
 };
 WgradPlan wgrad_plan(const muon_act8_wgrad_t& op);
-int launch_wgrad(const muon_act8_wgrad_t& op, const WgradPlan& p, void* workspace, void* stream);
-int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const void* workspace, void* stream);
+int launch_wgrad_copy(muon_act8_wgrad_t& op, const WgradPlan& p, char* ws, void* stream);   // op: now the copies
+int launch_wgrad(const muon_act8_wgrad_t& op, const WgradPlan& p, char* ws, void* stream);
+int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const char* ws, void* stream);
 
 // muon_embed.hip
 // Workspace of the gradient (nothing for few tokens, which are not sorted):

@@ -1,11 +1,25 @@
 // Weight gradient of a linear layer from its 8-bit input (gfx950):
-//   dW[i][j] = gain[j] sum_t dY[t][i] x[t][j].
+//   dW[i][j] = gain[j] sum_t dY[t][i] x[t][j],   x[t][j] = code[t][j] 2^e[t][j / 32].
 //
-// Both factors are summed over their rows, so both reach LDS as they lie in
-// memory, [token][column], and the matrix instruction's fragments are taken
-// from there by transposing reads (as in muon_gemm.h).  A value of x8 is a 4-bit
-// significand times a power of two: bf16 holds it exactly, so the products are
-// those of the bf16 matrix instruction and nothing is lost by unpacking.
+// Both factors are summed over their rows, so both lie in LDS as in memory,
+// [token][column], and the fragments of v_mfma_f32_16x16x32_bf16 are taken from
+// there by transposing reads (the MN-contiguous form of muon_gemm.h).  A value
+// of x8 is a 4-bit significand times a power of two: bf16 holds it exactly, so
+// unpacking loses nothing, and the products are exact in fp32.
+//
+// The scale changes with the token, which is the summed index, so it cannot
+// wait for the epilogue: x is unpacked between global memory and the matrix
+// instruction.  Once per block (and not once per wave that reads a fragment):
+// the codes and their scale bytes go straight into LDS; two steps later each
+// wave turns the 8 tokens that it loaded itself into bf16 (two values of one
+// group share an instruction) and writes them to a second LDS tile, from where
+// on both operands are alike.
+//
+// Bounds.  Every load goes through a buffer descriptor that ends where the
+// matrix ends: past it LDS receives zeros (whole dwords count, hence the
+// alignment rule below), so tokens past the end add nothing and no address
+// leaves the matrix.  Columns past a row's end read the next row and reach only
+// outputs that are not stored.
 #include <algorithm>
 
 #include "muon_act8.h"
@@ -16,126 +30,416 @@ namespace muon {
 
 namespace {
 
-constexpr int kTile = 128;
-using G = Geo<kTile>;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 
-// LDS place of the 16-byte chunk c of token row r (see muon_gemm.h).
-__device__ __forceinline__ int chunk_at(int r, int c) {
-  return r * kTile + ((c ^ (2 * (r & 3) + 8 * ((r >> 3) & 1))) << 3);
+// ---------------------------------------------------------------- loads ----
+// 16 bytes (or one byte, zero-extended to a dword) per lane from buffer `srd` at
+// voff + soff into LDS, at lds_dst + 16 (4) times the lane.  As dma16() of
+// muon_gemm.h: an asm statement with explicit waits, whose scalar operands are
+// formed by scalar instructions (tests/test_ops_isa.py checks the compiled code).
+template <bool BYTE>
+__device__ __forceinline__ void dma_bounded(u32x4 srd, uint32_t voff, uint32_t soff, const void* lds_dst) {
+  const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (__attribute__((addrescdspace(3))) void*)lds_dst));
+  if constexpr (BYTE)
+    asm volatile("buffer_load_ubyte %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(m0));
+  else
+    asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(m0));
 }
 
+// A matrix of which a block reads the rows from row0 on, columns from byte col0:
+// step kt is its 32 rows from 32 kt.  The descriptor of a step ends where the
+// matrix ends (offsets within a step stay below 2^31: wgrad_plan).
+struct Feed {
+  const char* base;
+  int64_t bytes;     // from base to the matrix's end
+  int64_t kstep;
+  __device__ __forceinline__ Feed(const void* p, int64_t ld_bytes, int64_t rows, int64_t row_bytes, int64_t row0, int64_t col0) {
+    base = static_cast<const char*>(p) + row0 * ld_bytes + col0;
+    bytes = (rows - 1 - row0) * ld_bytes + row_bytes - col0;
+    kstep = BK * ld_bytes;
+  }
+  __device__ __forceinline__ u32x4 step(int kt) const {
+    const int64_t off = kt * kstep, left = bytes - off;
+    const uint64_t b = reinterpret_cast<uint64_t>(base + off);
+    u32x4 srd;
+    srd[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
+    srd[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32) & 0xffffu);
+    srd[2] = __builtin_amdgcn_readfirstlane(left < 0x7fffffff ? static_cast<uint32_t>(left) : 0x7fffffffu);
+    srd[3] = 0x00020000u;   // raw buffer of dwords
+    return srd;
+  }
+};
+
+template <int TILE>
+struct Lds {
+  static constexpr int TE = Geo<TILE>::TE;
+  static constexpr int RE = TILE * BK;                   // bytes of codes of a step
+  static constexpr int SE = 4 * 64 * 4;                  // a dword per wave and lane for the scales
+  static constexpr int P = 0;                            // dY: 4 stages of bf16
+  static constexpr int R = P + 4 * TE * 2;               // codes: 4 stages
+  static constexpr int S = R + 4 * RE;                   // scales: 4 stages
+  static constexpr int B = S + 4 * SE;                   // unpacked x: 2 stages of bf16
+  static constexpr int bytes = B + 2 * TE * 2;
+};
+static_assert(Lds<256>::bytes <= 160 * 1024 && 2 * Lds<128>::bytes <= 160 * 1024, "LDS per CU");
+
+// ------------------------------------------------------------ the product ----
+// acc += dY[t0 .., i0 .. i0 + TILE]^T x[t0 .., j0 .. j0 + TILE] over `steps`
+// steps of 32 tokens; 4 waves of TILE / 2 x TILE / 2, one MFMA per slot in the
+// order of muon_gemm.h, operands exchanged (a lane ends up with four consecutive
+// columns of one row).
+//
+// Step kt opens with a wait for this wave's loads of two steps before (dY of
+// step kt + 1, codes and scales of kt + 2 have landed) and a barrier, and then
+//   multiplies dY[kt] and x[kt], whose first fragments were read in step kt - 1,
+//   loads dY of step kt + 3 and codes and scales of step kt + 4,
+//   unpacks x of step kt + 2, into the tile whose fragments were read before the
+//   barrier.
+//
+// The wave's codes of a step are 8 token rows.  TILE 256: lane l unpacks the 32
+// columns of group l & 7 of row l >> 3, two pieces of 16; TILE 128: the 16 columns
+// from 16 (l & 7).  Which half of its columns a lane reads and writes first
+// depends on its row such that the 16 lanes that LDS serves at a time touch all
+// banks (a row is one or two sweeps of the banks).
+template <int TILE>
+__device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0, int64_t j0, int64_t t0, int steps,
+                                        char* smem, f32x4_t (&acc)[Geo<TILE>::NB][Geo<TILE>::NB], int tid) {
+  using G = Geo<TILE>;
+  using L = Lds<TILE>;
+  constexpr int NB = G::NB, H = NB / 2, PASS = H * NB, SLOTS = NB * NB;
+  constexpr int LP = G::LPW, LR = TILE / 128, LPS = LP + LR + 1;
+  constexpr int LSS = (SLOTS - H) / LPS;                 // loads spread over the step
+  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rowA = G::WT * (w >> 1), rowB = G::WT * (w & 1);
+
+  // rows end on a dword: in memory, or in the padding of an aligned copy
+  const Feed fp(op.dy, op.ld_dy * 2, op.tokens, (op.n * 2 + 3) / 4 * 4, t0, i0 * 2);
+  const Feed fr(op.x8.codes, op.x8.ld_codes, op.tokens, (op.k + 3) / 4 * 4, t0, j0);
+  const Feed fs(op.x8.scales, op.x8.ld_scales, op.tokens, (op.k + 31) / 32, t0, j0 / 32);
+  // dY: the MN-contiguous form of DmaFeed (muon_gemm.h)
+  constexpr int CPR = TILE / 8, RPB = 512 / TILE;        // chunks of a row, rows of a 1 KB load
+  uint32_t vp[2], vr, vs;
+#pragma unroll
+  for (int par = 0; par < 2; ++par) {
+    const int r = lane / CPR, c = (lane % CPR) ^ (2 * ((RPB * par + r) & 3) + 8 * (w & 1));
+    vp[par] = static_cast<uint32_t>(r * op.ld_dy * 2 + 16 * c);
+  }
+  constexpr int RCPR = TILE / 16, RRPB = 1024 / TILE;    // the same of the codes
+  vr = static_cast<uint32_t>((lane / RCPR) * op.x8.ld_codes + 16 * (lane % RCPR));
+  constexpr int SPR = TILE / 32;                         // scales of a row; lanes past 8 rows repeat
+  vs = static_cast<uint32_t>(((lane / SPR) & 7) * op.x8.ld_scales + lane % SPR);
+
+  // the shares of the wave in a step: dY parts 0 .. LP - 1, codes, scales
+  const uint32_t qp = static_cast<uint32_t>(RPB * op.ld_dy * 2), qr = static_cast<uint32_t>(RRPB * op.x8.ld_codes);
+  const uint32_t qs = static_cast<uint32_t>(8 * w * op.x8.ld_scales);
+  auto load_p = [&](u32x4 srd, int kt, int part) __attribute__((always_inline)) {
+    dma_bounded<false>(srd, vp[part & 1], (w * LP + part) * qp, smem + L::P + (kt & 3) * (G::TE * 2) + (w * LP + part) * 1024);
+  };
+  auto load_r = [&](u32x4 srd, int kt, int part) __attribute__((always_inline)) {
+    dma_bounded<false>(srd, vr, (w * LR + part) * qr, smem + L::R + (kt & 3) * L::RE + (w * LR + part) * 1024);
+  };
+  auto load_s = [&](u32x4 srd, int kt) __attribute__((always_inline)) {
+    dma_bounded<true>(srd, vs, qs, smem + L::S + (kt & 3) * L::SE + w * 256);
+  };
+
+  // this lane's part in the unpacking
+  const int ur = lane >> 3, uc = lane & 7;               // row of the wave's 8, group or piece
+  const int hx = TILE == 256 ? (ur ^ (ur >> 1)) & 1 : 0, ix = ur & 1;
+  const int swz = 2 * (ur & 3) + 8 * (w & 1);
+  u32x4 raw[LR];
+  float scale = 0.f;
+  auto fetch = [&](int kt, int h) __attribute__((always_inline)) {                 // codes, 16 columns
+    const char* r = smem + L::R + (kt & 3) * L::RE + w * (8 * TILE);
+    raw[h] = *reinterpret_cast<const u32x4*>(r + ur * TILE + (TILE == 256 ? 32 * uc + 16 * (hx ^ h) : 16 * uc));
+  };
+  auto fetch_scale = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(smem + L::S + (kt & 3) * L::SE + w * 256);
+    scale = act8_scale(s[TILE == 256 ? lane : ur * 4 + (uc >> 1)]);
+  };
+  auto unpack = [&](int kt, int q) __attribute__((always_inline)) {                // 8 columns: write q of 2 LR
+    const int h = q >> 1, i = (q & 1) ^ ix;
+    const uint32_t a = i ? raw[h][2] : raw[h][0], b = i ? raw[h][3] : raw[h][1];
+    u32x4 o;
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true));
+    const int c = TILE == 256 ? 4 * uc + 2 * (hx ^ h) + i : 2 * uc + i;
+    char* t = smem + L::B + (kt & 1) * (G::TE * 2);
+    *reinterpret_cast<u32x4*>(t + (8 * w + ur) * (TILE * 2) + ((c ^ swz) << 4)) = o;
+  };
+  auto tile_p = [&](int kt) { return reinterpret_cast<const uint16_t*>(smem + L::P + (kt & 3) * (G::TE * 2)); };
+  auto tile_b = [&](int kt) { return reinterpret_cast<const uint16_t*>(smem + L::B + (kt & 1) * (G::TE * 2)); };
+
+  // dY of steps 0 .. 2, x8 of steps 0 .. 3, what the loop's step -1 would load
+  // last.  Steps past the end are the last step again, never multiplied.
+  const int last = steps - 1;
+  auto load_x = [&](int kt) __attribute__((always_inline)) {
+    const u32x4 r = fr.step(min(kt, last)), s = fs.step(min(kt, last));
+#pragma unroll
+    for (int part = 0; part < LR; ++part) load_r(r, kt, part);
+    load_s(s, kt);
+  };
+  load_x(0);
+  load_x(1);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const u32x4 srd = fp.step(min(k, last));
+#pragma unroll
+    for (int part = 0; part < LP; ++part) load_p(srd, k, part);
+    if (k > 0) load_x(k + 1);
+  }
+  vm_wait<LPS>();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int h = 0; h < LR; ++h) fetch(k, h);
+    fetch_scale(k);
+#pragma unroll
+    for (int q = 0; q < 2 * LR; ++q) unpack(k, q);
+  }
+  lds_barrier();
+  bf16x8_t fa[NB], fb[NB];
+#pragma unroll
+  for (int r = 0; r < H; ++r) fa[r] = frag<true, TILE>(tile_p(0), rowA + 16 * r, lane);
+#pragma unroll
+  for (int r = 0; r < NB; ++r) fb[r] = frag<true, TILE>(tile_b(0), rowB + 16 * r, lane);
+
+  for (int kt = 0; kt < steps; ++kt) {
+    const u32x4 dyd = fp.step(min(kt + 3, last)), cod = fr.step(min(kt + 4, last)), scd = fs.step(min(kt + 4, last));
+    vm_wait<LPS>();
+    lds_barrier();
+    const uint16_t* cu = tile_p(kt);
+    const uint16_t* nx = tile_p(kt + 1);
+    const uint16_t* nb = tile_b(kt + 1);
+    static_for<SLOTS>([&](auto sc) __attribute__((always_inline)) {
+      constexpr int s = decltype(sc)::value, pass = s / PASS, sp = s % PASS;
+      constexpr int bi = pass * H + sp % H, bj = sp / H;
+      acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[bj], fa[bi], acc[bi][bj], 0, 0, 0);
+      if constexpr (s < H) fa[H + s] = frag<true, TILE>(cu, rowA + 16 * (H + s), lane);
+      if constexpr (s >= PASS && s < PASS + H) fa[s - PASS] = frag<true, TILE>(nx, rowA + 16 * (s - PASS), lane);
+      if constexpr (pass == 1 && sp % H == H - 1) fb[bj] = frag<true, TILE>(nb, rowB + 16 * bj, lane);
+      if constexpr (s >= H && (s - H) % LSS == 0) {
+        constexpr int part = (s - H) / LSS;
+        if constexpr (part < LP) load_p(dyd, kt + 3, part);
+        else if constexpr (part < LP + LR) load_r(cod, kt + 4, part - LP);
+        else if constexpr (part < LPS) load_s(scd, kt + 4);
+      }
+      // unpacking: the codes and scale early in the first pass, the rest later in it
+      if constexpr (s >= H && s < H + LR) fetch(kt + 2, s - H);
+      if constexpr (s == H + LR) fetch_scale(kt + 2);
+      constexpr int U0 = PASS / 2, US = (PASS - U0) / (2 * LR);
+      if constexpr (s >= U0 && (s - U0) % US == 0 && (s - U0) / US < 2 * LR) unpack(kt + 2, (s - U0) / US);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+  vm_wait<0>();
+}
+
+// ---------------------------------------------------------------- output ----
+// Four consecutive elements from column j of row i, n of them inside.
 template <class T>
-__device__ __forceinline__ void put_out(const muon_act8_wgrad_t& op, int64_t i, int64_t j, float v) {
-  if (op.col_gain) v *= gld<float>(op.col_gain + j);
+__device__ __forceinline__ void put4(const muon_act8_wgrad_t& op, int64_t i, int64_t j, f32x4_t v) {
+  const int n = static_cast<int>(min(op.k - j, int64_t(4)));
   T* p = static_cast<T*>(op.dw) + i * op.ld_dw + j;
-  if constexpr (sizeof(T) == 2) {
-    if (op.accumulate) v += bf2f(gld<uint16_t>(p));
-    gst<uint16_t>(p, f2bf(v));
-  } else {
-    if (op.accumulate) v += gld<float>(p);
-    gst<float>(p, v);
+  typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+  typedef uint16_t u16x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+  if (n == 4) {
+    if (op.col_gain) v *= gld<f32x4_a4>(op.col_gain + j);
+    if constexpr (sizeof(T) == 2) {
+      if (op.accumulate) {
+        const u16x4_a2 o = gld<u16x4_a2>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += bf2f(o[e]);
+      }
+      u16x4_a2 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = f2bf(v[e]);
+      gst<u16x4_a2>(p, o);
+    } else {
+      if (op.accumulate) v += gld<f32x4_a4>(p);
+      gst<f32x4_a4>(p, v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (e >= n) break;
+    float x = v[e];
+    if (op.col_gain) x *= gld<float>(op.col_gain + j + e);
+    if constexpr (sizeof(T) == 2) {
+      if (op.accumulate) x += bf2f(gld<uint16_t>(p + e));
+      gst<uint16_t>(p + e, f2bf(x));
+    } else {
+      if (op.accumulate) x += gld<float>(p + e);
+      gst<float>(p + e, x);
+    }
   }
 }
 
+// partial: [split][n][k rounded up to 4] where there are several token ranges.
+__host__ __device__ __forceinline__ int64_t partial_ld(int64_t k) { return (k + 3) / 4 * 4; }
+
+template <int TILE>
 __global__ __launch_bounds__(kGemmThreads) void k_wgrad(muon_act8_wgrad_t op, WgradPlan p, float* partial) {
-  __shared__ __attribute__((aligned(16))) uint16_t sm[2 * G::TE];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t unit = blockIdx.x, tiles = p.tiles_n * p.tiles_k;
-  const int64_t split = unit / tiles, tile = unit % tiles;
-  const int64_t i0 = tile / p.tiles_k * kTile, j0 = tile % p.tiles_k * kTile;
-  const int64_t t0 = split * p.split_rows;
-  const int64_t t1 = t0 + p.split_rows < op.tokens ? t0 + p.split_rows : op.tokens;
-  const uint16_t* dy = static_cast<const uint16_t*>(op.dy);
+  using G = Geo<TILE>;
+  __shared__ __attribute__((aligned(16))) char smem[Lds<TILE>::bytes];
+  const int tid = opaque_tid();
+  const int64_t unit = xcd_remap(blockIdx.x, gridDim.x), tiles = p.tiles_n * p.tiles_k;
+  const int64_t split = unit / tiles;
+  int64_t ti, tj;
+  decode_full(unit - split * tiles, p.tiles_n, p.tiles_k, ti, tj);
+  const int64_t i0 = ti * TILE, j0 = tj * TILE, t0 = split * p.split_rows;
+  const int64_t rows = min(p.split_rows, op.tokens - t0);
   f32x4_t acc[G::NB][G::NB];
   zero_acc<G::NB>(acc);
-  const int rowA = G::WT * (w >> 1), rowB = G::WT * (w & 1);
-  for (int64_t t = t0; t < t1; t += BK) {
+  product<TILE>(op, i0, j0, t0, static_cast<int>((rows + BK - 1) / BK), smem, acc, tid);
+  // The sums leave through LDS, TILE / 2 rows (two waves) at a time, whole rows
+  // of the tile side by side: 16-byte pieces, piece c of row r at c ^ (r & 15) (the
+  // 16 rows that one write instruction covers then fall on distinct banks).
+  // Lane: row 16 bi + (lane & 15), columns 16 bj + 4 (lane >> 4) .. + 3.
+  static_assert(TILE / 2 * TILE * 4 <= Lds<TILE>::bytes, "half a tile of fp32");
+  const int lane = tid & 63, w = tid >> 6;
+  constexpr int PPR = TILE / 4;                     // pieces of a row
+  for (int half = 0; half < 2; ++half) {
+    lds_barrier();
+    if ((w >> 1) == half) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int v = tid + q * kGemmThreads, r = v >> 4, c = v & 15;
-      const bool in = t + r < t1;
-      Vec8<uint16_t> a;
-      load8(a, dy + (t + r) * op.ld_dy + i0 + c * 8, in ? static_cast<int>(min(op.n - i0 - c * 8, int64_t(8))) : 0);
-      *reinterpret_cast<u32x4*>(sm + chunk_at(r, c)) = a.r;
-      const int n = in ? static_cast<int>(min(op.k - j0 - c * 8, int64_t(8))) : 0;
-      u32x4 b{0, 0, 0, 0};
-      if (n > 0) {
-        const u32x2 code = load_codes(op.x8.codes + (t + r) * op.x8.ld_codes + j0 + c * 8, n);
-        float f[8];
-        act8_decode(code, gld<uint8_t>(op.x8.scales + (t + r) * op.x8.ld_scales + ((j0 + c * 8) >> 5)), f);
+      for (int bi = 0; bi < G::NB; ++bi)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) b[k] = pack2(f[2 * k], f[2 * k + 1]);
-      }
-      *reinterpret_cast<u32x4*>(sm + G::TE + chunk_at(r, c)) = b;
+        for (int bj = 0; bj < G::NB; ++bj) {
+          const int r = 16 * bi + (lane & 15), c = (G::WT / 4) * (w & 1) + 4 * bj + (lane >> 4);
+          *reinterpret_cast<f32x4_t*>(smem + (r * PPR + (c ^ (r & 15))) * 16) = acc[bi][bj];
+        }
     }
-    __syncthreads();
-    bf16x8_t fa[G::NB], fb[G::NB];
-#pragma unroll
-    for (int k = 0; k < G::NB; ++k) {
-      fa[k] = frag<true, kTile>(sm, rowA + 16 * k, lane);
-      fb[k] = frag<true, kTile>(sm + G::TE, rowB + 16 * k, lane);
-    }
-#pragma unroll
-    for (int bi = 0; bi < G::NB; ++bi)
-#pragma unroll
-      for (int bj = 0; bj < G::NB; ++bj)
-        acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[bj], fa[bi], acc[bi][bj], 0, 0, 0);
-    __syncthreads();
-  }
-  // lane: row 16 bi + (lane & 15), columns 16 bj + 4 (lane >> 4) .. + 3
-#pragma unroll
-  for (int bi = 0; bi < G::NB; ++bi) {
-    const int64_t i = i0 + rowA + 16 * bi + (lane & 15);
-    if (i >= op.n) continue;
-#pragma unroll
-    for (int bj = 0; bj < G::NB; ++bj)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t j = j0 + rowB + 16 * bj + 4 * (lane >> 4) + e;
-        if (j >= op.k) continue;
-        if (p.splits > 1) gst<float>(partial + (split * op.n + i) * op.k + j, acc[bi][bj][e]);
-        else if (op.dw_dtype == MUON_BF16) put_out<uint16_t>(op, i, j, acc[bi][bj][e]);
-        else put_out<float>(op, i, j, acc[bi][bj][e]);
+    lds_barrier();
+#pragma unroll 4
+    for (int u = tid; u < TILE / 2 * PPR; u += kGemmThreads) {
+      const int r = u / PPR, c = u % PPR;
+      const int64_t i = i0 + half * (TILE / 2) + r, j = j0 + 4 * c;
+      if (i < op.n && j < op.k) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(smem + (r * PPR + (c ^ (r & 15))) * 16);
+        if (p.splits > 1) gst<f32x4_t>(partial + (split * op.n + i) * partial_ld(op.k) + j, v);
+        else if (op.dw_dtype == MUON_BF16) put4<uint16_t>(op, i, j, v);
+        else put4<float>(op, i, j, v);
       }
+    }
   }
 }
 
-// The token ranges' sums, added in order (no range: zero).
+// The token ranges' sums, added in order (no range: zero), 4 columns a thread.
 __global__ __launch_bounds__(256) void k_wgrad_join(muon_act8_wgrad_t op, int64_t splits, const float* partial) {
-  for (int64_t u = blockIdx.x * int64_t(256) + threadIdx.x; u < op.n * op.k; u += int64_t(gridDim.x) * 256) {
-    float v = 0.f;
-    for (int64_t s = 0; s < splits; ++s) v += gld<float>(partial + s * op.n * op.k + u);
-    const int64_t i = u / op.k, j = u % op.k;
-    if (op.dw_dtype == MUON_BF16) put_out<uint16_t>(op, i, j, v);
-    else put_out<float>(op, i, j, v);
+  const int64_t ld = partial_ld(op.k), n4 = op.n * (ld / 4);
+  for (int64_t u = blockIdx.x * int64_t(256) + threadIdx.x; u < n4; u += int64_t(gridDim.x) * 256) {
+    f32x4_t v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int64_t s = 0; s < splits; ++s) v += gld<f32x4_t>(partial + s * op.n * ld + 4 * u);
+    const int64_t i = u / (ld / 4), j = (u - i * (ld / 4)) * 4;
+    if (op.dw_dtype == MUON_BF16) put4<uint16_t>(op, i, j, v);
+    else put4<float>(op, i, j, v);
   }
 }
+
+// A matrix of `width`-byte rows at any place, copied to rows of ld_out bytes (a
+// multiple of 16), zeros past each row's end.
+__global__ __launch_bounds__(256) void k_wgrad_copy(const uint8_t* in, int64_t ld_in, int64_t rows, int64_t width, uint8_t* out,
+                                                    int64_t ld_out) {
+  typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
+  const int64_t per = ld_out / 16, units = rows * per;
+  for (int64_t u = blockIdx.x * int64_t(256) + threadIdx.x; u < units; u += int64_t(gridDim.x) * 256) {
+    const int64_t r = u / per, c = (u - r * per) * 16;
+    const uint8_t* p = in + r * ld_in + c;
+    u32x4 v{0, 0, 0, 0};
+    if (c + 16 <= width) {
+      v = gld<u32x4_a1>(p);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 16; ++b)
+        if (c + b < width) v[b >> 2] |= static_cast<uint32_t>(gld<uint8_t>(p + b)) << (8 * (b & 3));
+    }
+    gst<u32x4>(out + r * ld_out + c, v);
+  }
+}
+
+bool is_aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
 
 WgradPlan wgrad_plan(const muon_act8_wgrad_t& op) {
-  WgradPlan p;
-  p.tiles_n = (op.n + kTile - 1) / kTile;
-  p.tiles_k = (op.k + kTile - 1) / kTile;
+  WgradPlan p{};
+  // 256 x 256 tiles where they fill the chip
+  p.tile = op.n * op.k >= int64_t(256) * 256 * 128 && std::min(op.n, op.k) >= 256 ? 256 : 128;
+  p.tiles_n = (op.n + p.tile - 1) / p.tile;
+  p.tiles_k = (op.k + p.tile - 1) / p.tile;
   const int64_t tiles = p.tiles_n * p.tiles_k, steps = (op.tokens + BK - 1) / BK;
-  // token ranges until there are two blocks per CU, of 8 steps at least
-  int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 8));
+  // token ranges until the chip is full (a 256-tile block takes a CU, two of
+  // 128 share one), of 8 steps at least
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((p.tile == 256 ? 256 : 512) / tiles, steps / 8));
   p.split_rows = std::max<int64_t>(1, (steps + want - 1) / want) * BK;
   p.splits = (op.tokens + p.split_rows - 1) / p.split_rows;
-  p.bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * op.n * op.k * sizeof(float) : 0;
+  // the loads take 16 bytes at multiples of 16, rows that end on a dword, and
+  // 32-bit offsets within a step's 32 rows
+  constexpr int64_t kMaxLd = int64_t(1) << 25;
+  p.copy_dy = op.tokens > 0 && !(is_aligned(op.dy, 16) && op.ld_dy % 8 == 0 && op.ld_dy < kMaxLd && op.n % 2 == 0);
+  p.copy_x = op.tokens > 0 && !(is_aligned(op.x8.codes, 16) && op.x8.ld_codes % 16 == 0 && op.x8.ld_codes < kMaxLd &&
+                                op.x8.ld_scales < kMaxLd && op.k % 4 == 0);
+  size_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t at = off;
+    off += static_cast<size_t>(up(bytes, 256));
+    return at;
+  };
+  if (p.splits > 1) p.partial_off = take(p.splits * op.n * partial_ld(op.k) * 4);
+  if (p.copy_dy) p.dy_off = take(op.tokens * up(op.n, 8) * 2);
+  if (p.copy_x) {
+    p.x_off = take(op.tokens * up(op.k, 16));
+    p.s_off = take(op.tokens * up((op.k + 31) / 32, 16));
+  }
+  p.bytes = off;
   return p;
 }
 
-int launch_wgrad(const muon_act8_wgrad_t& op, const WgradPlan& p, void* workspace, void* stream) {
-  hipLaunchKernelGGL(k_wgrad, dim3(static_cast<unsigned>(p.splits * p.tiles_n * p.tiles_k)), dim3(kGemmThreads), 0,
-                     static_cast<hipStream_t>(stream), op, p, static_cast<float*>(workspace));
+int launch_wgrad_copy(muon_act8_wgrad_t& op, const WgradPlan& p, char* ws, void* stream) {
+  auto copy = [&](const void* in, int64_t ld_in, int64_t width, char* out, int64_t ld_out) {
+    const int64_t blocks = std::min<int64_t>((op.tokens * (ld_out / 16) + 255) / 256, int64_t(1) << 20);
+    hipLaunchKernelGGL(k_wgrad_copy, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream),
+                       static_cast<const uint8_t*>(in), ld_in, op.tokens, width, reinterpret_cast<uint8_t*>(out), ld_out);
+  };
+  if (p.copy_dy) {
+    const int64_t ld = up(op.n, 8);
+    copy(op.dy, op.ld_dy * 2, op.n * 2, ws + p.dy_off, ld * 2);
+    op.dy = ws + p.dy_off;
+    op.ld_dy = ld;
+  }
+  if (p.copy_x) {
+    const int64_t ld = up(op.k, 16);
+    copy(op.x8.codes, op.x8.ld_codes, op.k, ws + p.x_off, ld);
+    op.x8.codes = reinterpret_cast<uint8_t*>(ws + p.x_off);
+    op.x8.ld_codes = ld;
+    const int64_t groups = (op.k + 31) / 32, lds = up(groups, 16);
+    copy(op.x8.scales, op.x8.ld_scales, groups, ws + p.s_off, lds);
+    op.x8.scales = reinterpret_cast<uint8_t*>(ws + p.s_off);
+    op.x8.ld_scales = lds;
+  }
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const void* workspace, void* stream) {
-  const int64_t blocks = std::min<int64_t>((op.n * op.k + 255) / 256, 8192);
+int launch_wgrad(const muon_act8_wgrad_t& op, const WgradPlan& p, char* ws, void* stream) {
+  const dim3 grid(static_cast<unsigned>(p.splits * p.tiles_n * p.tiles_k));
+  float* partial = p.splits > 1 ? reinterpret_cast<float*>(ws + p.partial_off) : nullptr;
+  if (p.tile == 256)
+    hipLaunchKernelGGL(k_wgrad<256>, grid, dim3(kGemmThreads), 0, static_cast<hipStream_t>(stream), op, p, partial);
+  else
+    hipLaunchKernelGGL(k_wgrad<128>, grid, dim3(kGemmThreads), 0, static_cast<hipStream_t>(stream), op, p, partial);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const char* ws, void* stream) {
+  const int64_t blocks = std::min<int64_t>((op.n * (partial_ld(op.k) / 4) + 255) / 256, 8192);
   hipLaunchKernelGGL(k_wgrad_join, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream),
-                     op, p.splits, static_cast<const float*>(workspace));
+                     op, p.splits, reinterpret_cast<const float*>(ws + p.partial_off));
   return static_cast<int>(hipGetLastError());
 }
 
