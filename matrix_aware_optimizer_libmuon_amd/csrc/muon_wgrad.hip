@@ -47,48 +47,36 @@ __device__ __forceinline__ void dma_bounded(u32x4 srd, uint32_t voff, uint32_t s
     asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(m0));
 }
 
-// A matrix of which a block reads the rows from row0 on, columns from byte col0:
-// step kt is its 32 rows from 32 kt.  The descriptor of a step ends where the
-// matrix ends (offsets within a step stay below 2^31: wgrad_plan).
-struct Feed {
-  const char* base;
-  int64_t bytes;     // from base to the matrix's end
-  int64_t kstep;
-  __device__ __forceinline__ Feed(const void* p, int64_t ld_bytes, int64_t rows, int64_t row_bytes, int64_t row0, int64_t col0) {
-    base = static_cast<const char*>(p) + row0 * ld_bytes + col0;
-    bytes = (rows - 1 - row0) * ld_bytes + row_bytes - col0;
-    kstep = BK * ld_bytes;
-  }
-  __device__ __forceinline__ u32x4 step(int kt) const {
-    const int64_t off = kt * kstep, left = bytes - off;
-    const uint64_t b = reinterpret_cast<uint64_t>(base + off);
-    u32x4 srd;
-    srd[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
-    srd[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32) & 0xffffu);
-    srd[2] = __builtin_amdgcn_readfirstlane(left < 0x7fffffff ? static_cast<uint32_t>(left) : 0x7fffffffu);
-    srd[3] = 0x00020000u;   // raw buffer of dwords
-    return srd;
-  }
-};
+// The descriptor of `rows` rows from row0, columns from byte col0, of a matrix:
+// it ends with the last of them (wgrad_plan keeps that below 2^31 bytes).
+__device__ __forceinline__ u32x4 window(const void* p, int64_t ld_bytes, int64_t row_bytes, int64_t row0, int64_t rows, int64_t col0) {
+  const uint64_t b = reinterpret_cast<uint64_t>(p) + row0 * ld_bytes + col0;
+  u32x4 srd;
+  srd[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
+  srd[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32) & 0xffffu);
+  srd[2] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>((rows - 1) * ld_bytes + row_bytes - col0));
+  srd[3] = 0x00020000u;   // raw buffer of dwords
+  return srd;
+}
 
 template <int TILE>
 struct Lds {
   static constexpr int TE = Geo<TILE>::TE;
   static constexpr int RE = TILE * BK;                   // bytes of codes of a step
   static constexpr int SE = 4 * 64 * 4;                  // a dword per wave and lane for the scales
-  static constexpr int P = 0;                            // dY: 4 stages of bf16
+  static constexpr int B = 0;                            // unpacked x: 2 stages of bf16
+  static constexpr int P = B + 2 * TE * 2;               // dY: 4 stages of bf16
   static constexpr int R = P + 4 * TE * 2;               // codes: 4 stages
   static constexpr int S = R + 4 * RE;                   // scales: 4 stages
-  static constexpr int B = S + 4 * SE;                   // unpacked x: 2 stages of bf16
-  static constexpr int bytes = B + 2 * TE * 2;
+  static constexpr int bytes = S + 4 * SE;
 };
 static_assert(Lds<256>::bytes <= 160 * 1024 && 2 * Lds<128>::bytes <= 160 * 1024, "LDS per CU");
 
 // ------------------------------------------------------------ the product ----
-// acc += dY[t0 .., i0 .. i0 + TILE]^T x[t0 .., j0 .. j0 + TILE] over `steps`
-// steps of 32 tokens; 4 waves of TILE / 2 x TILE / 2, one MFMA per slot in the
-// order of muon_gemm.h, operands exchanged (a lane ends up with four consecutive
-// columns of one row).
+// acc += dY[t0 .. + rows, i0 .. + TILE]^T x[t0 .. + rows, j0 .. + TILE], in steps of
+// 32 tokens; 4 waves of TILE / 2 x TILE / 2, one MFMA per slot in the order of
+// muon_gemm.h, operands exchanged (a lane ends up with four consecutive columns of
+// one row).
 //
 // Step kt opens with a wait for this wave's loads of two steps before (dY of
 // step kt + 1, codes and scales of kt + 2 have landed) and a barrier, and then
@@ -96,14 +84,19 @@ static_assert(Lds<256>::bytes <= 160 * 1024 && 2 * Lds<128>::bytes <= 160 * 1024
 //   loads dY of step kt + 3 and codes and scales of step kt + 4,
 //   unpacks x of step kt + 2, into the tile whose fragments were read before the
 //   barrier.
+// Loads past the last token give zeros and read nothing.
 //
-// The wave's codes of a step are 8 token rows.  TILE 256: lane l unpacks the 32
-// columns of group l & 7 of row l >> 3, two pieces of 16; TILE 128: the 16 columns
-// from 16 (l & 7).  Which half of its columns a lane reads and writes first
-// depends on its row such that the 16 lanes that LDS serves at a time touch all
-// banks (a row is one or two sweeps of the banks).
+// At TILE 256 a SIMD has one wave, which issues an instruction every 4 cycles at
+// best, 256 of them while its 64 MFMAs run: the loop has to stay below that.
+// Hence descriptors that hold for the whole product, where a step is a scalar
+// offset.
+//
+// The wave's codes of a step are 8 token rows; each lane unpacks 8 columns at a
+// time, the lanes side by side along a row, so that 8 consecutive lanes write 128
+// consecutive bytes (LDS takes a 16-byte write in such groups: with a lane on 32
+// columns of its own the writes took four times as long).
 template <int TILE>
-__device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0, int64_t j0, int64_t t0, int steps,
+__device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0, int64_t j0, int64_t t0, int64_t rows,
                                         char* smem, f32x4_t (&acc)[Geo<TILE>::NB][Geo<TILE>::NB], int tid) {
   using G = Geo<TILE>;
   using L = Lds<TILE>;
@@ -112,93 +105,84 @@ __device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0,
   constexpr int LSS = (SLOTS - H) / LPS;                 // loads spread over the step
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rowA = G::WT * (w >> 1), rowB = G::WT * (w & 1);
+  const int steps = static_cast<int>((rows + BK - 1) / BK);
 
+  const uint32_t ldp = static_cast<uint32_t>(op.ld_dy * 2), ldr = static_cast<uint32_t>(op.x8.ld_codes),
+                 lds = static_cast<uint32_t>(op.x8.ld_scales);
   // rows end on a dword: in memory, or in the padding of an aligned copy
-  const Feed fp(op.dy, op.ld_dy * 2, op.tokens, (op.n * 2 + 3) / 4 * 4, t0, i0 * 2);
-  const Feed fr(op.x8.codes, op.x8.ld_codes, op.tokens, (op.k + 3) / 4 * 4, t0, j0);
-  const Feed fs(op.x8.scales, op.x8.ld_scales, op.tokens, (op.k + 31) / 32, t0, j0 / 32);
+  const u32x4 dp = window(op.dy, op.ld_dy * 2, (op.n * 2 + 3) / 4 * 4, t0, rows, i0 * 2);
+  const u32x4 dr = window(op.x8.codes, op.x8.ld_codes, (op.k + 3) / 4 * 4, t0, rows, j0);
+  const u32x4 ds = window(op.x8.scales, op.x8.ld_scales, (op.k + 31) / 32, t0, rows, j0 / 32);
   // dY: the MN-contiguous form of DmaFeed (muon_gemm.h)
   constexpr int CPR = TILE / 8, RPB = 512 / TILE;        // chunks of a row, rows of a 1 KB load
-  uint32_t vp[2], vr, vs;
+  uint32_t vp[2];
 #pragma unroll
   for (int par = 0; par < 2; ++par) {
     const int r = lane / CPR, c = (lane % CPR) ^ (2 * ((RPB * par + r) & 3) + 8 * (w & 1));
-    vp[par] = static_cast<uint32_t>(r * op.ld_dy * 2 + 16 * c);
+    vp[par] = r * ldp + 16 * c;
   }
   constexpr int RCPR = TILE / 16, RRPB = 1024 / TILE;    // the same of the codes
-  vr = static_cast<uint32_t>((lane / RCPR) * op.x8.ld_codes + 16 * (lane % RCPR));
+  const uint32_t vr = (lane / RCPR) * ldr + 16 * (lane % RCPR);
   constexpr int SPR = TILE / 32;                         // scales of a row; lanes past 8 rows repeat
-  vs = static_cast<uint32_t>(((lane / SPR) & 7) * op.x8.ld_scales + lane % SPR);
+  const uint32_t vs = ((lane / SPR) & 7) * lds + lane % SPR;
+  // the wave's share of the step to be loaded next: dY parts 0 .. LP - 1, codes, scales
+  uint32_t sp = (w * LP * RPB) * ldp, sr = (w * LR * RRPB) * ldr, ss = (w * 8) * lds;
+  auto load_p = [&](int st, auto part) __attribute__((always_inline)) {        // st: kt & 3
+    constexpr int q = decltype(part)::value;
+    dma_bounded<false>(dp, vp[q & 1], sp + q * (RPB * ldp), smem + L::P + st * (G::TE * 2) + (w * LP + q) * 1024);
+    if constexpr (q == LP - 1) sp += BK * ldp;
+  };
+  auto load_x = [&](int st, auto part) __attribute__((always_inline)) {
+    constexpr int q = decltype(part)::value;
+    if constexpr (q < LR) {
+      dma_bounded<false>(dr, vr, sr + q * (RRPB * ldr), smem + L::R + st * L::RE + (w * LR + q) * 1024);
+      if constexpr (q == LR - 1) sr += BK * ldr;
+    } else {
+      dma_bounded<true>(ds, vs, ss, smem + L::S + st * L::SE + w * 256);
+      ss += BK * lds;
+    }
+  };
 
-  // the shares of the wave in a step: dY parts 0 .. LP - 1, codes, scales
-  const uint32_t qp = static_cast<uint32_t>(RPB * op.ld_dy * 2), qr = static_cast<uint32_t>(RRPB * op.x8.ld_codes);
-  const uint32_t qs = static_cast<uint32_t>(8 * w * op.x8.ld_scales);
-  auto load_p = [&](u32x4 srd, int kt, int part) __attribute__((always_inline)) {
-    dma_bounded<false>(srd, vp[part & 1], (w * LP + part) * qp, smem + L::P + (kt & 3) * (G::TE * 2) + (w * LP + part) * 1024);
-  };
-  auto load_r = [&](u32x4 srd, int kt, int part) __attribute__((always_inline)) {
-    dma_bounded<false>(srd, vr, (w * LR + part) * qr, smem + L::R + (kt & 3) * L::RE + (w * LR + part) * 1024);
-  };
-  auto load_s = [&](u32x4 srd, int kt) __attribute__((always_inline)) {
-    dma_bounded<true>(srd, vs, qs, smem + L::S + (kt & 3) * L::SE + w * 256);
-  };
-
-  // this lane's part in the unpacking
-  const int ur = lane >> 3, uc = lane & 7;               // row of the wave's 8, group or piece
-  const int hx = TILE == 256 ? (ur ^ (ur >> 1)) & 1 : 0, ix = ur & 1;
-  const int swz = 2 * (ur & 3) + 8 * (w & 1);
-  u32x4 raw[LR];
-  float scale = 0.f;
-  auto fetch = [&](int kt, int h) __attribute__((always_inline)) {                 // codes, 16 columns
-    const char* r = smem + L::R + (kt & 3) * L::RE + w * (8 * TILE);
-    raw[h] = *reinterpret_cast<const u32x4*>(r + ur * TILE + (TILE == 256 ? 32 * uc + 16 * (hx ^ h) : 16 * uc));
-  };
-  auto fetch_scale = [&](int kt) __attribute__((always_inline)) {
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(smem + L::S + (kt & 3) * L::SE + w * 256);
-    scale = act8_scale(s[TILE == 256 ? lane : ur * 4 + (uc >> 1)]);
-  };
-  auto unpack = [&](int kt, int q) __attribute__((always_inline)) {                // 8 columns: write q of 2 LR
-    const int h = q >> 1, i = (q & 1) ^ ix;
-    const uint32_t a = i ? raw[h][2] : raw[h][0], b = i ? raw[h][3] : raw[h][1];
-    u32x4 o;
-    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false));
-    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true));
-    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false));
-    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true));
-    const int c = TILE == 256 ? 4 * uc + 2 * (hx ^ h) + i : 2 * uc + i;
-    char* t = smem + L::B + (kt & 1) * (G::TE * 2);
-    *reinterpret_cast<u32x4*>(t + (8 * w + ur) * (TILE * 2) + ((c ^ swz) << 4)) = o;
-  };
-  auto tile_p = [&](int kt) { return reinterpret_cast<const uint16_t*>(smem + L::P + (kt & 3) * (G::TE * 2)); };
-  auto tile_b = [&](int kt) { return reinterpret_cast<const uint16_t*>(smem + L::B + (kt & 1) * (G::TE * 2)); };
-
-  // dY of steps 0 .. 2, x8 of steps 0 .. 3, what the loop's step -1 would load
-  // last.  Steps past the end are the last step again, never multiplied.
-  const int last = steps - 1;
-  auto load_x = [&](int kt) __attribute__((always_inline)) {
-    const u32x4 r = fr.step(min(kt, last)), s = fs.step(min(kt, last));
+  // unpacking: piece q covers 1024 / TILE rows of the wave's 8, 8 columns a lane
+  constexpr int Q = 2 * LR, URP = 8 / Q, UL = 64 / URP;  // pieces, rows of a piece, lanes of a row
+  const int ur = lane / UL, uc = lane % UL;
+  const char* const raw_at = smem + L::R + (8 * w + ur) * TILE + 8 * uc;
+  const char* const sb_at = smem + L::S + w * 256 + (ur * SPR + (uc >> 2)) * 4;
+  char* x_at[Q];
 #pragma unroll
-    for (int part = 0; part < LR; ++part) load_r(r, kt, part);
-    load_s(s, kt);
-  };
-  load_x(0);
-  load_x(1);
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const u32x4 srd = fp.step(min(k, last));
-#pragma unroll
-    for (int part = 0; part < LP; ++part) load_p(srd, k, part);
-    if (k > 0) load_x(k + 1);
+  for (int q = 0; q < Q; ++q) {
+    const int r = URP * q + ur;
+    x_at[q] = smem + L::B + (8 * w + r) * (TILE * 2) + ((uc ^ (2 * (r & 3) + 8 * (w & 1))) << 4);
   }
+  u32x2 raw[Q];
+  uint32_t sb[Q];
+  auto fetch = [&](int st, auto piece) __attribute__((always_inline)) {
+    constexpr int q = decltype(piece)::value;
+    raw[q] = *reinterpret_cast<const u32x2*>(raw_at + st * L::RE + URP * q * TILE);
+    sb[q] = *reinterpret_cast<const uint32_t*>(sb_at + st * L::SE + URP * q * SPR * 4);
+  };
+  u32x4 o;
+  auto unpack = [&](int st, auto part) __attribute__((always_inline)) {        // a quarter of a piece; st: kt & 1
+    constexpr int q = decltype(part)::value / 4, i = decltype(part)::value % 4;
+    const float scale = act8_scale(sb[q]);
+    o[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[q][i >> 1], scale, (i & 1) != 0));
+    if constexpr (i == 3) *reinterpret_cast<u32x4*>(x_at[q] + st * (G::TE * 2)) = o;
+  };
+  auto tile_p = [&](int st) { return reinterpret_cast<const uint16_t*>(smem + L::P + st * (G::TE * 2)); };
+  auto tile_b = [&](int st) { return reinterpret_cast<const uint16_t*>(smem + L::B + st * (G::TE * 2)); };
+
+  // x8 of steps 0 .. 3 and dY of steps 0 .. 2, the share of the loop's step -1 last
+  static_for<2>([&](auto k) { static_for<LR + 1>([&](auto part) { load_x(k, part); }); });
+  static_for<3>([&](auto k) {
+    static_for<LP>([&](auto part) { load_p(k, part); });
+    if constexpr (decltype(k)::value > 0)
+      static_for<LR + 1>([&](auto part) { load_x(k + 1, part); });
+  });
   vm_wait<LPS>();
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-#pragma unroll
-    for (int h = 0; h < LR; ++h) fetch(k, h);
-    fetch_scale(k);
-#pragma unroll
-    for (int q = 0; q < 2 * LR; ++q) unpack(k, q);
-  }
+  static_for<2>([&](auto k) {
+    static_for<Q>([&](auto q) { fetch(k, q); });
+    static_for<4 * Q>([&](auto part) { unpack(k, part); });
+  });
   lds_barrier();
   bf16x8_t fa[NB], fb[NB];
 #pragma unroll
@@ -207,30 +191,27 @@ __device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0,
   for (int r = 0; r < NB; ++r) fb[r] = frag<true, TILE>(tile_b(0), rowB + 16 * r, lane);
 
   for (int kt = 0; kt < steps; ++kt) {
-    const u32x4 dyd = fp.step(min(kt + 3, last)), cod = fr.step(min(kt + 4, last)), scd = fs.step(min(kt + 4, last));
     vm_wait<LPS>();
     lds_barrier();
-    const uint16_t* cu = tile_p(kt);
-    const uint16_t* nx = tile_p(kt + 1);
-    const uint16_t* nb = tile_b(kt + 1);
+    const uint16_t* cu = tile_p(kt & 3);
+    const uint16_t* nx = tile_p((kt + 1) & 3);
+    const uint16_t* nb = tile_b((kt + 1) & 1);
     static_for<SLOTS>([&](auto sc) __attribute__((always_inline)) {
-      constexpr int s = decltype(sc)::value, pass = s / PASS, sp = s % PASS;
-      constexpr int bi = pass * H + sp % H, bj = sp / H;
+      constexpr int s = decltype(sc)::value, pass = s / PASS, at = s % PASS;
+      constexpr int bi = pass * H + at % H, bj = at / H;
       acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[bj], fa[bi], acc[bi][bj], 0, 0, 0);
       if constexpr (s < H) fa[H + s] = frag<true, TILE>(cu, rowA + 16 * (H + s), lane);
       if constexpr (s >= PASS && s < PASS + H) fa[s - PASS] = frag<true, TILE>(nx, rowA + 16 * (s - PASS), lane);
-      if constexpr (pass == 1 && sp % H == H - 1) fb[bj] = frag<true, TILE>(nb, rowB + 16 * bj, lane);
-      if constexpr (s >= H && (s - H) % LSS == 0) {
+      if constexpr (pass == 1 && at % H == H - 1) fb[bj] = frag<true, TILE>(nb, rowB + 16 * bj, lane);
+      if constexpr (s >= H && (s - H) % LSS == 0 && (s - H) / LSS < LPS) {
         constexpr int part = (s - H) / LSS;
-        if constexpr (part < LP) load_p(dyd, kt + 3, part);
-        else if constexpr (part < LP + LR) load_r(cod, kt + 4, part - LP);
-        else if constexpr (part < LPS) load_s(scd, kt + 4);
+        if constexpr (part < LP) load_p((kt + 3) & 3, std::integral_constant<int, part>{});
+        else load_x(kt & 3, std::integral_constant<int, part - LP>{});
       }
-      // unpacking: the codes and scale early in the first pass, the rest later in it
-      if constexpr (s >= H && s < H + LR) fetch(kt + 2, s - H);
-      if constexpr (s == H + LR) fetch_scale(kt + 2);
-      constexpr int U0 = PASS / 2, US = (PASS - U0) / (2 * LR);
-      if constexpr (s >= U0 && (s - U0) % US == 0 && (s - U0) / US < 2 * LR) unpack(kt + 2, (s - U0) / US);
+      // unpacking: codes and scales early, one conversion per slot from a quarter of the step on
+      if constexpr (s >= H && s < H + Q) fetch((kt + 2) & 3, std::integral_constant<int, s - H>{});
+      constexpr int U0 = SLOTS / 4;
+      if constexpr (s >= U0 && s < U0 + 4 * Q) unpack(kt & 1, std::integral_constant<int, s - U0>{});
       __builtin_amdgcn_sched_barrier(0);
     });
   }
@@ -294,7 +275,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_wgrad(muon_act8_wgrad_t op, Wg
   const int64_t rows = min(p.split_rows, op.tokens - t0);
   f32x4_t acc[G::NB][G::NB];
   zero_acc<G::NB>(acc);
-  product<TILE>(op, i0, j0, t0, static_cast<int>((rows + BK - 1) / BK), smem, acc, tid);
+  product<TILE>(op, i0, j0, t0, rows, smem, acc, tid);
   // The sums leave through LDS, TILE / 2 rows (two waves) at a time, whole rows
   // of the tile side by side: 16-byte pieces, piece c of row r at c ^ (r & 15) (the
   // 16 rows that one write instruction covers then fall on distinct banks).
@@ -373,18 +354,21 @@ WgradPlan wgrad_plan(const muon_act8_wgrad_t& op) {
   p.tile = op.n * op.k >= int64_t(256) * 256 * 128 && std::min(op.n, op.k) >= 256 ? 256 : 128;
   p.tiles_n = (op.n + p.tile - 1) / p.tile;
   p.tiles_k = (op.k + p.tile - 1) / p.tile;
-  const int64_t tiles = p.tiles_n * p.tiles_k, steps = (op.tokens + BK - 1) / BK;
-  // token ranges until the chip is full (a 256-tile block takes a CU, two of
-  // 128 share one), of 8 steps at least
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((p.tile == 256 ? 256 : 512) / tiles, steps / 8));
-  p.split_rows = std::max<int64_t>(1, (steps + want - 1) / want) * BK;
-  p.splits = (op.tokens + p.split_rows - 1) / p.split_rows;
   // the loads take 16 bytes at multiples of 16, rows that end on a dword, and
-  // 32-bit offsets within a step's 32 rows
-  constexpr int64_t kMaxLd = int64_t(1) << 25;
+  // 32-bit offsets
+  constexpr int64_t kMaxLd = int64_t(1) << 21;
   p.copy_dy = op.tokens > 0 && !(is_aligned(op.dy, 16) && op.ld_dy % 8 == 0 && op.ld_dy < kMaxLd && op.n % 2 == 0);
   p.copy_x = op.tokens > 0 && !(is_aligned(op.x8.codes, 16) && op.x8.ld_codes % 16 == 0 && op.x8.ld_codes < kMaxLd &&
                                 op.x8.ld_scales < kMaxLd && op.k % 4 == 0);
+  const int64_t tiles = p.tiles_n * p.tiles_k, steps = (op.tokens + BK - 1) / BK;
+  // token ranges until the chip is full (a 256-tile block takes a CU, two of 128
+  // share one), of 8 steps at least, and below 2^31 bytes
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((p.tile == 256 ? 256 : 512) / tiles, steps / 8));
+  const int64_t ld = std::max({(p.copy_dy ? up(op.n, 8) : op.ld_dy) * 2, p.copy_x ? up(op.k, 16) : op.x8.ld_codes,
+                               p.copy_x ? int64_t(1) : op.x8.ld_scales});
+  const int64_t most = (int64_t(1) << 31) / ld / BK - 1;
+  p.split_rows = std::max<int64_t>(1, std::min((steps + want - 1) / want, most)) * BK;
+  p.splits = (op.tokens + p.split_rows - 1) / p.split_rows;
   size_t off = 0;
   auto take = [&](int64_t bytes) {
     const size_t at = off;
