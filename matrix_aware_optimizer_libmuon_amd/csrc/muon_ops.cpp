@@ -267,7 +267,7 @@ int muon_act8_wgrad(const muon_act8_wgrad_t* op, void* workspace, size_t workspa
     if (int rc = l.run("weight gradient, aligned copies", [&](void* st) { return launch_wgrad_copy(in, p, ws, st); })) return rc;
   if (op->tokens > 0)
     if (int rc = l.run("weight gradient", [&](void* st) { return launch_wgrad(in, p, ws, st); })) return rc;
-  if (p.splits != 1)
+  if (p.splits != 1)     // several ranges, or no tokens
     return l.run("weight gradient, join", [&](void* st) { return launch_wgrad_join(in, p, ws, st); });
   return MUON_OK;
 }

@@ -37,7 +37,8 @@ int launch_rmsnorm_dgain(const float* partial, int64_t blocks, int64_t cols, flo
 struct WgradPlan {
   int tile;                   // 256 or 128
   int64_t tiles_n, tiles_k;   // output tiles
-  int64_t splits, split_rows; // token ranges of split_rows (the last one may be shorter)
+  int64_t whole;              // tiles (the first ones) that one block makes from all tokens
+  int64_t splits, split_rows; // token ranges of the others, of split_rows (the last may be shorter)
   bool copy_dy, copy_x;
   size_t partial_off, dy_off, x_off, s_off;
   size_t bytes;

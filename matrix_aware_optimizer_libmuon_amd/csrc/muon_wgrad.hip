@@ -64,8 +64,8 @@ struct Lds {
   static constexpr int TE = Geo<TILE>::TE;
   static constexpr int RE = TILE * BK;                   // bytes of codes of a step
   static constexpr int SE = 4 * 64 * 4;                  // a dword per wave and lane for the scales
-  static constexpr int B = 0;                            // unpacked x: 2 stages of bf16
-  static constexpr int P = B + 2 * TE * 2;               // dY: 4 stages of bf16
+  static constexpr int B = 0;                            // unpacked x: 3 stages of bf16
+  static constexpr int P = B + 3 * TE * 2;               // dY: 4 stages of bf16
   static constexpr int R = P + 4 * TE * 2;               // codes: 4 stages
   static constexpr int S = R + 4 * RE;                   // scales: 4 stages
   static constexpr int bytes = S + 4 * SE;
@@ -82,8 +82,13 @@ static_assert(Lds<256>::bytes <= 160 * 1024 && 2 * Lds<128>::bytes <= 160 * 1024
 // step kt + 1, codes and scales of kt + 2 have landed) and a barrier, and then
 //   multiplies dY[kt] and x[kt], whose first fragments were read in step kt - 1,
 //   loads dY of step kt + 3 and codes and scales of step kt + 4,
-//   unpacks x of step kt + 2, into the tile whose fragments were read before the
-//   barrier.
+//   unpacks x of step kt + 2, into the tile whose fragments were read in step
+//   kt - 2 and used in step kt - 1.
+// So before the barrier only the wave's writes of the unpacked x have to be done,
+// not its last fragment reads, which are used later: LDS finishes in order, and
+// 8 + 16 (TILE 128: 4 + 8) reads were issued after the last write.  (Waiting for
+// them all, with two stages of x, left the matrix units idle for the length of an
+// LDS read in each step.)
 // Loads past the last token give zeros and read nothing.
 //
 // At TILE 256 a SIMD has one wave, which issues an instruction every 4 cycles at
@@ -162,14 +167,14 @@ __device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0,
     sb[q] = *reinterpret_cast<const uint32_t*>(sb_at + st * L::SE + URP * q * SPR * 4);
   };
   u32x4 o;
-  auto unpack = [&](int st, auto part) __attribute__((always_inline)) {        // a quarter of a piece; st: kt & 1
+  auto unpack = [&](int st, auto part) __attribute__((always_inline)) {        // a quarter of a piece; st: the tile's place
     constexpr int q = decltype(part)::value / 4, i = decltype(part)::value % 4;
     const float scale = act8_scale(sb[q]);
     o[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[q][i >> 1], scale, (i & 1) != 0));
-    if constexpr (i == 3) *reinterpret_cast<u32x4*>(x_at[q] + st * (G::TE * 2)) = o;
+    if constexpr (i == 3) *reinterpret_cast<u32x4*>(x_at[q] + st) = o;
   };
   auto tile_p = [&](int st) { return reinterpret_cast<const uint16_t*>(smem + L::P + st * (G::TE * 2)); };
-  auto tile_b = [&](int st) { return reinterpret_cast<const uint16_t*>(smem + L::B + st * (G::TE * 2)); };
+  auto tile_b = [&](int st) { return reinterpret_cast<const uint16_t*>(smem + L::B + st); };
 
   // x8 of steps 0 .. 3 and dY of steps 0 .. 2, the share of the loop's step -1 last
   static_for<2>([&](auto k) { static_for<LR + 1>([&](auto part) { load_x(k, part); }); });
@@ -181,7 +186,7 @@ __device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0,
   vm_wait<LPS>();
   static_for<2>([&](auto k) {
     static_for<Q>([&](auto q) { fetch(k, q); });
-    static_for<4 * Q>([&](auto part) { unpack(k, part); });
+    static_for<4 * Q>([&](auto part) { unpack(k * (G::TE * 2), part); });
   });
   lds_barrier();
   bf16x8_t fa[NB], fb[NB];
@@ -190,12 +195,20 @@ __device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0,
 #pragma unroll
   for (int r = 0; r < NB; ++r) fb[r] = frag<true, TILE>(tile_b(0), rowB + 16 * r, lane);
 
+  // a wait that the compiler knows of: with reads pending on entry it would wait
+  // for all of them at the top of every step
+  __builtin_amdgcn_s_waitcnt(0xc07f);                     // lgkmcnt(0)
+  // LDS operations issued after the step's last write: fragments of the next step
+  constexpr int AFTER = 2 * (H + NB) < 15 ? 2 * (H + NB) : 15;
+  constexpr int CPS = TILE == 256 ? 1 : 4, U0 = PASS - 4 * Q / CPS;   // conversions of a slot, first slot of them
+  static_assert(U0 > H + Q, "after the codes");
+  int b0 = 0, b1 = G::TE * 2, b2 = 2 * G::TE * 2;         // places of x of steps kt, kt + 1, kt + 2
   for (int kt = 0; kt < steps; ++kt) {
     vm_wait<LPS>();
-    lds_barrier();
+    asm volatile("s_waitcnt lgkmcnt(%0)\n\ts_barrier" ::"n"(AFTER) : "memory");
     const uint16_t* cu = tile_p(kt & 3);
     const uint16_t* nx = tile_p((kt + 1) & 3);
-    const uint16_t* nb = tile_b((kt + 1) & 1);
+    const uint16_t* nb = tile_b(b1);
     static_for<SLOTS>([&](auto sc) __attribute__((always_inline)) {
       constexpr int s = decltype(sc)::value, pass = s / PASS, at = s % PASS;
       constexpr int bi = pass * H + at % H, bj = at / H;
@@ -208,12 +221,16 @@ __device__ __forceinline__ void product(const muon_act8_wgrad_t& op, int64_t i0,
         if constexpr (part < LP) load_p((kt + 3) & 3, std::integral_constant<int, part>{});
         else load_x(kt & 3, std::integral_constant<int, part - LP>{});
       }
-      // unpacking: codes and scales early, one conversion per slot from a quarter of the step on
+      // unpacking: codes and scales early, the conversions in the slots before the second pass
       if constexpr (s >= H && s < H + Q) fetch((kt + 2) & 3, std::integral_constant<int, s - H>{});
-      constexpr int U0 = SLOTS / 4;
-      if constexpr (s >= U0 && s < U0 + 4 * Q) unpack(kt & 1, std::integral_constant<int, s - U0>{});
+      if constexpr (s >= U0 && s < PASS)
+        static_for<CPS>([&](auto k) { unpack(b2, std::integral_constant<int, (s - U0) * CPS + decltype(k)::value>{}); });
       __builtin_amdgcn_sched_barrier(0);
     });
+    const int b = b0;
+    b0 = b1;
+    b1 = b2;
+    b2 = b;
   }
   vm_wait<0>();
 }
@@ -259,20 +276,23 @@ __device__ __forceinline__ void put4(const muon_act8_wgrad_t& op, int64_t i, int
   }
 }
 
-// partial: [split][n][k rounded up to 4] where there are several token ranges.
-__host__ __device__ __forceinline__ int64_t partial_ld(int64_t k) { return (k + 3) / 4 * 4; }
-
 template <int TILE>
 __global__ __launch_bounds__(kGemmThreads) void k_wgrad(muon_act8_wgrad_t op, WgradPlan p, float* partial) {
   using G = Geo<TILE>;
   __shared__ __attribute__((aligned(16))) char smem[Lds<TILE>::bytes];
   const int tid = opaque_tid();
-  const int64_t unit = xcd_remap(blockIdx.x, gridDim.x), tiles = p.tiles_n * p.tiles_k;
-  const int64_t split = unit / tiles;
+  // first the tiles that are one block's whole, then the others, range by range
+  const bool whole = blockIdx.x < p.whole;
+  const int64_t units = whole ? p.whole : gridDim.x - p.whole;
+  const int64_t unit = xcd_remap(whole ? blockIdx.x : blockIdx.x - p.whole, units);
+  const int64_t rest = p.tiles_n * p.tiles_k - p.whole;
+  const int64_t split = whole ? 0 : unit / rest;
   int64_t ti, tj;
-  decode_full(unit - split * tiles, p.tiles_n, p.tiles_k, ti, tj);
+  decode_full(whole ? unit : p.whole + unit - split * rest, p.tiles_n, p.tiles_k, ti, tj);
   const int64_t i0 = ti * TILE, j0 = tj * TILE, t0 = split * p.split_rows;
-  const int64_t rows = min(p.split_rows, op.tokens - t0);
+  const int64_t rows = whole ? op.tokens : min(p.split_rows, op.tokens - t0);
+  const bool last = whole || p.splits == 1;
+  partial += unit * (TILE * TILE);
   f32x4_t acc[G::NB][G::NB];
   zero_acc<G::NB>(acc);
   product<TILE>(op, i0, j0, t0, rows, smem, acc, tid);
@@ -301,7 +321,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_wgrad(muon_act8_wgrad_t op, Wg
       const int64_t i = i0 + half * (TILE / 2) + r, j = j0 + 4 * c;
       if (i < op.n && j < op.k) {
         const f32x4_t v = *reinterpret_cast<const f32x4_t*>(smem + (r * PPR + (c ^ (r & 15))) * 16);
-        if (p.splits > 1) gst<f32x4_t>(partial + (split * op.n + i) * partial_ld(op.k) + j, v);
+        if (!last) gst<f32x4_t>(partial + (half * (TILE / 2) + r) * TILE + 4 * c, v);
         else if (op.dw_dtype == MUON_BF16) put4<uint16_t>(op, i, j, v);
         else put4<float>(op, i, j, v);
       }
@@ -309,14 +329,23 @@ __global__ __launch_bounds__(kGemmThreads) void k_wgrad(muon_act8_wgrad_t op, Wg
   }
 }
 
-// The token ranges' sums, added in order (no range: zero), 4 columns a thread.
-__global__ __launch_bounds__(256) void k_wgrad_join(muon_act8_wgrad_t op, int64_t splits, const float* partial) {
-  const int64_t ld = partial_ld(op.k), n4 = op.n * (ld / 4);
-  for (int64_t u = blockIdx.x * int64_t(256) + threadIdx.x; u < n4; u += int64_t(gridDim.x) * 256) {
+// The sums of the token ranges, added in order (no range: zero), 4 columns a
+// thread.  partial: [range][tile of the rest][TILE][TILE].
+template <int TILE>
+__global__ __launch_bounds__(256) void k_wgrad_join(muon_act8_wgrad_t op, WgradPlan p, const float* partial) {
+  constexpr int PPR = TILE / 4;
+  const int64_t rest = p.tiles_n * p.tiles_k - p.whole;
+  for (int64_t b = blockIdx.x; b < rest * (TILE * PPR / 256); b += gridDim.x) {   // 256 pieces of one tile
+    const int64_t tile = b / (TILE * PPR / 256);
+    const int u = static_cast<int>(b % (TILE * PPR / 256)) * 256 + threadIdx.x, r = u / PPR, c = u % PPR;
+    int64_t ti, tj;
+    decode_full(p.whole + tile, p.tiles_n, p.tiles_k, ti, tj);
+    const int64_t i = ti * TILE + r, j = tj * TILE + 4 * c;
+    if (i >= op.n || j >= op.k) continue;
     f32x4_t v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int64_t s = 0; s < splits; ++s) v += gld<f32x4_t>(partial + s * op.n * ld + 4 * u);
-    const int64_t i = u / (ld / 4), j = (u - i * (ld / 4)) * 4;
+    const float* at = partial + tile * (TILE * TILE) + r * TILE + 4 * c;
+#pragma unroll 8
+    for (int s = 0; s < static_cast<int>(p.splits); ++s) v += gld<f32x4_t>(at + s * rest * (TILE * TILE));
     if (op.dw_dtype == MUON_BF16) put4<uint16_t>(op, i, j, v);
     else put4<float>(op, i, j, v);
   }
@@ -348,34 +377,70 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
 
+namespace {
+
+// How a tile size would be dealt to the chip: `whole` tiles that one block makes
+// alone, in full rounds of the chip, and the rest cut into token ranges such that
+// they fill it too; and an estimate of the time, from measured figures.
+struct WgradShape {
+  int tile;
+  int64_t whole, split_steps;
+  double us;
+};
+
+WgradShape wgrad_shape(const muon_act8_wgrad_t& op, int tile, int64_t steps, int64_t most) {
+  const int64_t slots = tile == 256 ? 256 : 512;          // blocks that the chip holds
+  const double step_us = tile == 256 ? 0.80 : 0.42;       // a step, the chip full
+  const int64_t tiles = ((op.n + tile - 1) / tile) * ((op.k + tile - 1) / tile);
+  WgradShape best{tile, tiles, steps, 0.0};
+  const bool fits = steps <= most;
+  const int64_t rounds = tiles / slots, rest = tiles - rounds * slots;
+  best.us = fits ? (rounds + (rest > 0)) * (steps * step_us + 6.0) : 1e30;
+  if (steps == 0) return best;
+  const int64_t whole = fits ? rounds * slots : 0, cut = tiles - whole;
+  for (int64_t want = 2; want <= 64 && cut > 0; ++want) {
+    const int64_t each = (steps + want - 1) / want, ranges = (steps + each - 1) / each;
+    if (each < 4 && want > 2) break;
+    if (each > most) continue;
+    // the ranges' sums are written and read once at about 4 TB/s, and joined by one more launch
+    const double us = (whole / slots) * (steps * step_us + 6.0) + ((cut * ranges + slots - 1) / slots) * (each * step_us + 6.0) +
+                      2.0 * cut * ranges * tile * tile * 4 / 4e6 + 5.0;
+    if (us < best.us) best = {tile, whole, each, us};
+  }
+  if (best.us >= 1e30) best = {tile, 0, most, 1e29};      // more than 64 ranges: by the bound alone
+  return best;
+}
+
+}  // namespace
+
 WgradPlan wgrad_plan(const muon_act8_wgrad_t& op) {
   WgradPlan p{};
-  // 256 x 256 tiles where they fill the chip
-  p.tile = op.n * op.k >= int64_t(256) * 256 * 128 && std::min(op.n, op.k) >= 256 ? 256 : 128;
-  p.tiles_n = (op.n + p.tile - 1) / p.tile;
-  p.tiles_k = (op.k + p.tile - 1) / p.tile;
   // the loads take 16 bytes at multiples of 16, rows that end on a dword, and
   // 32-bit offsets
   constexpr int64_t kMaxLd = int64_t(1) << 21;
   p.copy_dy = op.tokens > 0 && !(is_aligned(op.dy, 16) && op.ld_dy % 8 == 0 && op.ld_dy < kMaxLd && op.n % 2 == 0);
   p.copy_x = op.tokens > 0 && !(is_aligned(op.x8.codes, 16) && op.x8.ld_codes % 16 == 0 && op.x8.ld_codes < kMaxLd &&
                                 op.x8.ld_scales < kMaxLd && op.k % 4 == 0);
-  const int64_t tiles = p.tiles_n * p.tiles_k, steps = (op.tokens + BK - 1) / BK;
-  // token ranges until the chip is full (a 256-tile block takes a CU, two of 128
-  // share one), of 8 steps at least, and below 2^31 bytes
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((p.tile == 256 ? 256 : 512) / tiles, steps / 8));
   const int64_t ld = std::max({(p.copy_dy ? up(op.n, 8) : op.ld_dy) * 2, p.copy_x ? up(op.k, 16) : op.x8.ld_codes,
                                p.copy_x ? int64_t(1) : op.x8.ld_scales});
-  const int64_t most = (int64_t(1) << 31) / ld / BK - 1;
-  p.split_rows = std::max<int64_t>(1, std::min((steps + want - 1) / want, most)) * BK;
-  p.splits = (op.tokens + p.split_rows - 1) / p.split_rows;
+  const int64_t most = (int64_t(1) << 31) / ld / BK - 1;   // steps of a range below 2^31 bytes
+  const int64_t steps = (op.tokens + BK - 1) / BK;
+  const WgradShape a = wgrad_shape(op, 256, steps, most), b = wgrad_shape(op, 128, steps, most);
+  const WgradShape& w = a.us <= b.us ? a : b;
+  p.tile = w.tile;
+  p.tiles_n = (op.n + w.tile - 1) / w.tile;
+  p.tiles_k = (op.k + w.tile - 1) / w.tile;
+  p.whole = w.whole;
+  p.split_rows = std::max<int64_t>(1, w.split_steps) * BK;
+  p.splits = p.whole == p.tiles_n * p.tiles_k ? 1 : (op.tokens + p.split_rows - 1) / p.split_rows;
+  if (op.tokens == 0) p.whole = p.splits = 0;              // k_wgrad_join writes the zeros
   size_t off = 0;
   auto take = [&](int64_t bytes) {
     const size_t at = off;
     off += static_cast<size_t>(up(bytes, 256));
     return at;
   };
-  if (p.splits > 1) p.partial_off = take(p.splits * op.n * partial_ld(op.k) * 4);
+  if (p.splits > 1) p.partial_off = take(p.splits * (p.tiles_n * p.tiles_k - p.whole) * p.tile * p.tile * 4);
   if (p.copy_dy) p.dy_off = take(op.tokens * up(op.n, 8) * 2);
   if (p.copy_x) {
     p.x_off = take(op.tokens * up(op.k, 16));
@@ -411,8 +476,9 @@ int launch_wgrad_copy(muon_act8_wgrad_t& op, const WgradPlan& p, char* ws, void*
 }
 
 int launch_wgrad(const muon_act8_wgrad_t& op, const WgradPlan& p, char* ws, void* stream) {
-  const dim3 grid(static_cast<unsigned>(p.splits * p.tiles_n * p.tiles_k));
-  float* partial = p.splits > 1 ? reinterpret_cast<float*>(ws + p.partial_off) : nullptr;
+  const int64_t rest = p.tiles_n * p.tiles_k - p.whole;
+  const dim3 grid(static_cast<unsigned>(p.whole + rest * p.splits));
+  float* partial = reinterpret_cast<float*>(ws + p.partial_off);   // not used where there is one range
   if (p.tile == 256)
     hipLaunchKernelGGL(k_wgrad<256>, grid, dim3(kGemmThreads), 0, static_cast<hipStream_t>(stream), op, p, partial);
   else
@@ -421,9 +487,13 @@ int launch_wgrad(const muon_act8_wgrad_t& op, const WgradPlan& p, char* ws, void
 }
 
 int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const char* ws, void* stream) {
-  const int64_t blocks = std::min<int64_t>((op.n * (partial_ld(op.k) / 4) + 255) / 256, 8192);
-  hipLaunchKernelGGL(k_wgrad_join, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream),
-                     op, p.splits, reinterpret_cast<const float*>(ws + p.partial_off));
+  const int64_t rest = p.tiles_n * p.tiles_k - p.whole;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rest * (p.tile * p.tile / 1024), int64_t(1) << 22)));
+  const float* partial = reinterpret_cast<const float*>(ws + p.partial_off);
+  if (p.tile == 256)
+    hipLaunchKernelGGL(k_wgrad_join<256>, grid, dim3(256), 0, static_cast<hipStream_t>(stream), op, p, partial);
+  else
+    hipLaunchKernelGGL(k_wgrad_join<128>, grid, dim3(256), 0, static_cast<hipStream_t>(stream), op, p, partial);
   return static_cast<int>(hipGetLastError());
 }
 
