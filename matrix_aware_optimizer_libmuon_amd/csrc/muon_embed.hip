@@ -8,13 +8,14 @@
 // the key `vocab` and end up past every row.
 //
 // Ids are as frequent as words: a few have thousands of tokens, most none.
-//   Rows of up to kRun tokens (and empty ones, which are written as zeros) go to
-//   k_rows, a wave or a block per 4 rows.
-//   Longer runs are cut where the sorted order passes a multiple of kRun:
-//   k_pieces sums each piece into the workspace, k_join adds a run's pieces in
-//   order.  A piece lies in one chunk of kRun places; a chunk can hold two of
-//   them, the end of one run and the beginning of another.
-// Up to kDirect tokens none of that is needed: each wave of k_rows finds its
+//   Rows of up to kRun tokens (and empty ones, which are written as zeros) are a
+//   wave's or a block's, 4 rows each.
+//   Longer runs are cut where the sorted order passes a multiple of kRun: each
+//   piece is summed into the workspace (by blocks of the same launch, k_sums), and
+//   k_join adds a run's pieces in order.  A piece lies in one chunk of kRun
+//   places; a chunk can hold two of them, the end of one run and the beginning of
+//   another.
+// Up to kDirect tokens none of that is needed: each wave of k_direct finds its
 // rows' tokens by comparing all ids.
 //
 // Bound by memory: dy is read once, the table's gradient written once.
@@ -34,7 +35,7 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRowThreads = 256;
 constexpr int kRun = 64;                            // longest run that one wave adds up
 constexpr int kDirect = 256;                        // tokens that are not sorted
-constexpr int kRowsEach = 4;                        // rows of a wave (or block) of k_rows
+constexpr int kRowsEach = 4;                        // rows of a wave (or block)
 
 __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_t i) {
   return id_bytes == 8 ? gld<int64_t>(static_cast<const char*>(ids) + 8 * i)
@@ -247,61 +248,48 @@ __device__ __forceinline__ void put_row(const muon_embed_grad_t& op, int64_t row
   Vec8<T>::store(out, n, s);
 }
 
-// kRowsEach rows for each group of TPR threads (a wave, or the block).
-template <class S, class T, int TPR, bool DIRECT>
-__global__ __launch_bounds__(kRowThreads) void k_rows(muon_embed_grad_t op, const uint32_t* start, const uint32_t* toks) {
+// Few tokens: kRowsEach rows for each group of TPR threads (a wave, or the
+// block), whose tokens are found by comparing all ids.
+template <class S, class T, int TPR>
+__global__ __launch_bounds__(kRowThreads) void k_direct(muon_embed_grad_t op) {
   const int lane = threadIdx.x & 63;
   // uniform over a wave: taken from its first lane
   const int group = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / TPR);
   const int t = static_cast<int>(threadIdx.x) % TPR;
   const int cols = static_cast<int>(op.cols);
-  for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kRowThreads / TPR) + group) * kRowsEach; row0 < op.vocab;
-       row0 += static_cast<int64_t>(gridDim.x) * (kRowThreads / TPR) * kRowsEach) {
-    if constexpr (DIRECT) {
-      uint32_t key[kDirect / 64];
+  uint32_t key[kDirect / 64];
 #pragma unroll
-      for (int q = 0; q < kDirect / 64; ++q) {
-        const int64_t i = q * 64 + lane;
-        key[q] = i < op.tokens ? key_of(op.ids, op.id_bytes, op.vocab, i) : 0xffffffffu;
-      }
-      for (int r = 0; r < kRowsEach && row0 + r < op.vocab; ++r)
-        for (int c0 = 0; c0 < cols; c0 += TPR * 8) {
-          const int c = c0 + t * 8;
-          float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < kDirect / 64; ++q)
-            for (uint64_t m = __ballot(key[q] == static_cast<uint32_t>(row0 + r)); m; m &= m - 1) {
-              Vec8<S> v;
-              load8(v, static_cast<const S*>(op.dy) + (q * 64 + __builtin_ctzll(m)) * op.ld_dy + c, cols - c);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) s[j] += v.get(j);
-            }
-          put_row<T>(op, row0 + r, c, s);
-        }
-    } else {
-      uint32_t first[kRowsEach], held[kRowsEach];
-      int len[kRowsEach];
-#pragma unroll
-      for (int r = 0; r < kRowsEach; ++r) {
-        const bool in = row0 + r < op.vocab;
-        first[r] = in ? gld<uint32_t>(start + row0 + r) : 0u;
-        len[r] = in ? static_cast<int>(gld<uint32_t>(start + row0 + r + 1) - first[r]) : kRun + 1;
-      }
-#pragma unroll
-      for (int r = 0; r < kRowsEach; ++r)
-        held[r] = len[r] <= kRun && lane < len[r] ? gld<uint32_t>(toks + first[r] + lane) : 0u;
-#pragma unroll
-      for (int r = 0; r < kRowsEach; ++r) {
-        if (len[r] > kRun) continue;                // k_join's, or past the table
-        for (int c0 = 0; c0 < cols; c0 += TPR * 8) {
-          float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          add_rows<S>(op, held[r], 0, len[r], c0 + t * 8, s);
-          put_row<T>(op, row0 + r, c0 + t * 8, s);
-        }
-      }
-    }
+  for (int q = 0; q < kDirect / 64; ++q) {
+    const int64_t i = q * 64 + lane;
+    key[q] = i < op.tokens ? key_of(op.ids, op.id_bytes, op.vocab, i) : 0xffffffffu;
   }
+  for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kRowThreads / TPR) + group) * kRowsEach; row0 < op.vocab;
+       row0 += static_cast<int64_t>(gridDim.x) * (kRowThreads / TPR) * kRowsEach)
+    for (int r = 0; r < kRowsEach && row0 + r < op.vocab; ++r)
+      for (int c0 = 0; c0 < cols; c0 += TPR * 8) {
+        const int c = c0 + t * 8;
+        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < kDirect / 64; ++q)
+          for (uint64_t m = __ballot(key[q] == static_cast<uint32_t>(row0 + r)); m; m &= m - 1) {
+            Vec8<S> v;
+            load8(v, static_cast<const S*>(op.dy) + (q * 64 + __builtin_ctzll(m)) * op.ld_dy + c, cols - c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] += v.get(j);
+          }
+        put_row<T>(op, row0 + r, c, s);
+      }
 }
+
+// What the sums of sorted tokens work on.
+struct Sorted {
+  const uint32_t* keys;
+  const uint32_t* toks;
+  const uint32_t* start;
+  float* pieces;                // [chunk][left, right][cols]
+  int64_t chunks;
+  unsigned piece_blocks;        // the launch's first blocks: pieces, the others: rows
+};
 
 // The long runs that touch chunk `chunk` of the sorted order, one place per
 // lane: `left`, lanes of a run that began in an earlier chunk, and `right`, lanes
@@ -310,15 +298,14 @@ struct Chunk {
   uint64_t left, right;
   uint32_t key, begin, end;     // of this lane's run
 };
-__device__ __forceinline__ Chunk chunk_runs(const uint32_t* keys, const uint32_t* start, int64_t tokens, int64_t vocab,
-                                            int64_t chunk, int lane) {
+__device__ __forceinline__ Chunk chunk_runs(const Sorted& a, int64_t tokens, int64_t vocab, int64_t chunk, int lane) {
   const int64_t i = chunk * kRun + lane;
   Chunk c;
-  c.key = i < tokens ? gld<uint32_t>(keys + i) : static_cast<uint32_t>(vocab);
+  c.key = i < tokens ? gld<uint32_t>(a.keys + i) : static_cast<uint32_t>(vocab);
   c.begin = c.end = 0;
   if (c.key < vocab) {
-    c.begin = gld<uint32_t>(start + c.key);
-    c.end = gld<uint32_t>(start + c.key + 1);
+    c.begin = gld<uint32_t>(a.start + c.key);
+    c.end = gld<uint32_t>(a.start + c.key + 1);
   }
   const bool is_long = c.end - c.begin > kRun;
   c.left = __ballot(is_long && c.begin < chunk * kRun);
@@ -326,43 +313,84 @@ __device__ __forceinline__ Chunk chunk_runs(const uint32_t* keys, const uint32_t
   return c;
 }
 
-// Sums of the pieces of each chunk, columns of a wave: 512 from
-// (4 blockIdx.y + wave) * 512.  pieces: [chunk][left, right][cols].
+// Sums of the pieces of one chunk, the wave's 512 columns from c - 8 lane.
 template <class S>
-__global__ __launch_bounds__(kRowThreads) void k_pieces(muon_embed_grad_t op, int64_t chunks, const uint32_t* keys,
-                                                        const uint32_t* toks, const uint32_t* start, float* pieces) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void sum_pieces(const muon_embed_grad_t& op, const Sorted& a, int64_t chunk, int c, int lane) {
   const int cols = static_cast<int>(op.cols);
-  const int c = (static_cast<int>(blockIdx.y) * 4 + (threadIdx.x >> 6)) * 512 + lane * 8;
-  if (c - lane * 8 >= cols) return;
-  for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-    const Chunk r = chunk_runs(keys, start, op.tokens, op.vocab, chunk, lane);
-    if (!(r.left | r.right)) continue;
-    const int64_t i = chunk * kRun + lane;
-    const uint32_t held = i < op.tokens ? gld<uint32_t>(toks + i) : 0u;
+  const Chunk r = chunk_runs(a, op.tokens, op.vocab, chunk, lane);
+  if (!(r.left | r.right)) return;
+  const int64_t i = chunk * kRun + lane;
+  const uint32_t held = i < op.tokens ? gld<uint32_t>(a.toks + i) : 0u;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const uint64_t m = side ? r.right : r.left;
-      if (!m) continue;
+  for (int side = 0; side < 2; ++side) {
+    const uint64_t m = side ? r.right : r.left;
+    if (!m) continue;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    add_rows<S>(op, held, __builtin_ctzll(m), __popcll(m), c, s);
+    Vec8<float>::store(a.pieces + (chunk * 2 + side) * cols + c, cols - c, s);
+  }
+}
+
+// Rows row0 .. + kRowsEach - 1 (those inside the table, without a long run), by
+// the TPR threads of a group, t of them this one.
+template <class S, class T, int TPR>
+__device__ __forceinline__ void sum_rows(const muon_embed_grad_t& op, const Sorted& a, int64_t row0, int t, int lane) {
+  uint32_t first[kRowsEach], held[kRowsEach];
+  int len[kRowsEach];
+#pragma unroll
+  for (int r = 0; r < kRowsEach; ++r) {
+    const bool in = row0 + r < op.vocab;
+    first[r] = in ? gld<uint32_t>(a.start + row0 + r) : 0u;
+    len[r] = in ? static_cast<int>(gld<uint32_t>(a.start + row0 + r + 1) - first[r]) : kRun + 1;
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsEach; ++r)
+    held[r] = len[r] <= kRun && lane < len[r] ? gld<uint32_t>(a.toks + first[r] + lane) : 0u;
+#pragma unroll
+  for (int r = 0; r < kRowsEach; ++r) {
+    if (len[r] > kRun) continue;                  // k_join's, or past the table
+    for (int c0 = 0; c0 < static_cast<int>(op.cols); c0 += TPR * 8) {
       float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      add_rows<S>(op, held, __builtin_ctzll(m), __popcll(m), c, s);
-      Vec8<float>::store(pieces + (chunk * 2 + side) * cols + c, cols - c, s);
+      add_rows<S>(op, held[r], 0, len[r], c0 + t * 8, s);
+      put_row<T>(op, row0 + r, c0 + t * 8, s);
     }
   }
 }
 
+// The pieces of the long runs (a wave per chunk and 512 columns) and, in the
+// blocks behind them, the other rows.
+template <class S, class T, int TPR>
+__global__ __launch_bounds__(kRowThreads) void k_sums(muon_embed_grad_t op, Sorted a) {
+  const int lane = threadIdx.x & 63;
+  // uniform over a wave: taken from its first lane
+  const int w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  if (blockIdx.x < a.piece_blocks) {
+    const int per = static_cast<int>((op.cols + 511) / 512);   // waves of a chunk
+    const int64_t n = a.chunks * per;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + w; u < n; u += static_cast<int64_t>(a.piece_blocks) * 4) {
+      const int64_t chunk = u / per;
+      sum_pieces<S>(op, a, chunk, static_cast<int>(u - chunk * per) * 512 + lane * 8, lane);
+    }
+    return;
+  }
+  constexpr int GPB = kRowThreads / TPR;
+  const int64_t step = static_cast<int64_t>(gridDim.x - a.piece_blocks) * GPB * kRowsEach;
+  for (int64_t row0 = (static_cast<int64_t>(blockIdx.x - a.piece_blocks) * GPB + (GPB > 1 ? w : 0)) * kRowsEach; row0 < op.vocab;
+       row0 += step)
+    sum_rows<S, T, TPR>(op, a, row0, static_cast<int>(threadIdx.x) % TPR, lane);
+}
+
 // The run that begins in a chunk: its pieces, 512 columns from 512 blockIdx.y.
 // The waves take consecutive shares of them, which are added in order.
-constexpr int kJoinWaves = 16;
+constexpr int kJoinWaves = 4;
 template <class T>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, int64_t chunks, const uint32_t* keys,
-                                                          const uint32_t* start, const float* pieces) {
+__global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, Sorted a) {
   __shared__ float red[kJoinWaves][512];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int cols = static_cast<int>(op.cols);
   const int c = static_cast<int>(blockIdx.y) * 512 + lane * 8;
-  for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-    const Chunk r = chunk_runs(keys, start, op.tokens, op.vocab, chunk, lane);
+  for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    const Chunk r = chunk_runs(a, op.tokens, op.vocab, chunk, lane);
     if (!r.right) continue;                          // the whole block
     const int src = __builtin_ctzll(r.right);
     const int64_t row = static_cast<uint32_t>(__builtin_amdgcn_readlane(r.key, src));
@@ -370,10 +398,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, 
     const int n = static_cast<int>(last - chunk + 1), per = (n + kJoinWaves - 1) / kJoinWaves;
     const int end = min((w + 1) * per, n);
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
     for (int k = w * per; k < end; ++k) {
       Vec8<float> v;
-      load8(v, pieces + ((chunk + k) * 2 + (k == 0)) * cols + c, cols - c);
+      load8(v, a.pieces + ((chunk + k) * 2 + (k == 0)) * cols + c, cols - c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] += v.get(j);
     }
@@ -475,37 +503,47 @@ int launch_embed_starts(const muon_embed_grad_t& op, const EmbedSortPlan& p, cha
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_embed_pieces(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
-  const dim3 grid(static_cast<unsigned>(std::min(p.chunks, kMaxGrid)), static_cast<unsigned>((op.cols + 2047) / 2048));
-  return by_types(op.dy_dtype, op.table_dtype, [&](auto s, auto) {
-    hipLaunchKernelGGL((k_pieces<decltype(s)>), grid, dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), op,
-                       p.chunks, p.keys(ws), p.toks(ws), p.starts(ws), p.pieces(ws));
+namespace {
+Sorted sorted(const EmbedSortPlan& p, char* ws) {
+  Sorted a;
+  a.keys = p.keys(ws);
+  a.toks = p.toks(ws);
+  a.start = p.starts(ws);
+  a.pieces = p.pieces(ws);
+  a.chunks = p.chunks;
+  a.piece_blocks = 0;
+  return a;
+}
+}  // namespace
+
+int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
+  const bool direct = p.passes == 0, wide = op.cols > 512;
+  const int64_t per_block = (wide ? 1 : 4) * kRowsEach;
+  const int64_t row_blocks = std::min((op.vocab + per_block - 1) / per_block, kMaxGrid / 2);
+  return by_types(op.dy_dtype, op.table_dtype, [&](auto s, auto t) {
+    using S = decltype(s);
+    using T = decltype(t);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (direct) {
+      const dim3 grid(static_cast<unsigned>(row_blocks));
+      if (wide) hipLaunchKernelGGL((k_direct<S, T, 256>), grid, dim3(kRowThreads), 0, st, op);
+      else hipLaunchKernelGGL((k_direct<S, T, 64>), grid, dim3(kRowThreads), 0, st, op);
+    } else {
+      Sorted a = sorted(p, ws);
+      a.piece_blocks = static_cast<unsigned>(std::min((p.chunks * ((op.cols + 511) / 512) + 3) / 4, kMaxGrid / 2));
+      const dim3 grid(a.piece_blocks + static_cast<unsigned>(row_blocks));
+      if (wide) hipLaunchKernelGGL((k_sums<S, T, 256>), grid, dim3(kRowThreads), 0, st, op, a);
+      else hipLaunchKernelGGL((k_sums<S, T, 64>), grid, dim3(kRowThreads), 0, st, op, a);
+    }
     return static_cast<int>(hipGetLastError());
   });
 }
 
-int launch_embed_rows(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
-  const bool direct = op.tokens <= kDirect, wide = op.cols > 512;
-  const int64_t per_block = (wide ? 1 : 4) * kRowsEach, blocks = (op.vocab + per_block - 1) / per_block;
-  const dim3 grid(static_cast<unsigned>(std::min(blocks, kMaxGrid)));
-  return by_types(op.dy_dtype, op.table_dtype, [&](auto s, auto t) {
-    using S = decltype(s);
-    using T = decltype(t);
-    auto go = [&](auto k) {
-      hipLaunchKernelGGL(k, grid, dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), op,
-                         direct ? nullptr : p.starts(ws), direct ? nullptr : p.toks(ws));
-      return static_cast<int>(hipGetLastError());
-    };
-    if (direct) return wide ? go(k_rows<S, T, 256, true>) : go(k_rows<S, T, 64, true>);
-    return wide ? go(k_rows<S, T, 256, false>) : go(k_rows<S, T, 64, false>);
-  });
-}
-
 int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
-  const dim3 grid(static_cast<unsigned>(std::min(p.chunks, kMaxGrid / 4)), static_cast<unsigned>((op.cols + 511) / 512));
+  const dim3 grid(static_cast<unsigned>(std::min(p.chunks, kMaxGrid)), static_cast<unsigned>((op.cols + 511) / 512));
   return by_types(op.dy_dtype, op.table_dtype, [&](auto, auto t) {
     hipLaunchKernelGGL((k_join<decltype(t)>), grid, dim3(64 * kJoinWaves), 0, static_cast<hipStream_t>(stream), op,
-                       p.chunks, p.keys(ws), p.starts(ws), p.pieces(ws));
+                       sorted(p, ws));
     return static_cast<int>(hipGetLastError());
   });
 }

@@ -329,6 +329,20 @@ def test_wgrad_is_exact_on_integers(tokens, n, k, layout):
     assert got.data_ptr() == out.data_ptr() and np.array_equal(np64(got), np64(base) + want * np64(gain))
 
 
+@pytest.mark.parametrize("tokens,n,k", [(260, 4352, 4100), (1000, 4100, 4352), (33, 5000, 4099), (640, 2304, 4608)])
+def test_wgrad_of_large_tiles_is_exact_on_integers(tokens, n, k):
+    """Sizes that 256 x 256 tiles serve, more of them than the chip holds at once: the last ones in token ranges."""
+    dy, x = int_case(tokens, n, k)
+    want = (dy.to(DEV).double().t().contiguous() @ x.to(DEV).double())
+    x8 = muon.act8_pack(x.to(DEV))
+    assert torch.equal(muon.act8_wgrad(dy.to(DEV), x8).double(), want)
+    gain = torch.exp2(torch.randint(-1, 2, (k,), generator=gen(5)).float()).to(DEV)
+    out = torch.ones(n, k + 3, device=DEV)[:, 1:1 + k]
+    muon.act8_wgrad(dy.to(DEV), x8, col_gain=gain, out=out, accumulate=True)
+    assert torch.equal(out.double(), 1 + want * gain)
+    assert torch.equal(muon.act8_wgrad(dy.to(DEV), x8, dtype=torch.bfloat16), want.float().bfloat16())
+
+
 @pytest.mark.parametrize("tokens,n,k", [(700, 200, 300), (64, 1024, 96), (3001, 80, 1536)])
 def test_wgrad_random(tokens, n, k):
     dy, x8 = randn(1, tokens, n, dtype=torch.bfloat16), muon.act8_pack((randn(2, tokens, k) * torch.exp2(4 * randn(3, tokens, 1))).to(DEV))
