@@ -9,7 +9,8 @@
 //
 // Ids are as frequent as words: a few have thousands of tokens, most none.
 //   Rows of up to kRun tokens (and empty ones, which are written as zeros) are a
-//   wave's or a block's, 4 rows each.
+//   wave's or a block's, one each (4 or 8 each were 4 and 8 % slower: too few
+//   independent loads).
 //   Longer runs are cut where the sorted order passes a multiple of kRun: each
 //   piece is summed into the workspace (by blocks of the same launch, k_sums), and
 //   k_join adds a run's pieces in order.  A piece lies in one chunk of kRun
@@ -35,7 +36,7 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRowThreads = 256;
 constexpr int kRun = 64;                            // longest run that one wave adds up
 constexpr int kDirect = 256;                        // tokens that are not sorted
-constexpr int kRowsEach = 4;                        // rows of a wave (or block)
+constexpr int kRowsEach = 4;                        // rows of a wave (or block) of k_direct
 
 __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_t i) {
   return id_bytes == 8 ? gld<int64_t>(static_cast<const char*>(ids) + 8 * i)
@@ -331,29 +332,31 @@ __device__ __forceinline__ void sum_pieces(const muon_embed_grad_t& op, const So
   }
 }
 
-// Rows row0 .. + kRowsEach - 1 (those inside the table, without a long run), by
-// the TPR threads of a group, t of them this one.
+// One row without a long run, by the TPR threads of a group, t of them this one.
+// A row without tokens (most of them) is written in 16-byte pieces side by side,
+// past the caches (222 us with the stores of put_row, 198 side by side, 190 past
+// the caches: 32768 tokens into 32000 x 4096 in fp32).
 template <class S, class T, int TPR>
-__device__ __forceinline__ void sum_rows(const muon_embed_grad_t& op, const Sorted& a, int64_t row0, int t, int lane) {
-  uint32_t first[kRowsEach], held[kRowsEach];
-  int len[kRowsEach];
-#pragma unroll
-  for (int r = 0; r < kRowsEach; ++r) {
-    const bool in = row0 + r < op.vocab;
-    first[r] = in ? gld<uint32_t>(a.start + row0 + r) : 0u;
-    len[r] = in ? static_cast<int>(gld<uint32_t>(a.start + row0 + r + 1) - first[r]) : kRun + 1;
+__device__ __forceinline__ void sum_row(const muon_embed_grad_t& op, const Sorted& a, int64_t row, int t, int lane) {
+  const int cols = static_cast<int>(op.cols);
+  const uint32_t first = gld<uint32_t>(a.start + row);
+  const int len = static_cast<int>(gld<uint32_t>(a.start + row + 1) - first);
+  if (len > kRun) return;                         // k_join's
+  if (len == 0) {
+    if (op.accumulate) return;
+    constexpr int E = 16 / sizeof(T);
+    T* out = static_cast<T*>(op.dtable) + row * op.ld_dtable;
+    int c = t * E;
+    for (; c + E <= cols; c += TPR * E)
+      __builtin_nontemporal_store(u32x4_a2{0, 0, 0, 0}, (__attribute__((address_space(1))) u32x4_a2*)(out + c));
+    for (int e = c; e < min(c + E, cols); ++e) gst<T>(out + e, T(0));
+    return;
   }
-#pragma unroll
-  for (int r = 0; r < kRowsEach; ++r)
-    held[r] = len[r] <= kRun && lane < len[r] ? gld<uint32_t>(a.toks + first[r] + lane) : 0u;
-#pragma unroll
-  for (int r = 0; r < kRowsEach; ++r) {
-    if (len[r] > kRun) continue;                  // k_join's, or past the table
-    for (int c0 = 0; c0 < static_cast<int>(op.cols); c0 += TPR * 8) {
-      float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      add_rows<S>(op, held[r], 0, len[r], c0 + t * 8, s);
-      put_row<T>(op, row0 + r, c0 + t * 8, s);
-    }
+  const uint32_t held = lane < len ? gld<uint32_t>(a.toks + first + lane) : 0u;
+  for (int c0 = 0; c0 < cols; c0 += TPR * 8) {
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    add_rows<S>(op, held, 0, len, c0 + t * 8, s);
+    put_row<T>(op, row, c0 + t * 8, s);
   }
 }
 
@@ -374,10 +377,9 @@ __global__ __launch_bounds__(kRowThreads) void k_sums(muon_embed_grad_t op, Sort
     return;
   }
   constexpr int GPB = kRowThreads / TPR;
-  const int64_t step = static_cast<int64_t>(gridDim.x - a.piece_blocks) * GPB * kRowsEach;
-  for (int64_t row0 = (static_cast<int64_t>(blockIdx.x - a.piece_blocks) * GPB + (GPB > 1 ? w : 0)) * kRowsEach; row0 < op.vocab;
-       row0 += step)
-    sum_rows<S, T, TPR>(op, a, row0, static_cast<int>(threadIdx.x) % TPR, lane);
+  const int64_t step = static_cast<int64_t>(gridDim.x - a.piece_blocks) * GPB;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x - a.piece_blocks) * GPB + (GPB > 1 ? w : 0); row < op.vocab; row += step)
+    sum_row<S, T, TPR>(op, a, row, static_cast<int>(threadIdx.x) % TPR, lane);
 }
 
 // The run that begins in a chunk: its pieces, 512 columns from 512 blockIdx.y.
@@ -518,7 +520,7 @@ Sorted sorted(const EmbedSortPlan& p, char* ws) {
 
 int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
   const bool direct = p.passes == 0, wide = op.cols > 512;
-  const int64_t per_block = (wide ? 1 : 4) * kRowsEach;
+  const int64_t per_block = (wide ? 1 : 4) * (direct ? kRowsEach : 1);
   const int64_t row_blocks = std::min((op.vocab + per_block - 1) / per_block, kMaxGrid / 2);
   return by_types(op.dy_dtype, op.table_dtype, [&](auto s, auto t) {
     using S = decltype(s);

@@ -15,7 +15,7 @@ namespace {
 // Rows per block: 4 waves with a row each, or the whole block on one.
 template <int RT>
 struct Rows {
-  static constexpr int threads = RT < 256 ? 256 : RT;
+  static constexpr int threads = RT < 128 ? 256 : RT;
   static constexpr int per_block = threads / RT;
 };
 
@@ -198,21 +198,27 @@ __global__ __launch_bounds__(64 * kDgainWaves) void k_dgain(const float* partial
   }
 }
 
-// f.operator()<RT, VPL>() for the narrowest layout that holds a row: waves up
-// to 1024 columns, then blocks of 256, 512 and 1024 threads.
+// f(RT, VPL) for the layout of a row: one vector a thread up to 8192 columns
+// (two a thread, with half the threads, need twice the registers: 115 us instead
+// of 90 for the backward pass of 16384 x 4096 bf16).
 template <class F>
 int by_width(int64_t cols, F&& f) {
   if (cols <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  if (cols <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (cols <= 1024) return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
   if (cols <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  if (cols <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (cols <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  if (cols <= 4096) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
+  if (cols <= 8192) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
   return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
 }
 static_assert(MUON_NORM_MAX_COLS == 1024 * 2 * 8, "widest layout");
 
 // threads of a grid stay below 2^32
 constexpr int64_t kMaxGrid = int64_t(1) << 21;
+// Threads of the backward pass, all resident at once (half as many: 109 us, one
+// and a half times: 103, this: 88 for 16384 x 4096 bf16); and 4 rows to a wave or
+// block at least, or the partial sums of dgain cost as much as the rows (2048 x 768
+// bf16: 15.4 us with one row, 11.5 with 4, 14.1 with 8).
+constexpr int64_t kGradThreads = 1024 * 256;
 
 }  // namespace
 
@@ -231,8 +237,9 @@ int launch_rmsnorm(const muon_rmsnorm_t& op, void* stream) {
 
 int64_t rmsnorm_grad_blocks(int64_t rows, int64_t cols) {
   return by_width(cols, [&](auto rt, auto) {
-    const int64_t need = (rows + Rows<decltype(rt)::value>::per_block - 1) / Rows<decltype(rt)::value>::per_block;
-    return static_cast<int>(need < 1024 ? need : 1024);
+    using R = Rows<decltype(rt)::value>;
+    const int64_t need = (rows + 4 * R::per_block - 1) / (4 * R::per_block), most = kGradThreads / R::threads;
+    return static_cast<int>(need < most ? need : most);
   });
 }
 
