@@ -190,6 +190,90 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_scatter(SortArgs a) {
   }
 }
 
+// The whole sort of up to kSmall tokens by one block (at 4000 tokens 2 us less
+// than the launches below, at 8000 4 to 5 us more): as k_embed_scatter, the
+// tokens in registers, each wave's share side by side, and moved through LDS.
+constexpr int kSmall = 4 * kSortThreads;
+__global__ __launch_bounds__(kSortThreads) void k_embed_sort(SortArgs a, int passes) {
+  constexpr int E = kSmall / kSortThreads;          // tokens of a thread at most
+  __shared__ uint32_t wcnt[kSortWaves][kDigits];
+  __shared__ uint32_t wsum[kSortWaves];
+  __shared__ uint32_t skey[kSmall], stok[kSmall];
+  const int t = static_cast<int>(threadIdx.x), lane = t & 63, w = t >> 6;
+  const int n = static_cast<int>(a.tokens), each = (n + kSortThreads - 1) / kSortThreads;
+  const int base = w * 64 * each + lane;            // + 64 e: this thread's e-th place
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = kDigitBits * pass;
+    for (int i = t; i < kSortWaves * kDigits; i += kSortThreads) (&wcnt[0][0])[i] = 0;
+    uint32_t key[E], tok[E], rank[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = base + 64 * e;
+      key[e] = tok[e] = rank[e] = 0;
+      if (e < each && i < n) {
+        key[e] = pass ? skey[i] : key_of(a.ids, a.id_bytes, a.vocab, i);
+        tok[e] = pass ? stok[i] : static_cast<uint32_t>(i);
+      }
+    }
+    __syncthreads();                                // the counts are clear, the places read
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (e >= each) break;
+      const bool valid = base + 64 * e < n;
+      const uint32_t d = (key[e] >> shift) & (kDigits - 1);
+      uint64_t same = __ballot(valid);
+#pragma unroll
+      for (int bit = 0; bit < kDigitBits; ++bit) {
+        const uint64_t on = __ballot((d >> bit) & 1);
+        same &= (d >> bit) & 1 ? on : ~on;
+      }
+      rank[e] = wcnt[w][d] + __popcll(same & ((uint64_t(1) << lane) - 1));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (valid && (same >> lane) == 1) wcnt[w][d] = rank[e] + 1;   // the digit's last lane
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    // first place of each digit, then of each wave's share of it
+    uint32_t sum = 0;
+    if (t < kDigits)
+#pragma unroll
+      for (int k = 0; k < kSortWaves; ++k) sum += wcnt[k][t];
+    uint32_t scan = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t v = __shfl_up(scan, o, 64);
+      scan += lane >= o ? v : 0u;
+    }
+    if (lane == 63) wsum[w] = scan;
+    __syncthreads();
+    if (t < kDigits) {
+      uint32_t run = scan - sum;
+      for (int k = 0; k < w; ++k) run += wsum[k];
+#pragma unroll
+      for (int k = 0; k < kSortWaves; ++k) {
+        const uint32_t c = wcnt[k][t];
+        wcnt[k][t] = run;
+        run += c;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < each && base + 64 * e < n) {
+        const uint32_t p = wcnt[w][(key[e] >> shift) & (kDigits - 1)] + rank[e];
+        skey[p] = key[e];
+        stok[p] = tok[e];
+      }
+    __syncthreads();
+  }
+  for (int i = t; i < n; i += kSortThreads) {
+    gst<uint32_t>(a.keys_out + i, skey[i]);
+    gst<uint32_t>(a.toks_out + i, stok[i]);
+  }
+}
+
 // start[v] = first place whose key is >= v, for v = 0 .. vocab.
 __global__ __launch_bounds__(kRowThreads) void k_starts(const uint32_t* keys, uint32_t tokens, uint32_t vocab, uint32_t* start) {
   const uint32_t v = blockIdx.x * kRowThreads + threadIdx.x;
@@ -271,13 +355,15 @@ __global__ __launch_bounds__(kRowThreads) void k_direct(muon_embed_grad_t op) {
         const int c = c0 + t * 8;
         float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < kDirect / 64; ++q)
-          for (uint64_t m = __ballot(key[q] == static_cast<uint32_t>(row0 + r)); m; m &= m - 1) {
-            Vec8<S> v;
-            load8(v, static_cast<const S*>(op.dy) + (q * 64 + __builtin_ctzll(m)) * op.ld_dy + c, cols - c);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] += v.get(j);
-          }
+        for (int q = 0; q < kDirect / 64; ++q) {
+          const bool mine = key[q] == static_cast<uint32_t>(row0 + r);
+          const uint64_t m = __ballot(mine);
+          if (!m) continue;
+          // the row's tokens, in order, to the first lanes; the others' go past them
+          const int n = __popcll(m), before = __popcll(m & ((uint64_t(1) << lane) - 1));
+          const int to = mine ? before : n + lane - before;
+          add_rows<S>(op, static_cast<uint32_t>(__builtin_amdgcn_ds_permute(4 * to, q * 64 + lane)), 0, n, c, s);
+        }
         put_row<T>(op, row0 + r, c, s);
       }
 }
@@ -456,6 +542,7 @@ EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols) {
   EmbedSortPlan p{};
   if (tokens <= kDirect) return p;
   for (int64_t top = vocab; top > 0; top >>= kDigitBits) ++p.passes;
+  p.one_block = tokens <= kSmall;
   // at most 256 blocks, whole steps each
   p.block_tokens = kSortThreads * ((tokens + kSortThreads * 256 - 1) / (kSortThreads * 256));
   p.blocks = (tokens + p.block_tokens - 1) / p.block_tokens;
@@ -484,6 +571,12 @@ int launch_embed(const muon_embed_t& op, void* stream) {
                        dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), op, blocks);
     return static_cast<int>(hipGetLastError());
   });
+}
+
+int launch_embed_sort(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
+  hipLaunchKernelGGL(k_embed_sort, dim3(1), dim3(kSortThreads), 0, static_cast<hipStream_t>(stream),
+                     sort_args(op, p, p.passes - 1, ws), p.passes);
+  return static_cast<int>(hipGetLastError());
 }
 
 int launch_embed_count(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream) {

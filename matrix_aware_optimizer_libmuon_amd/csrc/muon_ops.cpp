@@ -241,8 +241,22 @@ static bool wgrad_sizes_ok(const muon_act8_wgrad_t* op) {
          op->n <= MUON_MAX_DIM && op->k >= 1 && op->k <= MUON_MAX_DIM;
 }
 
+// The row strides of a single row are not read: the kernel gets ones that fit.
+static muon_act8_wgrad_t wgrad_strides(const muon_act8_wgrad_t* op) {
+  muon_act8_wgrad_t r = *op;
+  if (r.tokens <= 1) {
+    r.ld_dy = (r.n + 7) / 8 * 8;
+    r.x8.ld_codes = (r.k + 15) / 16 * 16;
+    r.x8.ld_scales = (r.k + 31) / 32;
+  }
+  return r;
+}
+
 size_t muon_act8_wgrad_workspace_bytes(const muon_act8_wgrad_t* op) {
-  return wgrad_sizes_ok(op) ? wgrad_plan(*op).bytes : 0;
+  if (!wgrad_sizes_ok(op)) return 0;
+  const muon_act8_wgrad_t in = wgrad_strides(op);
+  if (in.ld_dy < in.n || in.x8.ld_codes < in.k || in.x8.ld_scales < (in.k + 31) / 32) return 0;
+  return wgrad_plan(in).bytes;
 }
 
 int muon_act8_wgrad(const muon_act8_wgrad_t* op, void* workspace, size_t workspace_bytes,
@@ -253,7 +267,8 @@ int muon_act8_wgrad(const muon_act8_wgrad_t* op, void* workspace, size_t workspa
       !a.vec(op->col_gain, op->k, 4, false, false) ||
       !a.mat(op->dw, op->n, op->k, op->ld_dw, type_size(op->dw_dtype), true))
     return MUON_EINVAL;
-  const WgradPlan p = wgrad_plan(*op);
+  muon_act8_wgrad_t in = wgrad_strides(op);
+  const WgradPlan p = wgrad_plan(in);
   if (!workspace_ok(workspace, workspace_bytes, p.bytes)) return MUON_EWORKSPACE;
   if (p.bytes && !a.mat(workspace, 1, static_cast<int64_t>(p.bytes), 0, 1, true)) return MUON_EWORKSPACE;
   if (a.clash()) return MUON_EALIAS;
@@ -262,7 +277,6 @@ int muon_act8_wgrad(const muon_act8_wgrad_t* op, void* workspace, size_t workspa
   if (int rc = l.open()) return rc;
   if (int rc = l.poison(workspace, p.bytes)) return rc;
   char* ws = static_cast<char*>(workspace);
-  muon_act8_wgrad_t in = *op;
   if (p.copy_dy || p.copy_x)
     if (int rc = l.run("weight gradient, aligned copies", [&](void* st) { return launch_wgrad_copy(in, p, ws, st); })) return rc;
   if (op->tokens > 0)
@@ -315,7 +329,9 @@ int muon_embed_grad(const muon_embed_grad_t* op, void* workspace, size_t workspa
   char* ws = static_cast<char*>(workspace);
   if (p.passes == 0)
     return l.run("embedding gradient", [&](void* st) { return launch_embed_sums(*op, p, ws, st); });
-  for (int pass = 0; pass < p.passes; ++pass) {
+  if (p.one_block)
+    if (int rc = l.run("token sort", [&](void* st) { return launch_embed_sort(*op, p, ws, st); })) return rc;
+  for (int pass = 0; pass < p.passes && !p.one_block; ++pass) {
     if (int rc = l.run("token sort, count", [&](void* st) { return launch_embed_count(*op, p, pass, ws, st); })) return rc;
     if (int rc = l.run("token sort, scatter", [&](void* st) { return launch_embed_scatter(*op, p, pass, ws, st); })) return rc;
   }

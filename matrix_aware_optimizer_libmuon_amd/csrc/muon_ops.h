@@ -53,7 +53,8 @@ int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const cha
 // keys and tokens before and after a pass, each block's digit counts, each
 // row's first place, the sums of the long runs' pieces.
 struct EmbedSortPlan {
-  int passes;                 // digits of the keys 0 .. vocab
+  int passes;                 // digits of the keys 0 .. vocab (0: not sorted)
+  bool one_block;             // few enough for one block to sort them in one launch
   int64_t blocks;             // blocks of a pass, block_tokens tokens each
   int64_t block_tokens;
   int64_t chunks;             // pieces of long runs lie in one chunk
@@ -67,6 +68,7 @@ struct EmbedSortPlan {
 };
 EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols);
 int launch_embed(const muon_embed_t& op, void* stream);
+int launch_embed_sort(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
 int launch_embed_count(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream);
 int launch_embed_scatter(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream);
 int launch_embed_starts(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);

@@ -282,17 +282,17 @@ __global__ __launch_bounds__(kGemmThreads) void k_wgrad(muon_act8_wgrad_t op, Wg
   __shared__ __attribute__((aligned(16))) char smem[Lds<TILE>::bytes];
   const int tid = opaque_tid();
   // first the tiles that are one block's whole, then the others, range by range
-  const bool whole = blockIdx.x < p.whole;
-  const int64_t units = whole ? p.whole : gridDim.x - p.whole;
-  const int64_t unit = xcd_remap(whole ? blockIdx.x : blockIdx.x - p.whole, units);
-  const int64_t rest = p.tiles_n * p.tiles_k - p.whole;
-  const int64_t split = whole ? 0 : unit / rest;
+  const uint32_t nwhole = static_cast<uint32_t>(p.whole), tiles = static_cast<uint32_t>(p.tiles_n * p.tiles_k);
+  const bool whole = blockIdx.x < nwhole;
+  const uint32_t unit = static_cast<uint32_t>(whole ? xcd_remap(blockIdx.x, nwhole)
+                                                    : xcd_remap(blockIdx.x - nwhole, gridDim.x - nwhole));
+  const uint32_t split = whole ? 0u : unit / (tiles - nwhole);
   int64_t ti, tj;
-  decode_full(whole ? unit : p.whole + unit - split * rest, p.tiles_n, p.tiles_k, ti, tj);
+  decode_full(whole ? unit : nwhole + unit - split * (tiles - nwhole), p.tiles_n, p.tiles_k, ti, tj);
   const int64_t i0 = ti * TILE, j0 = tj * TILE, t0 = split * p.split_rows;
   const int64_t rows = whole ? op.tokens : min(p.split_rows, op.tokens - t0);
   const bool last = whole || p.splits == 1;
-  partial += unit * (TILE * TILE);
+  partial += static_cast<int64_t>(unit) * (TILE * TILE);
   f32x4_t acc[G::NB][G::NB];
   zero_acc<G::NB>(acc);
   product<TILE>(op, i0, j0, t0, rows, smem, acc, tid);

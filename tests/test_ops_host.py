@@ -171,6 +171,11 @@ def test_wgrad_refuses(lib):
     op = wgrad()
     need = lib.muon_act8_wgrad_workspace_bytes(ctypes.byref(op))
     assert need > 0 and lib.muon_act8_wgrad_workspace_bytes(ctypes.byref(wgrad(n=0))) == 0
+    assert lib.muon_act8_wgrad_workspace_bytes(ctypes.byref(wgrad(ld_dy=0))) == 0
+    # a single row's strides are not read
+    one = [lib.muon_act8_wgrad_workspace_bytes(ctypes.byref(wgrad(tokens=1, ld_dy=ld, x8=act8(ld_codes=ld, ld_scales=ld))))
+           for ld in (64, 0, -64, 1 << 50)]
+    assert len(set(one)) == 1
     assert call(ws_bytes=need - 1) == EWORKSPACE and call(ws=None) == EWORKSPACE
     assert call(ws=ctypes.c_void_p((1 << 42) + 4)) == EWORKSPACE
     p = ptr()
