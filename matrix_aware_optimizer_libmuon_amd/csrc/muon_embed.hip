@@ -44,29 +44,41 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_
 }
 
 // ------------------------------------------------------------------ lookup ----
-// One lane per 8 columns; rows of 8-vectors laid end to end.
+// Rows of 8-column vectors laid end to end, kVecs of them 256 apart for each
+// thread: the ids, then the rows, are loaded for all of them at once (one each:
+// 43 us, two: 37.2, four: 37.7 for 16384 tokens of 4096 bf16).
+constexpr int kVecs = 2;
 template <class S, class T>
 __global__ __launch_bounds__(kRowThreads) void k_embed(muon_embed_t op, int64_t blocks) {
   const uint32_t vpr = static_cast<uint32_t>((op.cols + 7) >> 3);
+  const int cols = static_cast<int>(op.cols);
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const uint64_t first = static_cast<uint64_t>(b) * kRowThreads;
+    const uint64_t first = static_cast<uint64_t>(b) * (kRowThreads * kVecs);
     const uint64_t row0 = first / vpr;
-    const uint32_t u = static_cast<uint32_t>(first - row0 * vpr) + threadIdx.x;
-    const uint32_t dr = u / vpr;
-    const int64_t row = static_cast<int64_t>(row0 + dr);
-    if (row >= op.tokens) continue;
-    const int c = static_cast<int>(u - dr * vpr) * 8, n = static_cast<int>(op.cols) - c;
-    const int64_t id = load_id(op.ids, op.id_bytes, row);
-    float v[8];
+    const uint32_t u0 = static_cast<uint32_t>(first - row0 * vpr) + threadIdx.x;
+    int64_t row[kVecs], id[kVecs];
+    int c[kVecs];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (id >= 0 && id < op.vocab) {
-      Vec8<S> raw;
-      load8(raw, static_cast<const S*>(op.table) + id * op.ld_table + c, n);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = raw.get(i) * op.scale;
+    for (int k = 0; k < kVecs; ++k) {
+      const uint32_t u = u0 + k * kRowThreads, dr = u / vpr;
+      row[k] = static_cast<int64_t>(row0 + dr);
+      c[k] = static_cast<int>(u - dr * vpr) * 8;
+      id[k] = row[k] < op.tokens ? load_id(op.ids, op.id_bytes, row[k]) : -1;
     }
-    Vec8<T>::store(static_cast<T*>(op.out) + row * op.ld_out + c, n, v);
+    Vec8<S> raw[kVecs];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const bool in = id[k] >= 0 && id[k] < op.vocab;
+      load8(raw[k], static_cast<const S*>(op.table) + (in ? id[k] : 0) * op.ld_table + c[k], in ? cols - c[k] : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      if (row[k] >= op.tokens) continue;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = raw[k].get(i) * op.scale;
+      Vec8<T>::store(static_cast<T*>(op.out) + row[k] * op.ld_out + c[k], cols - c[k], v);
+    }
   }
 }
 
@@ -565,7 +577,7 @@ EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols) {
 }
 
 int launch_embed(const muon_embed_t& op, void* stream) {
-  const int64_t vpr = (op.cols + 7) / 8, blocks = (op.tokens * vpr + kRowThreads - 1) / kRowThreads;
+  const int64_t vpr = (op.cols + 7) / 8, blocks = (op.tokens * vpr + kRowThreads * kVecs - 1) / (kRowThreads * kVecs);
   return by_types(op.table_dtype, op.out_dtype, [&](auto s, auto t) {
     hipLaunchKernelGGL((k_embed<decltype(s), decltype(t)>), dim3(static_cast<unsigned>(std::min(blocks, kMaxGrid))),
                        dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), op, blocks);

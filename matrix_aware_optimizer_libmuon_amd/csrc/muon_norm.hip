@@ -174,26 +174,27 @@ __global__ __launch_bounds__(Rows<RT>::threads) void k_rmsnorm_grad(muon_rmsnorm
   }
 }
 
-// dgain[c] = sum over blocks of partial[b][c]: 64 columns per block, the
-// partial rows split over its 16 waves, whose sums are added in order.
-constexpr int kDgainWaves = 16;
-__global__ __launch_bounds__(64 * kDgainWaves) void k_dgain(const float* partial, int64_t blocks, int cols, float* dgain) {
-  __shared__ float red[kDgainWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = static_cast<int>(blockIdx.x) * 64 + lane;
-  const int64_t per = (blocks + kDgainWaves - 1) / kDgainWaves;
-  const int64_t end = (w + 1) * per < blocks ? (w + 1) * per : blocks;
+// dgain[c] = sum over blocks of partial[b][c]: 16 columns per block, the partial
+// rows dealt in turn to its 64 groups of 16 threads.
+constexpr int kDgainCols = 16, kDgainThreads = 1024;
+__global__ __launch_bounds__(kDgainThreads) void k_dgain(const float* partial, int64_t blocks, int cols, float* dgain) {
+  constexpr int kGroups = kDgainThreads / kDgainCols, kWaves = kDgainThreads / 64;
+  __shared__ float red[kWaves][kDgainCols];
+  const int t = static_cast<int>(threadIdx.x), g = t / kDgainCols;
+  const int c = static_cast<int>(blockIdx.x) * kDgainCols + t % kDgainCols;
   float v = 0.f;
   if (c < cols) {
 #pragma unroll 8
-    for (int64_t b = w * per; b < end; ++b) v += gld<float>(partial + b * cols + c);
+    for (int b = g; b < static_cast<int>(blocks); b += kGroups) v += gld<float>(partial + static_cast<int64_t>(b) * cols + c);
   }
-  red[w][lane] = v;
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  if ((t & 63) < kDgainCols) red[t >> 6][t & 63] = v;
   __syncthreads();
-  if (w == 0 && c < cols) {
+  if (t < kDgainCols && c < cols) {
     v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kDgainWaves; ++k) v += red[k][lane];
+    for (int k = 0; k < kWaves; ++k) v += red[k][t];
     gst<float>(dgain + c, v);
   }
 }
@@ -257,7 +258,7 @@ int launch_rmsnorm_grad(const muon_rmsnorm_grad_t& op, float* partial, void* str
 }
 
 int launch_rmsnorm_dgain(const float* partial, int64_t blocks, int64_t cols, float* dgain, void* stream) {
-  hipLaunchKernelGGL(k_dgain, dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(64 * kDgainWaves), 0,
+  hipLaunchKernelGGL(k_dgain, dim3(static_cast<unsigned>((cols + kDgainCols - 1) / kDgainCols)), dim3(kDgainThreads), 0,
                      static_cast<hipStream_t>(stream), partial, blocks, static_cast<int>(cols), dgain);
   return static_cast<int>(hipGetLastError());
 }
