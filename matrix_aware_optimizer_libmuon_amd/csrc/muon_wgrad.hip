@@ -36,15 +36,16 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 // 16 bytes (or one byte, zero-extended to a dword) per lane from buffer `srd` at
 // voff + soff into LDS, at lds_dst + 16 (4) times the lane.  As dma16() of
 // muon_gemm.h: an asm statement with explicit waits, whose scalar operands are
-// formed by scalar instructions (tests/test_ops_isa.py checks the compiled code).
+// formed by scalar instructions (tests/test_ops_isa.py checks the compiled code);
+// the s_nop keeps the wait state between a scalar write of m0 and a load to LDS.
 template <bool BYTE>
 __device__ __forceinline__ void dma_bounded(u32x4 srd, uint32_t voff, uint32_t soff, const void* lds_dst) {
   const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (__attribute__((addrescdspace(3))) void*)lds_dst));
   if constexpr (BYTE)
-    asm volatile("buffer_load_ubyte %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(m0));
+    asm volatile("s_nop 0\n\tbuffer_load_ubyte %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(m0));
   else
-    asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(m0));
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(m0));
 }
 
 // The descriptor of `rows` rows from row0, columns from byte col0, of a matrix:

@@ -39,6 +39,9 @@ def test_weight_gradient_keeps_the_wait_states(tmp_path):
     r = subprocess.run([HIPCC, *build.FLAGS, *extra, "--offload-device-only", "-S", "-o", out, os.path.join(build.CSRC, src)],
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
-    n, bad = _scan(open(out).read())
+    text = open(out).read()
+    n, bad = _scan(text)
     assert n > 20
+    # and the one wait state after a scalar write of m0
+    assert len(re.findall(r"s_nop 0\s+buffer_load_\w+ .* offen lds", text)) == n
     assert not bad, [(h.load, h.writer, h.wait_states) for h in bad[:5]]
