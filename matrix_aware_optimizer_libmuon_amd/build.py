@@ -83,7 +83,7 @@ def _marshal_cmd(out):
             "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include",
             *[f"-I{p}" for p in ce.include_paths()], f"-I{sysconfig.get_paths()['include']}",
             os.path.join(CSRC, "marshal.cpp"), os.path.join(CSRC, "marshal_ops.cpp"), "-o", out,
-            f"-L{libdir}", "-lc10", "-lc10_hip", "-ltorch", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libdir}"]
+            f"-L{libdir}", "-lc10", "-lc10_hip", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", f"-Wl,-rpath,{libdir}"]
 
 
 def build(verbose: bool = False) -> str:

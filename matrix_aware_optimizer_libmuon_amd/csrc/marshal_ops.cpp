@@ -11,6 +11,7 @@
 // argument; a call's status is returned with its outputs.
 #include <torch/extension.h>
 
+#include <ATen/hip/EmptyTensor.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
 
@@ -72,7 +73,10 @@ class Call {
   }
   hipStream_t stream() const { return c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(device_.index()).stream(); }
   const c10::Device& device() const { return device_; }
-  at::Tensor empty(at::IntArrayRef size, at::ScalarType t) const { return at::empty(size, at::TensorOptions().dtype(t).device(device_)); }
+  // (the allocation alone: about 0.2 us less than at::empty with its dispatcher)
+  at::Tensor empty(at::IntArrayRef size, at::ScalarType t) const {
+    return at::Tensor(at::detail::empty_cuda(size, t, device_, c10::nullopt));
+  }
   // a workspace of n bytes (torch aligns allocations to 256 bytes and more)
   at::Tensor workspace(size_t n) const { return n ? empty({static_cast<int64_t>(n)}, at::kByte) : at::Tensor(); }
   void on_device(const at::Tensor& t, const char* name) const {

@@ -88,7 +88,8 @@ class Launcher {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return host_hip_fail(e, "hipGetDevice");
-    if (!host_stream_on_device(stream_, dev)) return MUON_EINVAL;
+    // (the null stream is the current device's)
+    if (stream_ && !host_stream_on_device(stream_, dev)) return MUON_EINVAL;
     if (host_debug()) {
       hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
       e = hipStreamIsCapturing(stream_, &cap);

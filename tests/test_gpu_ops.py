@@ -431,6 +431,19 @@ def test_embed_gradient_is_exact_on_integers(kind, tokens, vocab, cols):
     assert torch.equal(out.cpu().double(), want + base.double())
 
 
+@pytest.mark.parametrize("tokens,vocab", [(256, 40), (257, 40), (4096, 600), (4097, 600), (262144, 3000), (262145, 3000), (700001, 300000)])
+def test_embed_gradient_at_the_sort_s_limits(tokens, vocab):
+    """Unsorted, one block, one step a block, several steps a block."""
+    g = gen(tokens)
+    ids = (torch.rand(tokens, generator=g) ** 3 * vocab).long()
+    ids[torch.rand(tokens, generator=g) < 0.1] = -7
+    dy = torch.randint(-8, 9, (tokens, 3), generator=g).float()
+    live = ids >= 0
+    want = torch.zeros(vocab, 3, dtype=torch.float64).index_add_(0, ids[live], dy[live].double())
+    for it in (torch.int64, torch.int32):
+        assert torch.equal(muon.embed_grad(dy.to(DEV), ids.to(it).to(DEV), vocab).cpu().double(), want)
+
+
 def test_embed_gradient_random_and_repeatable():
     ids, dy = embed_ids("skewed", 5000, 400), randn(9, 5000, 264, dtype=torch.bfloat16)
     want = O.embed_grad(np64(dy), ids.numpy(), 400, 0.7)
