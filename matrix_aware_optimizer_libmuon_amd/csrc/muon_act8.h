@@ -4,7 +4,9 @@
 // quad hold one group of 32, whose maximum they share by two quad
 // permutations.  The vector accesses carry the alignment of one element:
 // gfx950 global accesses may start at any byte, so rows of every stride take
-// the same path, and only a row's last, shorter vector goes element by element.
+// the same path.  A row's last, shorter vector is loaded with the elements before
+// it, 8 up to the row's end, and shifted down in registers, so that it costs no
+// further trip to memory; it is stored in pieces of 4, 2 and 1.
 #pragma once
 #include "muon_device.h"
 #include "muon.h"
@@ -14,6 +16,11 @@ namespace muon {
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2_a1 __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 // Element types: raw 8-vectors as loaded, and their values.
@@ -32,6 +39,13 @@ struct Vec8<uint16_t> {            // bf16
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = h[2 * i] | (h[2 * i + 1] << 16);
   }
+  // elements k .. 7 to the front, zeros behind them (0 < k < 8)
+  __device__ __forceinline__ void drop(int k) {
+    if (k & 4) r = u32x4{r[2], r[3], 0, 0};
+    if (k & 2) r = u32x4{r[1], r[2], r[3], 0};
+    if (k & 1)
+      r = u32x4{(r[0] >> 16) | (r[1] << 16), (r[1] >> 16) | (r[2] << 16), (r[2] >> 16) | (r[3] << 16), r[3] >> 16};
+  }
   __device__ __forceinline__ float get(int i) const {
     return __uint_as_float(i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
   }
@@ -41,10 +55,19 @@ struct Vec8<uint16_t> {            // bf16
     for (int i = 0; i < 4; ++i) o[i] = pack2(v[2 * i], v[2 * i + 1]);
     if (n >= 8) {
       gst<u32x4_a2>(p, o);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) gst<uint16_t>(p + i, static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1))));
+    } else if (n > 0) {
+      if (n & 4) {
+        gst<u32x2_a2>(p, u32x2_a2{o[0], o[1]});
+        o[0] = o[2];
+        o[1] = o[3];
+        p += 4;
+      }
+      if (n & 2) {
+        gst<u32_a2>(p, o[0]);
+        o[0] = o[1];
+        p += 2;
+      }
+      if (n & 1) gst<uint16_t>(p, static_cast<uint16_t>(o[0]));
     }
   }
 };
@@ -61,25 +84,60 @@ struct Vec8<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i >> 2][i & 3] = i < n ? gld<uint32_t>(p + i) : 0u;
   }
+  __device__ __forceinline__ void drop(int k) {
+    if (k & 4) {
+      r[0] = r[1];
+      r[1] = u32x4{0, 0, 0, 0};
+    }
+    if (k & 2) {
+      r[0] = u32x4{r[0][2], r[0][3], r[1][0], r[1][1]};
+      r[1] = u32x4{r[1][2], r[1][3], 0, 0};
+    }
+    if (k & 1) {
+      r[0] = u32x4{r[0][1], r[0][2], r[0][3], r[1][0]};
+      r[1] = u32x4{r[1][1], r[1][2], r[1][3], 0};
+    }
+  }
   __device__ __forceinline__ float get(int i) const { return __uint_as_float(r[i >> 2][i & 3]); }
   static __device__ __forceinline__ void store(float* p, int n, const float (&v)[8]) {
     if (n >= 8) {
       gst<u32x4_a4>(p, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
       gst<u32x4_a4>(p + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) gst<float>(p + i, v[i]);
+    } else if (n > 0) {
+      u32x4 o = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+      if (n & 4) {
+        gst<u32x4_a4>(p, o);
+        o = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), 0};
+        p += 4;
+      }
+      if (n & 2) {
+        gst<u32x2_a4>(p, u32x2_a4{o[0], o[1]});
+        o[0] = o[2];
+        p += 2;
+      }
+      if (n & 1) gst<uint32_t>(p, o[0]);
     }
   }
 };
 
-// n valid elements (<= 0: none, zeros).
+// The 8 columns at p, columns c .. of a row, n of them inside (<= 0: none, zeros):
+// fetch8 issues the load, settle8 puts a shorter vector in its place.  Several
+// vectors are fetched before the first is settled.
 template <class T>
-__device__ __forceinline__ void load8(Vec8<T>& v, const T* p, int n) {
-  if (n >= 8) v.load(p);
-  else if (n > 0) v.load(p, n);
-  else v.zero();
+__device__ __forceinline__ void fetch8(Vec8<T>& v, const T* p, int c, int n) {
+  const int back = n < 8 ? 8 - n : 0;
+  if (n <= 0) v.zero();
+  else if (back <= c) v.load(p - back);
+  else v.load(p, n);                 // a row of fewer than 8
+}
+template <class T>
+__device__ __forceinline__ void settle8(Vec8<T>& v, int c, int n) {
+  if (n > 0 && n < 8 && 8 - n <= c) v.drop(8 - n);
+}
+template <class T>
+__device__ __forceinline__ void load8(Vec8<T>& v, const T* p, int c, int n) {
+  fetch8(v, p, c, n);
+  settle8(v, c, n);
 }
 
 template <int CTRL>
@@ -154,25 +212,55 @@ __device__ __forceinline__ void act8_decode(u32x2 c, uint32_t scale_byte, float 
   }
 }
 
-__device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int n) {
-  if (n >= 8) return gld<u32x2_a1>(p);
-  u32x2 c{0, 0};
+// A lane's codes and their scale byte, columns c .. of row r, n of them inside:
+// fetched and settled as above.
+struct Codes8 {
+  u32x2 c;
+  uint32_t sb;
+  __device__ __forceinline__ void fetch(const muon_act8_t& a, int64_t r, int col, int n) {
+    const uint8_t* p = a.codes + r * a.ld_codes + col;
+    const int back = n < 8 ? 8 - n : 0;
+    c = u32x2{0, 0};
+    sb = 127;
+    if (n <= 0) return;
+    sb = gld<uint8_t>(a.scales + r * a.ld_scales + (col >> 5));
+    if (back <= col) {
+      c = gld<u32x2_a1>(p - back);
+    } else {                         // a row of fewer than 8
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) c[i >> 2] |= static_cast<uint32_t>(gld<uint8_t>(p + i)) << (8 * (i & 3));
-  return c;
-}
+      for (int i = 0; i < 8; ++i)
+        if (i < n) c[i >> 2] |= static_cast<uint32_t>(gld<uint8_t>(p + i)) << (8 * (i & 3));
+    }
+  }
+  __device__ __forceinline__ void settle(int col, int n) {
+    if (n > 0 && n < 8 && 8 - n <= col) {
+      const uint64_t w = (static_cast<uint64_t>(c[1]) << 32 | c[0]) >> (8 * (8 - n));
+      c = u32x2{static_cast<uint32_t>(w), static_cast<uint32_t>(w >> 32)};
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { act8_decode(c, sb, v); }
+};
+
 __device__ __forceinline__ void store_codes(uint8_t* p, int n, u32x2 c) {
   if (n >= 8) {
     gst<u32x2_a1>(p, c);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) gst<uint8_t>(p + i, static_cast<uint8_t>(c[i >> 2] >> (8 * (i & 3))));
+  } else if (n > 0) {
+    uint32_t o = c[0];
+    if (n & 4) {
+      gst<u32_a1>(p, o);
+      o = c[1];
+      p += 4;
+    }
+    if (n & 2) {
+      gst<u16_a1>(p, static_cast<uint16_t>(o));
+      o >>= 16;
+      p += 2;
+    }
+    if (n & 1) gst<uint8_t>(p, static_cast<uint8_t>(o));
   }
 }
 
-// A lane's 8 columns from c0 of row r, written to / read from an 8-bit matrix.
+// A lane's 8 columns from c0 of row r, written to an 8-bit matrix.
 __device__ __forceinline__ void act8_put(const muon_act8_t& a, int64_t r, int c0, int n, const float (&v)[8]) {
   int sb;
   const u32x2 c = act8_encode(v, sb);

@@ -45,7 +45,7 @@ __global__ __launch_bounds__(kThreads) void k_act8_pack(int64_t blocks, const T*
                                                         muon_act8_t out) {
   each_vector(blocks, rows, cols, [&](const Place& p) __attribute__((always_inline)) {
     Vec8<T> raw;
-    load8(raw, x + p.row * ld + p.col, p.n);
+    load8(raw, x + p.row * ld + p.col, p.col, p.n);
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = raw.get(i);
@@ -53,22 +53,15 @@ __global__ __launch_bounds__(kThreads) void k_act8_pack(int64_t blocks, const T*
   });
 }
 
-__device__ __forceinline__ void act8_get(const muon_act8_t& a, const Place& p, float (&v)[8]) {
-  if (p.n > 0) {
-    const u32x2 c = load_codes(a.codes + p.row * a.ld_codes + p.col, p.n);
-    act8_decode(c, gld<uint8_t>(a.scales + p.row * a.ld_scales + (p.col >> 5)), v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  }
-}
-
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_act8_unpack(int64_t blocks, muon_act8_t in, int64_t rows, int cols, T* out,
                                                           int64_t ld) {
   each_vector(blocks, rows, cols, [&](const Place& p) __attribute__((always_inline)) {
+    Codes8 c;
+    c.fetch(in, p.row, p.col, p.n);
+    c.settle(p.col, p.n);
     float v[8];
-    act8_get(in, p, v);
+    c.get(v);
     Vec8<T>::store(out + p.row * ld + p.col, p.n, v);
   });
 }
@@ -85,8 +78,10 @@ template <class T>
 __global__ __launch_bounds__(kThreads) void k_swiglu(int64_t blocks, muon_swiglu_t op) {
   each_vector(blocks, op.rows, static_cast<int>(op.cols), [&](const Place& p) __attribute__((always_inline)) {
     Vec8<T> rg, ru;
-    load8(rg, static_cast<const T*>(op.gate) + p.row * op.ld_gate + p.col, p.n);
-    load8(ru, static_cast<const T*>(op.up) + p.row * op.ld_up + p.col, p.n);
+    fetch8(rg, static_cast<const T*>(op.gate) + p.row * op.ld_gate + p.col, p.col, p.n);
+    fetch8(ru, static_cast<const T*>(op.up) + p.row * op.ld_up + p.col, p.col, p.n);
+    settle8(rg, p.col, p.n);
+    settle8(ru, p.col, p.n);
     float g[8], u[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -110,10 +105,16 @@ template <class T>
 __global__ __launch_bounds__(kThreads) void k_swiglu_grad(int64_t blocks, muon_swiglu_grad_t op) {
   each_vector(blocks, op.rows, static_cast<int>(op.cols), [&](const Place& p) __attribute__((always_inline)) {
     Vec8<T> rd;
-    load8(rd, static_cast<const T*>(op.da) + p.row * op.ld_da + p.col, p.n);
+    Codes8 cg, cu;
+    fetch8(rd, static_cast<const T*>(op.da) + p.row * op.ld_da + p.col, p.col, p.n);
+    cg.fetch(op.gate8, p.row, p.col, p.n);
+    cu.fetch(op.up8, p.row, p.col, p.n);
+    settle8(rd, p.col, p.n);
+    cg.settle(p.col, p.n);
+    cu.settle(p.col, p.n);
     float g[8], u[8], dg[8], du[8];
-    act8_get(op.gate8, p, g);
-    act8_get(op.up8, p, u);
+    cg.get(g);
+    cu.get(u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = rd.get(i), s = sigmoid(g[i]), act = g[i] * s;

@@ -34,7 +34,7 @@ constexpr int kDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 1024;                  // tokens of a block per step
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRowThreads = 256;
-constexpr int kRun = 64;                            // longest run that one wave adds up
+constexpr int kRun = 32;                            // longest run that one wave adds up (at most 64)
 constexpr int kDirect = 256;                        // tokens that are not sorted
 constexpr int kRowsEach = 4;                        // rows of a wave (or block) of k_direct
 
@@ -69,11 +69,12 @@ __global__ __launch_bounds__(kRowThreads) void k_embed(muon_embed_t op, int64_t 
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       const bool in = id[k] >= 0 && id[k] < op.vocab;
-      load8(raw[k], static_cast<const S*>(op.table) + (in ? id[k] : 0) * op.ld_table + c[k], in ? cols - c[k] : 0);
+      fetch8(raw[k], static_cast<const S*>(op.table) + (in ? id[k] : 0) * op.ld_table + c[k], c[k], in ? cols - c[k] : 0);
     }
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       if (row[k] >= op.tokens) continue;
+      settle8(raw[k], c[k], id[k] >= 0 && id[k] < op.vocab ? cols - c[k] : 0);
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = raw[k].get(i) * op.scale;
@@ -307,30 +308,30 @@ __device__ __forceinline__ void add_rows(const muon_embed_grad_t& op, uint32_t h
   const int valid = static_cast<int>(op.cols) - c;
   const S* dy = static_cast<const S*>(op.dy) + c;
   auto row = [&](int i) { return dy + static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(held, i))) * op.ld_dy; };
-  int i = first;
-  const int end = first + n;
-  for (; i + 8 <= end; i += 8) {
-    Vec8<S> v[8];
+  auto batch = [&](auto size, int i) __attribute__((always_inline)) {
+    constexpr int N = decltype(size)::value;
+    Vec8<S> v[N];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) load8(v[k], row(i + k), valid);
+    for (int k = 0; k < N; ++k) fetch8(v[k], row(i + k), c, valid);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < N; ++k) {
+      settle8(v[k], c, valid);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] += v[k].get(j);
+    }
+  };
+  int i = first;
+  const int end = first + n;
+  for (; i + 8 <= end; i += 8) batch(std::integral_constant<int, 8>{}, i);
+  if (i + 4 <= end) {
+    batch(std::integral_constant<int, 4>{}, i);
+    i += 4;
   }
-  for (; i + 2 <= end; i += 2) {
-    Vec8<S> v[2];
-    load8(v[0], row(i), valid);
-    load8(v[1], row(i + 1), valid);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = s[j] + v[0].get(j) + v[1].get(j);
+  if (i + 2 <= end) {
+    batch(std::integral_constant<int, 2>{}, i);
+    i += 2;
   }
-  if (i < end) {
-    Vec8<S> v;
-    load8(v, row(i), valid);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] += v.get(j);
-  }
+  if (i < end) batch(std::integral_constant<int, 1>{}, i);
 }
 
 // dtable[row] (+)= scale s, columns c .. c + 7.
@@ -339,7 +340,7 @@ __device__ __forceinline__ void put_row(const muon_embed_grad_t& op, int64_t row
   const int n = static_cast<int>(op.cols) - c;
   T* out = static_cast<T*>(op.dtable) + row * op.ld_dtable + c;
   Vec8<T> old;
-  if (op.accumulate) load8(old, out, n);
+  if (op.accumulate) load8(old, static_cast<const T*>(out), c, n);
 #pragma unroll
   for (int j = 0; j < 8; ++j) s[j] = op.accumulate ? fmaf(op.scale, s[j], old.get(j)) : op.scale * s[j];
   Vec8<T>::store(out, n, s);
@@ -400,7 +401,7 @@ struct Chunk {
 __device__ __forceinline__ Chunk chunk_runs(const Sorted& a, int64_t tokens, int64_t vocab, int64_t chunk, int lane) {
   const int64_t i = chunk * kRun + lane;
   Chunk c;
-  c.key = i < tokens ? gld<uint32_t>(a.keys + i) : static_cast<uint32_t>(vocab);
+  c.key = lane < kRun && i < tokens ? gld<uint32_t>(a.keys + i) : static_cast<uint32_t>(vocab);
   c.begin = c.end = 0;
   if (c.key < vocab) {
     c.begin = gld<uint32_t>(a.start + c.key);
@@ -480,8 +481,9 @@ __global__ __launch_bounds__(kRowThreads) void k_sums(muon_embed_grad_t op, Sort
     sum_row<S, T, TPR>(op, a, row, static_cast<int>(threadIdx.x) % TPR, lane);
 }
 
-// The run that begins in a chunk: its pieces, 512 columns from 512 blockIdx.y.
-// The waves take consecutive shares of them, which are added in order.
+// The long runs that begin among 64 places of the sorted order: their pieces,
+// 512 columns from 512 blockIdx.y.  The waves take consecutive shares of a run's
+// pieces, which are added in order.
 constexpr int kJoinWaves = 4;
 template <class T>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, Sorted a) {
@@ -489,34 +491,43 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int cols = static_cast<int>(op.cols);
   const int c = static_cast<int>(blockIdx.y) * 512 + lane * 8;
-  for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
-    const Chunk r = chunk_runs(a, op.tokens, op.vocab, chunk, lane);
-    if (!r.right) continue;                          // the whole block
-    const int src = __builtin_ctzll(r.right);
-    const int64_t row = static_cast<uint32_t>(__builtin_amdgcn_readlane(r.key, src));
-    const int64_t last = (static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(r.end, src))) - 1) / kRun;
-    const int n = static_cast<int>(last - chunk + 1), per = (n + kJoinWaves - 1) / kJoinWaves;
-    const int end = min((w + 1) * per, n);
-    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 64; at < op.tokens; at += static_cast<int64_t>(gridDim.x) * 64) {
+    const int64_t i = at + lane;
+    uint32_t key = static_cast<uint32_t>(op.vocab), begin = 0, end = 0;
+    if (i < op.tokens) key = gld<uint32_t>(a.keys + i);
+    if (key < op.vocab) {
+      begin = gld<uint32_t>(a.start + key);
+      end = gld<uint32_t>(a.start + key + 1);
+    }
+    // (the same in all waves)
+    for (uint64_t m = __ballot(end - begin > kRun && begin == i); m; m &= m - 1) {
+      const int src = __builtin_ctzll(m);
+      const int64_t row = static_cast<uint32_t>(__builtin_amdgcn_readlane(key, src));
+      const int64_t chunk = (at + src) / kRun;
+      const int64_t last = (static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(end, src))) - 1) / kRun;
+      const int n = static_cast<int>(last - chunk + 1), per = (n + kJoinWaves - 1) / kJoinWaves;
+      const int to = min((w + 1) * per, n);
+      float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int k = w * per; k < end; ++k) {
-      Vec8<float> v;
-      load8(v, a.pieces + ((chunk + k) * 2 + (k == 0)) * cols + c, cols - c);
+      for (int k = w * per; k < to; ++k) {
+        Vec8<float> v;
+        load8(v, static_cast<const float*>(a.pieces) + ((chunk + k) * 2 + (k == 0)) * cols + c, c, cols - c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += v.get(j);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) red[w][j * 64 + lane] = s[j];
-    __syncthreads();
-    if (w == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[j] = 0.f;
-        for (int k = 0; k < kJoinWaves; ++k) s[j] += red[k][j * 64 + lane];
+        for (int j = 0; j < 8; ++j) s[j] += v.get(j);
       }
-      put_row<T>(op, row, c, s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) red[w][j * 64 + lane] = s[j];
+      __syncthreads();
+      if (w == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s[j] = 0.f;
+          for (int k = 0; k < kJoinWaves; ++k) s[j] += red[k][j * 64 + lane];
+        }
+        put_row<T>(op, row, c, s);
+      }
+      __syncthreads();                               // before red is used again
     }
-    __syncthreads();                                 // before red is used again
   }
 }
 
@@ -647,7 +658,7 @@ int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char*
 }
 
 int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
-  const dim3 grid(static_cast<unsigned>(std::min(p.chunks, kMaxGrid)), static_cast<unsigned>((op.cols + 511) / 512));
+  const dim3 grid(static_cast<unsigned>(std::min((op.tokens + 63) / 64, kMaxGrid)), static_cast<unsigned>((op.cols + 511) / 512));
   return by_types(op.dy_dtype, op.table_dtype, [&](auto, auto t) {
     hipLaunchKernelGGL((k_join<decltype(t)>), grid, dim3(64 * kJoinWaves), 0, static_cast<hipStream_t>(stream), op,
                        sorted(p, ws));

@@ -55,8 +55,14 @@ __global__ __launch_bounds__(Rows<RT>::threads) void k_rmsnorm(muon_rmsnorm_t op
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       const int c = (t + j * RT) * 8;
-      load8(x[j], static_cast<const T*>(op.x) + row * op.ld_x + c, cols - c);
-      if (op.residual) load8(r[j], static_cast<const T*>(op.residual) + row * op.ld_residual + c, cols - c);
+      fetch8(x[j], static_cast<const T*>(op.x) + row * op.ld_x + c, c, cols - c);
+      if (op.residual) fetch8(r[j], static_cast<const T*>(op.residual) + row * op.ld_residual + c, c, cols - c);
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int c = (t + j * RT) * 8;
+      settle8(x[j], c, cols - c);
+      if (op.residual) settle8(r[j], c, cols - c);
     }
     float h[VPL][8], ss = 0.f;
 #pragma unroll
@@ -79,7 +85,7 @@ __global__ __launch_bounds__(Rows<RT>::threads) void k_rmsnorm(muon_rmsnorm_t op
       if (op.y) {
         if (op.gain) {
           Vec8<float> g;
-          load8(g, op.gain + c, n);
+          load8(g, op.gain + c, c, n);
 #pragma unroll
           for (int i = 0; i < 8; ++i) h[j][i] *= g.get(i);
         }
@@ -104,7 +110,7 @@ __global__ __launch_bounds__(Rows<RT>::threads) void k_rmsnorm_grad(muon_rmsnorm
   for (int j = 0; j < VPL; ++j) {
     const int c = (t + j * RT) * 8;
     Vec8<float> g;
-    if (op.gain) load8(g, op.gain + c, cols - c);
+    if (op.gain) load8(g, op.gain + c, c, cols - c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       gain[j][i] = op.gain ? g.get(i) : 1.f;
@@ -115,21 +121,26 @@ __global__ __launch_bounds__(Rows<RT>::threads) void k_rmsnorm_grad(muon_rmsnorm
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * R::per_block + threadIdx.x / RT; row < op.rows;
        row += static_cast<int64_t>(gridDim.x) * R::per_block) {
     Vec8<T> dy[VPL], dres[VPL];
-    u32x2 code[VPL];
-    uint32_t sb[VPL];
+    Codes8 code[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       const int c = (t + j * RT) * 8, n = cols - c;
-      load8(dy[j], static_cast<const T*>(op.dy) + row * op.ld_dy + c, n);
-      if (op.dres) load8(dres[j], static_cast<const T*>(op.dres) + row * op.ld_dres + c, n);
-      code[j] = load_codes(op.n.codes + row * op.n.ld_codes + c, n);
-      sb[j] = n > 0 ? gld<uint8_t>(op.n.scales + row * op.n.ld_scales + (c >> 5)) : 127u;
+      fetch8(dy[j], static_cast<const T*>(op.dy) + row * op.ld_dy + c, c, n);
+      if (op.dres) fetch8(dres[j], static_cast<const T*>(op.dres) + row * op.ld_dres + c, c, n);
+      code[j].fetch(op.n, row, c, n);
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int c = (t + j * RT) * 8, n = cols - c;
+      settle8(dy[j], c, n);
+      if (op.dres) settle8(dres[j], c, n);
+      code[j].settle(c, n);
     }
     const float rstd = gld<float>(op.rstd + row);
     float gd[VPL][8], nv[VPL][8], s = 0.f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      act8_decode(code[j], sb[j], nv[j]);
+      code[j].get(nv[j]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float d = dy[j].get(i);
