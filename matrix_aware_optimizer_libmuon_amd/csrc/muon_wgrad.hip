@@ -41,7 +41,7 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 template <bool BYTE>
 __device__ __forceinline__ void dma_bounded(u32x4 srd, uint32_t voff, uint32_t soff, const void* lds_dst) {
   const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-      (__attribute__((addrescdspace(3))) void*)lds_dst));
+      (__attribute__((address_space(3))) void*)lds_dst));
   if constexpr (BYTE)
     asm volatile("s_nop 0\n\tbuffer_load_ubyte %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(m0));
   else
