@@ -35,7 +35,7 @@ int launch_rmsnorm_dgain(const float* partial, int64_t blocks, int64_t cols, flo
 // Workspace: the token ranges' partial outputs where there are several, and
 // aligned copies of a dy or x8 that the kernel's loads cannot take as they are.
 struct WgradPlan {
-  int tile;                   // 256 or 128
+  int tn, tk;                 // output tile: 256 x 256, 256 x 128 or 128 x 128
   int64_t tiles_n, tiles_k;   // output tiles
   int64_t whole;              // tiles (the first ones) that one block makes from all tokens
   int64_t splits, split_rows; // token ranges of the others, of split_rows (the last may be shorter)
