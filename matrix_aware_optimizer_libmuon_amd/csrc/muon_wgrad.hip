@@ -354,24 +354,40 @@ __global__ __launch_bounds__(256) void k_wgrad_join(muon_act8_wgrad_t op, WgradP
   }
 }
 
-// A matrix of `width`-byte rows at any place, copied to rows of ld_out bytes (a
-// multiple of 16), zeros past each row's end.
-__global__ __launch_bounds__(256) void k_wgrad_copy(const uint8_t* in, int64_t ld_in, int64_t rows, int64_t width, uint8_t* out,
-                                                    int64_t ld_out) {
+// Matrices of `width`-byte rows at any place, copied to rows of ld_out bytes (a
+// multiple of 16), zeros past each row's end; all of a call's in one launch.
+struct Copy {
+  const uint8_t* in;
+  uint8_t* out;
+  int64_t ld_in, width, ld_out;
+  int64_t begin, end;         // blocks of this one, 256 pieces of 16 bytes each
+};
+struct Copies {
+  Copy c[3];
+  int n;
+  int64_t rows;
+};
+__global__ __launch_bounds__(256) void k_wgrad_copy(Copies a) {
   typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
-  const int64_t per = ld_out / 16, units = rows * per;
-  for (int64_t u = blockIdx.x * int64_t(256) + threadIdx.x; u < units; u += int64_t(gridDim.x) * 256) {
-    const int64_t r = u / per, c = (u - r * per) * 16;
-    const uint8_t* p = in + r * ld_in + c;
+  for (int64_t b = blockIdx.x; b < a.c[a.n - 1].end; b += gridDim.x) {
+    int which = 0;
+    while (b >= a.c[which].end) ++which;
+    const Copy& k = a.c[which];
+    const uint32_t per = static_cast<uint32_t>(k.ld_out / 16);
+    const uint64_t first = static_cast<uint64_t>(b - k.begin) * 256, row0 = first / per;   // uniform
+    const uint32_t u = static_cast<uint32_t>(first - row0 * per) + threadIdx.x, dr = u / per;
+    const int64_t r = static_cast<int64_t>(row0 + dr), c = static_cast<int64_t>(u - dr * per) * 16;
+    if (r >= a.rows) continue;
+    const uint8_t* p = k.in + r * k.ld_in + c;
     u32x4 v{0, 0, 0, 0};
-    if (c + 16 <= width) {
+    if (c + 16 <= k.width) {
       v = gld<u32x4_a1>(p);
     } else {
 #pragma unroll
-      for (int b = 0; b < 16; ++b)
-        if (c + b < width) v[b >> 2] |= static_cast<uint32_t>(gld<uint8_t>(p + b)) << (8 * (b & 3));
+      for (int e = 0; e < 16; ++e)
+        if (c + e < k.width) v[e >> 2] |= static_cast<uint32_t>(gld<uint8_t>(p + e)) << (8 * (e & 3));
     }
-    gst<u32x4>(out + r * ld_out + c, v);
+    gst<u32x4>(k.out + r * k.ld_out + c, v);
   }
 }
 
@@ -472,27 +488,28 @@ WgradPlan wgrad_plan(const muon_act8_wgrad_t& op) {
 }
 
 int launch_wgrad_copy(muon_act8_wgrad_t& op, const WgradPlan& p, char* ws, void* stream) {
-  auto copy = [&](const void* in, int64_t ld_in, int64_t width, char* out, int64_t ld_out) {
-    const int64_t blocks = std::min<int64_t>((op.tokens * (ld_out / 16) + 255) / 256, int64_t(1) << 20);
-    hipLaunchKernelGGL(k_wgrad_copy, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream),
-                       static_cast<const uint8_t*>(in), ld_in, op.tokens, width, reinterpret_cast<uint8_t*>(out), ld_out);
+  Copies a{};
+  a.rows = op.tokens;
+  int64_t end = 0;
+  auto add = [&](const void* in, int64_t ld_in, int64_t width, size_t off, int64_t ld_out) {
+    const int64_t begin = end;
+    end += (op.tokens * (ld_out / 16) + 255) / 256;
+    a.c[a.n++] = {static_cast<const uint8_t*>(in), reinterpret_cast<uint8_t*>(ws + off), ld_in, width, ld_out, begin, end};
+    return reinterpret_cast<uint8_t*>(ws + off);
   };
   if (p.copy_dy) {
     const int64_t ld = up(op.n, 8);
-    copy(op.dy, op.ld_dy * 2, op.n * 2, ws + p.dy_off, ld * 2);
-    op.dy = ws + p.dy_off;
+    op.dy = add(op.dy, op.ld_dy * 2, op.n * 2, p.dy_off, ld * 2);
     op.ld_dy = ld;
   }
   if (p.copy_x) {
-    const int64_t ld = up(op.k, 16);
-    copy(op.x8.codes, op.x8.ld_codes, op.k, ws + p.x_off, ld);
-    op.x8.codes = reinterpret_cast<uint8_t*>(ws + p.x_off);
+    const int64_t ld = up(op.k, 16), groups = (op.k + 31) / 32, lds = up(groups, 16);
+    op.x8.codes = add(op.x8.codes, op.x8.ld_codes, op.k, p.x_off, ld);
     op.x8.ld_codes = ld;
-    const int64_t groups = (op.k + 31) / 32, lds = up(groups, 16);
-    copy(op.x8.scales, op.x8.ld_scales, groups, ws + p.s_off, lds);
-    op.x8.scales = reinterpret_cast<uint8_t*>(ws + p.s_off);
+    op.x8.scales = add(op.x8.scales, op.x8.ld_scales, groups, p.s_off, lds);
     op.x8.ld_scales = lds;
   }
+  hipLaunchKernelGGL(k_wgrad_copy, dim3(static_cast<unsigned>(std::min(end, int64_t(1) << 23))), dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return static_cast<int>(hipGetLastError());
 }
 
