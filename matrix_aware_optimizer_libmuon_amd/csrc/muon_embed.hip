@@ -1,11 +1,12 @@
 // Embedding lookup and its gradient (gfx950).
 //
 // The gradient adds the rows of dy by id without atomics, so that its sums do
-// not depend on scheduling.  The tokens are sorted by id with a stable radix
-// sort (9-bit digits, least significant first: two passes up to 262143 rows),
-// which puts each row's tokens side by side and in their own order; k_starts
-// then notes where each row's begin.  Tokens whose id is outside the table take
-// the key `vocab` and end up past every row.
+// not depend on scheduling.  The tokens are sorted by id, which puts each row's
+// side by side and in their own order: up to 32768 of them in one launch
+// (k_embed_buckets), more with a stable radix sort (9-bit digits, least significant
+// first: two passes up to 262143 rows) and k_starts, which notes where each row's
+// begin.  Tokens whose id is outside the table take the key `vocab`, which is no
+// row's.
 //
 // Ids are as frequent as words: a few have thousands of tokens, most none.
 //   Rows of up to kRun tokens (and empty ones, which are written as zeros) are a
@@ -98,11 +99,38 @@ struct SortArgs {
 };
 
 __device__ __forceinline__ uint32_t key_of(const void* ids, int id_bytes, int64_t vocab, int64_t i) {
-  const int64_t id = load_id(ids, id_bytes, i);
-  return static_cast<uint32_t>(id >= 0 && id < vocab ? id : vocab);
+  const uint64_t id = static_cast<uint64_t>(load_id(ids, id_bytes, i));   // negative: past any table
+  return static_cast<uint32_t>(id >> 32) == 0 && static_cast<uint32_t>(id) < static_cast<uint32_t>(vocab)
+             ? static_cast<uint32_t>(id) : static_cast<uint32_t>(vocab);
 }
 __device__ __forceinline__ uint32_t key_in(const SortArgs& a, int64_t i) {
   return a.keys_in ? gld<uint32_t>(a.keys_in + i) : key_of(a.ids, a.id_bytes, a.vocab, i);
+}
+
+// The wave's valid lanes with this lane's digit, by a ballot per digit bit.
+__device__ __forceinline__ uint64_t same_digit(bool valid, uint32_t d) {
+  uint64_t same = __ballot(valid);
+#pragma unroll
+  for (int bit = 0; bit < kDigitBits; ++bit) {
+    const uint64_t on = __ballot((d >> bit) & 1);
+    same &= (d >> bit) & 1 ? on : ~on;
+  }
+  return same;
+}
+
+// Whether that is all of them (lane 0 is valid if any is).
+__device__ __forceinline__ bool one_digit(bool valid, uint32_t d) {
+  return __ballot(valid && d != static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(d))) == 0;
+}
+
+// v of this lane and the lanes before it.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t u = __shfl_up(v, o, 64);
+    v += lane >= o ? u : 0u;
+  }
+  return v;
 }
 
 // Tokens of each digit in each block's share.
@@ -119,8 +147,7 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_count(SortArgs a) {
 }
 
 // Moves each block's share to its place.  A digit's tokens of earlier blocks
-// come first, then those of earlier waves, then in order within the wave: the
-// lanes with one digit find each other by a ballot per digit bit.
+// come first, then those of earlier waves, then in order within the wave.
 __global__ __launch_bounds__(kSortThreads) void k_embed_scatter(SortArgs a) {
   __shared__ uint32_t base[kDigits];                // next place of each digit
   __shared__ uint32_t wcnt[kSortWaves][kDigits];    // a step's tokens by wave, then their places
@@ -146,12 +173,7 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_scatter(SortArgs a) {
       before += base[t];
     }
     // exclusive scan of the totals over the digits
-    uint32_t scan = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t v = __shfl_up(scan, o, 64);
-      scan += lane >= o ? v : 0u;
-    }
+    const uint32_t scan = wave_scan(sum, lane);
     if (lane == 63) wsum[w] = scan;
     __syncthreads();
     if (t < kDigits) {
@@ -174,12 +196,7 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_scatter(SortArgs a) {
       tok = a.toks_in ? gld<uint32_t>(a.toks_in + i) : static_cast<uint32_t>(i);
     }
     const uint32_t d = (key >> a.shift) & (kDigits - 1);
-    uint64_t same = __ballot(valid);
-#pragma unroll
-    for (int bit = 0; bit < kDigitBits; ++bit) {
-      const uint64_t on = __ballot((d >> bit) & 1);
-      same &= (d >> bit) & 1 ? on : ~on;
-    }
+    const uint64_t same = same_digit(valid, d);
     const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
     if (valid && (same >> lane) == 1) wcnt[w][d] = rank + 1;   // the digit's last lane
     __syncthreads();
@@ -203,87 +220,125 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_scatter(SortArgs a) {
   }
 }
 
-// The whole sort of up to kSmall tokens by one block (at 4000 tokens 2 us less
-// than the launches below, at 8000 4 to 5 us more): as k_embed_scatter, the
-// tokens in registers, each wave's share side by side, and moved through LDS.
-constexpr int kSmall = 4 * kSortThreads;
-__global__ __launch_bounds__(kSortThreads) void k_embed_sort(SortArgs a, int passes) {
-  constexpr int E = kSmall / kSortThreads;          // tokens of a thread at most
-  __shared__ uint32_t wcnt[kSortWaves][kDigits];
+// The whole sort in one launch: block b takes the ids whose low bits are b.  It
+// goes over all ids once, noting its own and counting those of lower blocks, so
+// that it knows where its places begin, and orders its own by their high bits.
+// A row's tokens are side by side all the same, and each block writes the starts
+// of its rows, [block][high bits], as it has them.
+//   Against one block alone (up to 4096 tokens) or the launches above and k_starts:
+// 1000 tokens 6.3 for 10.2 us, 4000 6.9 for 16.4, 10010 8.5 for 21.6, 32768 13.0 for
+// 27.3.  An id that has them all is the worst case, one block's work: the whole
+// gradient of 32768 x 64 then takes 76 us for 69, with half of them 50 for 55.  (More
+// tokens would make that worse.)
+constexpr int64_t kBucketTokens = 32 * kSortThreads;   // 32 loads of 64 tokens for a wave: 64 lanes hold their masks
+constexpr uint32_t kHighs = kDigits - 1;               // (what LDS has room for)
+constexpr int kLogBuckets = 8;                         // a block to a CU; for larger tables twice as many
+constexpr int64_t kBucketVocab = (int64_t(1) << (kLogBuckets + 1)) * kHighs - 1;
+template <int ID_BYTES>
+__global__ __launch_bounds__(kSortThreads) void k_embed_buckets(SortArgs a, int log_buckets, uint32_t highs, uint32_t* start) {
+  __shared__ uint16_t list[kBucketTokens], high[kBucketTokens];   // the block's tokens in order, their high bits
+  __shared__ uint32_t wcnt[kSortWaves * kHighs];    // [wave][high]: counts, then places
   __shared__ uint32_t wsum[kSortWaves];
-  __shared__ uint32_t skey[kSmall], stok[kSmall];
-  const int t = static_cast<int>(threadIdx.x), lane = t & 63, w = t >> 6;
-  const int n = static_cast<int>(a.tokens), each = (n + kSortThreads - 1) / kSortThreads;
-  const int base = w * 64 * each + lane;            // + 64 e: this thread's e-th place
-  for (int pass = 0; pass < passes; ++pass) {
-    const int shift = kDigitBits * pass;
-    for (int i = t; i < kSortWaves * kDigits; i += kSortThreads) (&wcnt[0][0])[i] = 0;
-    uint32_t key[E], tok[E], rank[E];
+  const int t = static_cast<int>(threadIdx.x), lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int n = static_cast<int>(a.tokens);
+  const uint32_t low = (1u << log_buckets) - 1;
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+  for (uint32_t i = t; i < kSortWaves * highs; i += kSortThreads) wcnt[i] = 0;
+  // the ids, each wave's share side by side: lanes 2 e and 2 e + 1 keep the mask of
+  // load e's tokens that are the block's
+  const int loads = (n + kSortThreads - 1) / kSortThreads, begin = w * 64 * loads;
+  uint32_t hits = 0, less = 0;
+  auto note = [&](uint32_t key, bool valid, int e) __attribute__((always_inline)) {
+    const uint32_t b = key & low;
+    const uint64_t m = __ballot(valid && b == blockIdx.x);
+    less += __popcll(__ballot(valid && b < blockIdx.x));
+    if (lane >> 1 == e) hits = static_cast<uint32_t>(lane & 1 ? m >> 32 : m);
+  };
+  const int full = min(loads, max(0, n - begin) / 64);   // then a short one, if any
+  constexpr int kAtOnce = 8, kGather = 4;
+  for (int e = 0; e < full; e += kAtOnce) {
+    uint32_t key[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = base + 64 * e;
-      key[e] = tok[e] = rank[e] = 0;
-      if (e < each && i < n) {
-        key[e] = pass ? skey[i] : key_of(a.ids, a.id_bytes, a.vocab, i);
-        tok[e] = pass ? stok[i] : static_cast<uint32_t>(i);
-      }
-    }
-    __syncthreads();                                // the counts are clear, the places read
+    for (int k = 0; k < kAtOnce; ++k) key[k] = key_of(a.ids, ID_BYTES, a.vocab, begin + 64 * min(e + k, full - 1) + lane);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (e >= each) break;
-      const bool valid = base + 64 * e < n;
-      const uint32_t d = (key[e] >> shift) & (kDigits - 1);
-      uint64_t same = __ballot(valid);
-#pragma unroll
-      for (int bit = 0; bit < kDigitBits; ++bit) {
-        const uint64_t on = __ballot((d >> bit) & 1);
-        same &= (d >> bit) & 1 ? on : ~on;
-      }
-      rank[e] = wcnt[w][d] + __popcll(same & ((uint64_t(1) << lane) - 1));
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      if (valid && (same >> lane) == 1) wcnt[w][d] = rank[e] + 1;   // the digit's last lane
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
-    __syncthreads();
-    // first place of each digit, then of each wave's share of it
-    uint32_t sum = 0;
-    if (t < kDigits)
-#pragma unroll
-      for (int k = 0; k < kSortWaves; ++k) sum += wcnt[k][t];
-    uint32_t scan = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t v = __shfl_up(scan, o, 64);
-      scan += lane >= o ? v : 0u;
-    }
-    if (lane == 63) wsum[w] = scan;
-    __syncthreads();
-    if (t < kDigits) {
-      uint32_t run = scan - sum;
-      for (int k = 0; k < w; ++k) run += wsum[k];
-#pragma unroll
-      for (int k = 0; k < kSortWaves; ++k) {
-        const uint32_t c = wcnt[k][t];
-        wcnt[k][t] = run;
-        run += c;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (e < each && base + 64 * e < n) {
-        const uint32_t p = wcnt[w][(key[e] >> shift) & (kDigits - 1)] + rank[e];
-        skey[p] = key[e];
-        stok[p] = tok[e];
-      }
-    __syncthreads();
+    for (int k = 0; k < kAtOnce; ++k)
+      if (k == 0 || e + k < full) note(key[k], true, e + k);
   }
-  for (int i = t; i < n; i += kSortThreads) {
-    gst<uint32_t>(a.keys_out + i, skey[i]);
-    gst<uint32_t>(a.toks_out + i, stok[i]);
+  if (full < loads && begin + 64 * full < n) {
+    const int i = begin + 64 * full + lane;
+    note(key_of(a.ids, ID_BYTES, a.vocab, min(i, n - 1)), i < n, full);
+  }
+  uint32_t before = wave_scan(__popc(hits), lane);  // tokens of this lane and the lanes before it
+  if (lane == 63) wsum[w] = before << 16 | less;    // (2048 at most)
+  before -= __popc(hits);
+  __syncthreads();
+  uint32_t base = 0, count = 0;                     // the block's first place, its tokens
+#pragma unroll
+  for (int k = 0; k < kSortWaves; ++k) {
+    const uint32_t v = wsum[k];
+    base += v & 0xffffu;
+    before += k < w ? v >> 16 : 0u;
+    count += v >> 16;
+  }
+  for (; hits; hits &= hits - 1) list[before++] = static_cast<uint16_t>(begin + 32 * lane + __builtin_ctz(hits));
+  __syncthreads();
+  // the list by high bits, each wave's share of it side by side: counted, then placed
+  const uint32_t each = (count + kSortThreads - 1) / kSortThreads, first = w * 64 * each + lane;
+  uint32_t* const mine = wcnt + w * highs;
+  for (uint32_t e = 0; e < each; e += kGather) {
+    uint32_t d[kGather];
+#pragma unroll
+    for (uint32_t k = 0; k < kGather; ++k)
+      d[k] = key_of(a.ids, ID_BYTES, a.vocab, list[min(first + 64 * (e + k), count - 1)]) >> log_buckets;
+#pragma unroll
+    for (uint32_t k = 0; k < kGather; ++k) {
+      if (k > 0 && e + k >= each) break;
+      const uint32_t i = first + 64 * (e + k);
+      const uint64_t valid = __ballot(i < count);
+      const bool one = one_digit(i < count, d[k]);  // frequent ids: no atomics in one place
+      if (i < count) {
+        high[i] = static_cast<uint16_t>(d[k]);
+        if (!one) atomicAdd(&mine[d[k]], 1u);
+        else if ((valid >> lane) == 1) atomicAdd(&mine[d[k]], static_cast<uint32_t>(__popcll(valid)));
+      }
+    }
+  }
+  __syncthreads();
+  uint32_t cnt[kSortWaves], sum = 0;
+  if (t < static_cast<int>(highs))
+#pragma unroll
+    for (int k = 0; k < kSortWaves; ++k) sum += cnt[k] = wcnt[k * highs + t];
+  uint32_t run = wave_scan(sum, lane);
+  if (lane == 63) wsum[w] = run;
+  __syncthreads();
+  if (t < static_cast<int>(highs)) {
+    run += base - sum;
+#pragma unroll
+    for (int k = 0; k < kDigits / 64; ++k) run += k < w ? wsum[k] : 0u;
+    gst<uint32_t>(start + blockIdx.x * highs + t, run);
+#pragma unroll
+    for (int k = 0; k < kSortWaves; ++k) {
+      wcnt[k * highs + t] = run;
+      run += cnt[k];
+    }
+  }
+  if (blockIdx.x == gridDim.x - 1 && t == 0) gst<uint32_t>(start + gridDim.x * highs, static_cast<uint32_t>(n));
+  __syncthreads();
+  for (uint32_t e = 0; e < each; ++e) {
+    const uint32_t i = first + 64 * e;
+    const bool valid = i < count;
+    const uint32_t d = valid ? high[i] : 0u;
+    const uint64_t same = one_digit(valid, d) ? __ballot(valid) : same_digit(valid, d);
+    const uint32_t p = mine[d] + __popcll(same & below);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (valid) {
+      if ((same >> lane) == 1) mine[d] = p + 1;     // the digit's last lane
+      gst<uint32_t>(a.keys_out + p, d << log_buckets | blockIdx.x);
+      gst<uint32_t>(a.toks_out + p, static_cast<uint32_t>(list[i]));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -385,11 +440,19 @@ __global__ __launch_bounds__(kRowThreads) void k_direct(muon_embed_grad_t op) {
 struct Sorted {
   const uint32_t* keys;
   const uint32_t* toks;
-  const uint32_t* start;
+  const uint32_t* start;        // [low bits of the row][high bits]
+  int log_buckets;              // low bits (0: in the order of the rows)
+  uint32_t highs;
   float* pieces;                // [chunk][left, right][cols]
   int64_t chunks;
   unsigned piece_blocks;        // the launch's first blocks: pieces, the others: rows
 };
+// Where a row's tokens begin and end in the sorted order.
+__device__ __forceinline__ void run_of(const Sorted& a, uint32_t row, uint32_t& begin, uint32_t& end) {
+  const uint32_t* p = a.start + ((row & ((1u << a.log_buckets) - 1)) * a.highs + (row >> a.log_buckets));
+  begin = gld<uint32_t>(p);
+  end = gld<uint32_t>(p + 1);
+}
 
 // The long runs that touch chunk `chunk` of the sorted order, one place per
 // lane: `left`, lanes of a run that began in an earlier chunk, and `right`, lanes
@@ -403,10 +466,7 @@ __device__ __forceinline__ Chunk chunk_runs(const Sorted& a, int64_t tokens, int
   Chunk c;
   c.key = lane < kRun && i < tokens ? gld<uint32_t>(a.keys + i) : static_cast<uint32_t>(vocab);
   c.begin = c.end = 0;
-  if (c.key < vocab) {
-    c.begin = gld<uint32_t>(a.start + c.key);
-    c.end = gld<uint32_t>(a.start + c.key + 1);
-  }
+  if (c.key < vocab) run_of(a, c.key, c.begin, c.end);
   const bool is_long = c.end - c.begin > kRun;
   c.left = __ballot(is_long && c.begin < chunk * kRun);
   c.right = __ballot(is_long && c.begin >= chunk * kRun);
@@ -438,8 +498,9 @@ __device__ __forceinline__ void sum_pieces(const muon_embed_grad_t& op, const So
 template <class S, class T, int TPR>
 __device__ __forceinline__ void sum_row(const muon_embed_grad_t& op, const Sorted& a, int64_t row, int t, int lane) {
   const int cols = static_cast<int>(op.cols);
-  const uint32_t first = gld<uint32_t>(a.start + row);
-  const int len = static_cast<int>(gld<uint32_t>(a.start + row + 1) - first);
+  uint32_t first, end;
+  run_of(a, static_cast<uint32_t>(row), first, end);
+  const int len = static_cast<int>(end - first);
   if (len > kRun) return;                         // k_join's
   if (len == 0) {
     if (op.accumulate) return;
@@ -495,10 +556,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, 
     const int64_t i = at + lane;
     uint32_t key = static_cast<uint32_t>(op.vocab), begin = 0, end = 0;
     if (i < op.tokens) key = gld<uint32_t>(a.keys + i);
-    if (key < op.vocab) {
-      begin = gld<uint32_t>(a.start + key);
-      end = gld<uint32_t>(a.start + key + 1);
-    }
+    if (key < op.vocab) run_of(a, key, begin, end);
     // (the same in all waves)
     for (uint64_t m = __ballot(end - begin > kRun && begin == i); m; m &= m - 1) {
       const int src = __builtin_ctzll(m);
@@ -564,8 +622,13 @@ int by_types(int32_t in, int32_t out, F&& f) {
 EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols) {
   EmbedSortPlan p{};
   if (tokens <= kDirect) return p;
-  for (int64_t top = vocab; top > 0; top >>= kDigitBits) ++p.passes;
-  p.one_block = tokens <= kSmall;
+  if (tokens <= kBucketTokens && vocab <= kBucketVocab) {
+    p.passes = 1;
+    p.log_buckets = kLogBuckets + ((vocab >> kLogBuckets) >= kHighs ? 1 : 0);
+  } else {
+    for (int64_t top = vocab; top > 0; top >>= kDigitBits) ++p.passes;
+  }
+  p.highs = static_cast<uint32_t>((vocab >> p.log_buckets) + 1);
   // at most 256 blocks, whole steps each
   p.block_tokens = kSortThreads * ((tokens + kSortThreads * 256 - 1) / (kSortThreads * 256));
   p.blocks = (tokens + p.block_tokens - 1) / p.block_tokens;
@@ -576,12 +639,12 @@ EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols) {
     off = up256(off + static_cast<size_t>(n) * 4);
     return at;
   };
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < std::min(p.passes, 2); ++k) {
     p.keys_off[k] = take(tokens);
     p.toks_off[k] = take(tokens);
   }
-  p.count_off = take(p.blocks * kDigits);
-  p.start_off = take(vocab + 1);
+  if (!p.log_buckets) p.count_off = take(p.blocks * kDigits);
+  p.start_off = take((int64_t(p.highs) << p.log_buckets) + 1);
   p.pieces_off = take(p.chunks * 2 * cols);
   p.bytes = off;
   return p;
@@ -596,9 +659,12 @@ int launch_embed(const muon_embed_t& op, void* stream) {
   });
 }
 
-int launch_embed_sort(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
-  hipLaunchKernelGGL(k_embed_sort, dim3(1), dim3(kSortThreads), 0, static_cast<hipStream_t>(stream),
-                     sort_args(op, p, p.passes - 1, ws), p.passes);
+int launch_embed_buckets(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
+  const dim3 grid(1u << p.log_buckets), block(kSortThreads);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const SortArgs a = sort_args(op, p, 0, ws);
+  if (op.id_bytes == 8) hipLaunchKernelGGL((k_embed_buckets<8>), grid, block, 0, st, a, p.log_buckets, p.highs, p.starts(ws));
+  else hipLaunchKernelGGL((k_embed_buckets<4>), grid, block, 0, st, a, p.log_buckets, p.highs, p.starts(ws));
   return static_cast<int>(hipGetLastError());
 }
 
@@ -627,6 +693,8 @@ Sorted sorted(const EmbedSortPlan& p, char* ws) {
   a.keys = p.keys(ws);
   a.toks = p.toks(ws);
   a.start = p.starts(ws);
+  a.log_buckets = p.log_buckets;
+  a.highs = p.highs;
   a.pieces = p.pieces(ws);
   a.chunks = p.chunks;
   a.piece_blocks = 0;

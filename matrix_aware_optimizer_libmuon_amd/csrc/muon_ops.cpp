@@ -330,13 +330,15 @@ int muon_embed_grad(const muon_embed_grad_t* op, void* workspace, size_t workspa
   char* ws = static_cast<char*>(workspace);
   if (p.passes == 0)
     return l.run("embedding gradient", [&](void* st) { return launch_embed_sums(*op, p, ws, st); });
-  if (p.one_block)
-    if (int rc = l.run("token sort", [&](void* st) { return launch_embed_sort(*op, p, ws, st); })) return rc;
-  for (int pass = 0; pass < p.passes && !p.one_block; ++pass) {
-    if (int rc = l.run("token sort, count", [&](void* st) { return launch_embed_count(*op, p, pass, ws, st); })) return rc;
-    if (int rc = l.run("token sort, scatter", [&](void* st) { return launch_embed_scatter(*op, p, pass, ws, st); })) return rc;
+  if (p.log_buckets) {
+    if (int rc = l.run("token sort", [&](void* st) { return launch_embed_buckets(*op, p, ws, st); })) return rc;
+  } else {
+    for (int pass = 0; pass < p.passes; ++pass) {
+      if (int rc = l.run("token sort, count", [&](void* st) { return launch_embed_count(*op, p, pass, ws, st); })) return rc;
+      if (int rc = l.run("token sort, scatter", [&](void* st) { return launch_embed_scatter(*op, p, pass, ws, st); })) return rc;
+    }
+    if (int rc = l.run("embedding gradient, starts", [&](void* st) { return launch_embed_starts(*op, p, ws, st); })) return rc;
   }
-  if (int rc = l.run("embedding gradient, starts", [&](void* st) { return launch_embed_starts(*op, p, ws, st); })) return rc;
   if (int rc = l.run("embedding gradient, sums", [&](void* st) { return launch_embed_sums(*op, p, ws, st); })) return rc;
   return l.run("embedding gradient, join", [&](void* st) { return launch_embed_join(*op, p, ws, st); });
 }

@@ -54,7 +54,8 @@ int launch_wgrad_join(const muon_act8_wgrad_t& op, const WgradPlan& p, const cha
 // row's first place, the sums of the long runs' pieces.
 struct EmbedSortPlan {
   int passes;                 // digits of the keys 0 .. vocab (0: not sorted)
-  bool one_block;             // few enough for one block to sort them in one launch
+  int log_buckets;            // sorted in one launch, by the low bits of the ids (0: digit by digit)
+  uint32_t highs;             // values of the other bits
   int64_t blocks;             // blocks of a pass, block_tokens tokens each
   int64_t block_tokens;
   int64_t chunks;             // pieces of long runs lie in one chunk
@@ -68,7 +69,7 @@ struct EmbedSortPlan {
 };
 EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols);
 int launch_embed(const muon_embed_t& op, void* stream);
-int launch_embed_sort(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
+int launch_embed_buckets(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
 int launch_embed_count(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream);
 int launch_embed_scatter(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws, void* stream);
 int launch_embed_starts(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);

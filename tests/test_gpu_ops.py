@@ -414,7 +414,7 @@ def embed_ids(kind, tokens, vocab):
 
 @pytest.mark.parametrize("kind", ["uniform", "one", "none", "far", "skewed"])
 @pytest.mark.parametrize("tokens,vocab,cols", [(1, 1, 8), (2, 7, 5), (63, 100, 64), (65, 1, 40), (200, 255, 33), (700, 256, 72),
-                                               (1500, 65536, 16), (4097, 300, 520), (9001, 70000, 24), (20000, 1000, 8)])
+                                               (1500, 65536, 16), (4097, 300, 520), (9001, 70000, 24), (20000, 1000, 8), (32768, 2000, 8)])
 def test_embed_gradient_is_exact_on_integers(kind, tokens, vocab, cols):
     ids = embed_ids(kind, tokens, vocab)
     dy = torch.randint(-8, 9, (tokens, cols), generator=gen(7)).float()
@@ -431,9 +431,11 @@ def test_embed_gradient_is_exact_on_integers(kind, tokens, vocab, cols):
     assert torch.equal(out.cpu().double(), want + base.double())
 
 
-@pytest.mark.parametrize("tokens,vocab", [(256, 40), (257, 40), (4096, 600), (4097, 600), (262144, 3000), (262145, 3000), (700001, 300000)])
+@pytest.mark.parametrize("tokens,vocab", [(256, 40), (257, 40), (4096, 600), (4097, 600), (262144, 3000), (262145, 3000), (700001, 300000),
+                                          (32768, 255), (32768, 256), (32769, 256), (3000, 130815), (3000, 130816), (3000, 261631),
+                                          (3000, 261632), (32767, 261631)])
 def test_embed_gradient_at_the_sort_s_limits(tokens, vocab):
-    """Unsorted, one block, one step a block, several steps a block."""
+    """Unsorted, one launch (with 256 and 512 blocks), one step a block, several steps a block."""
     g = gen(tokens)
     ids = (torch.rand(tokens, generator=g) ** 3 * vocab).long()
     ids[torch.rand(tokens, generator=g) < 0.1] = -7
