@@ -227,9 +227,8 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_scatter(SortArgs a) {
 // of its rows, [block][high bits], as it has them.
 //   Against one block alone (up to 4096 tokens) or the launches above and k_starts:
 // 1000 tokens 6.3 for 10.2 us, 4000 6.9 for 16.4, 10010 8.5 for 21.6, 32768 13.0 for
-// 27.3.  An id that has them all is the worst case, one block's work: the whole
-// gradient of 32768 x 64 then takes 76 us for 69, with half of them 50 for 55.  (More
-// tokens would make that worse.)
+// 27.3.  An id that has them all is the worst case, one block's work: the sort then
+// costs 7 us more than by digits at 32768 tokens (and would cost more with more).
 constexpr int64_t kBucketTokens = 32 * kSortThreads;   // 32 loads of 64 tokens for a wave: 64 lanes hold their masks
 constexpr uint32_t kHighs = kDigits - 1;               // (what LDS has room for)
 constexpr int kLogBuckets = 8;                         // a block to a CU; for larger tables twice as many
@@ -544,11 +543,13 @@ __global__ __launch_bounds__(kRowThreads) void k_sums(muon_embed_grad_t op, Sort
 
 // The long runs that begin among 64 places of the sorted order: their pieces,
 // 512 columns from 512 blockIdx.y.  The waves take consecutive shares of a run's
-// pieces, which are added in order.
-constexpr int kJoinWaves = 4;
-template <class T>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, Sorted a) {
-  __shared__ float red[kJoinWaves][512];
+// pieces, which are added in order.  8 waves where a row is one block's: a run of all
+// of 32768 x 64 takes 59 us (with 4: 76) for the whole gradient, 10010 x 150 43 (58);
+// 4 for wider rows, where the many blocks without a run count (32768 x 4096: 182 us,
+// with 8: 185).
+template <class T, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_join(muon_embed_grad_t op, Sorted a) {
+  __shared__ float red[WAVES][512];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int cols = static_cast<int>(op.cols);
   const int c = static_cast<int>(blockIdx.y) * 512 + lane * 8;
@@ -563,7 +564,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, 
       const int64_t row = static_cast<uint32_t>(__builtin_amdgcn_readlane(key, src));
       const int64_t chunk = (at + src) / kRun;
       const int64_t last = (static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(end, src))) - 1) / kRun;
-      const int n = static_cast<int>(last - chunk + 1), per = (n + kJoinWaves - 1) / kJoinWaves;
+      const int n = static_cast<int>(last - chunk + 1), per = (n + WAVES - 1) / WAVES;
       const int to = min((w + 1) * per, n);
       float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
@@ -580,7 +581,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_join(muon_embed_grad_t op, 
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           s[j] = 0.f;
-          for (int k = 0; k < kJoinWaves; ++k) s[j] += red[k][j * 64 + lane];
+          for (int k = 0; k < WAVES; ++k) s[j] += red[k][j * 64 + lane];
         }
         put_row<T>(op, row, c, s);
       }
@@ -728,8 +729,9 @@ int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char*
 int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
   const dim3 grid(static_cast<unsigned>(std::min((op.tokens + 63) / 64, kMaxGrid)), static_cast<unsigned>((op.cols + 511) / 512));
   return by_types(op.dy_dtype, op.table_dtype, [&](auto, auto t) {
-    hipLaunchKernelGGL((k_join<decltype(t)>), grid, dim3(64 * kJoinWaves), 0, static_cast<hipStream_t>(stream), op,
-                       sorted(p, ws));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (op.cols > 512) hipLaunchKernelGGL((k_join<decltype(t), 4>), grid, dim3(64 * 4), 0, st, op, sorted(p, ws));
+    else hipLaunchKernelGGL((k_join<decltype(t), 8>), grid, dim3(64 * 8), 0, st, op, sorted(p, ws));
     return static_cast<int>(hipGetLastError());
   });
 }
