@@ -590,8 +590,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_join(muon_embed_grad_t op, Sorte
   }
 }
 
-// threads of a grid stay below 2^32
-constexpr int64_t kMaxGrid = int64_t(1) << 23;
+// Blocks of a grid of `threads` each: its threads stay below 2^32, whatever the block.
+constexpr int64_t max_grid(int64_t threads) { return (int64_t(1) << 31) / threads; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 SortArgs sort_args(const muon_embed_grad_t& op, const EmbedSortPlan& p, int pass, char* ws) {
@@ -654,7 +654,7 @@ EmbedSortPlan embed_sort_plan(int64_t tokens, int64_t vocab, int64_t cols) {
 int launch_embed(const muon_embed_t& op, void* stream) {
   const int64_t vpr = (op.cols + 7) / 8, blocks = (op.tokens * vpr + kRowThreads * kVecs - 1) / (kRowThreads * kVecs);
   return by_types(op.table_dtype, op.out_dtype, [&](auto s, auto t) {
-    hipLaunchKernelGGL((k_embed<decltype(s), decltype(t)>), dim3(static_cast<unsigned>(std::min(blocks, kMaxGrid))),
+    hipLaunchKernelGGL((k_embed<decltype(s), decltype(t)>), dim3(static_cast<unsigned>(std::min(blocks, max_grid(kRowThreads)))),
                        dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), op, blocks);
     return static_cast<int>(hipGetLastError());
   });
@@ -706,7 +706,7 @@ Sorted sorted(const EmbedSortPlan& p, char* ws) {
 int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
   const bool direct = p.passes == 0, wide = op.cols > 512;
   const int64_t per_block = (wide ? 1 : 4) * (direct ? kRowsEach : 1);
-  const int64_t row_blocks = std::min((op.vocab + per_block - 1) / per_block, kMaxGrid / 2);
+  const int64_t row_blocks = std::min((op.vocab + per_block - 1) / per_block, max_grid(kRowThreads) / 2);
   return by_types(op.dy_dtype, op.table_dtype, [&](auto s, auto t) {
     using S = decltype(s);
     using T = decltype(t);
@@ -717,7 +717,7 @@ int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char*
       else hipLaunchKernelGGL((k_direct<S, T, 64>), grid, dim3(kRowThreads), 0, st, op);
     } else {
       Sorted a = sorted(p, ws);
-      a.piece_blocks = static_cast<unsigned>(std::min((p.chunks * ((op.cols + 511) / 512) + 3) / 4, kMaxGrid / 2));
+      a.piece_blocks = static_cast<unsigned>(std::min((p.chunks * ((op.cols + 511) / 512) + 3) / 4, max_grid(kRowThreads) / 2));
       const dim3 grid(a.piece_blocks + static_cast<unsigned>(row_blocks));
       if (wide) hipLaunchKernelGGL((k_sums<S, T, 256>), grid, dim3(kRowThreads), 0, st, op, a);
       else hipLaunchKernelGGL((k_sums<S, T, 64>), grid, dim3(kRowThreads), 0, st, op, a);
@@ -727,11 +727,12 @@ int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char*
 }
 
 int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream) {
-  const dim3 grid(static_cast<unsigned>(std::min((op.tokens + 63) / 64, kMaxGrid)), static_cast<unsigned>((op.cols + 511) / 512));
+  const int threads = 64 * (op.cols > 512 ? 4 : 8);
+  const dim3 grid(static_cast<unsigned>(std::min((op.tokens + 63) / 64, max_grid(threads))), static_cast<unsigned>((op.cols + 511) / 512));
   return by_types(op.dy_dtype, op.table_dtype, [&](auto, auto t) {
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (op.cols > 512) hipLaunchKernelGGL((k_join<decltype(t), 4>), grid, dim3(64 * 4), 0, st, op, sorted(p, ws));
-    else hipLaunchKernelGGL((k_join<decltype(t), 8>), grid, dim3(64 * 8), 0, st, op, sorted(p, ws));
+    if (op.cols > 512) hipLaunchKernelGGL((k_join<decltype(t), 4>), grid, dim3(threads), 0, st, op, sorted(p, ws));
+    else hipLaunchKernelGGL((k_join<decltype(t), 8>), grid, dim3(threads), 0, st, op, sorted(p, ws));
     return static_cast<int>(hipGetLastError());
   });
 }
