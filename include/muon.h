@@ -546,7 +546,8 @@ int muon_embed(const muon_embed_t* op, hipStream_t stream);
 
 /* Its gradient, from the tokens sorted by id:
  *   dtable[v] (+)= scale * sum over t with ids[t] == v of dy[t]
- * every row is written (zeros where no token has its id) unless accumulate.
+ * every row is written (zeros where no token has its id), except that with
+ * accumulate only the rows that have tokens are read and written.
  *   dy        tokens x cols, dy_dtype;  dtable  vocab x cols, table_dtype
  *   workspace muon_embed_grad_workspace_bytes(tokens, vocab, cols) bytes,
  *             256-byte aligned */

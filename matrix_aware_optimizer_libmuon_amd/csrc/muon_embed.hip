@@ -417,7 +417,13 @@ __global__ __launch_bounds__(kRowThreads) void k_direct(muon_embed_grad_t op) {
   }
   for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kRowThreads / TPR) + group) * kRowsEach; row0 < op.vocab;
        row0 += static_cast<int64_t>(gridDim.x) * (kRowThreads / TPR) * kRowsEach)
-    for (int r = 0; r < kRowsEach && row0 + r < op.vocab; ++r)
+    for (int r = 0; r < kRowsEach && row0 + r < op.vocab; ++r) {
+      if (op.accumulate) {   // a row without tokens is neither read nor written
+        bool mine = false;
+#pragma unroll
+        for (int q = 0; q < kDirect / 64; ++q) mine |= key[q] == static_cast<uint32_t>(row0 + r);
+        if (!__ballot(mine)) continue;
+      }
       for (int c0 = 0; c0 < cols; c0 += TPR * 8) {
         const int c = c0 + t * 8;
         float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -433,6 +439,7 @@ __global__ __launch_bounds__(kRowThreads) void k_direct(muon_embed_grad_t op) {
         }
         put_row<T>(op, row0 + r, c, s);
       }
+    }
 }
 
 // What the sums of sorted tokens work on.

@@ -135,5 +135,6 @@ def embed_grad(dy, ids, vocab: int, *, scale: float = 1.0, out=None, dtype=torch
                stream=None):
     """The gradient of embed()'s table (vocab x cols): scale * the sum of the
     rows of dy with each id, in an order that depends on the ids alone.  Every
-    row of the result is written, or with ``accumulate`` added to ``out``."""
+    row of the result is written; with ``accumulate`` the sums are added to
+    ``out``, of which only the rows that have tokens are touched."""
     return _run("embed_grad", dy, stream, dy, ids, int(vocab), float(scale), out, dtype, bool(accumulate))[0]
