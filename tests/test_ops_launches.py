@@ -25,3 +25,15 @@ def test_the_largest_sizes_can_be_launched(entry, args):
         for g, b in zip(grid, block):
             assert 0 < g * b < 1 << 32, (kernel, grid, block)
     assert status == 0
+
+
+def test_embedding_gradient_kernels_of_the_tested_sizes():
+    from tests.test_gpu_ops_paths import WIDE, WIDE_SORTED
+    got = record([("embed_grad", dict(tokens=t, vocab=v, cols=c)) for t, v, c in WIDE + WIDE_SORTED])
+    for (tokens, vocab, cols), (status, launches) in zip(WIDE + WIDE_SORTED, got):
+        assert status == 0
+        if (tokens, vocab, cols) in WIDE:
+            assert [kernel for kernel, _, _ in launches] == ["k_direct<float, float, 256>"]
+        else:
+            assert [kernel for kernel, _, _ in launches] == ["k_embed_buckets<4>", "k_sums<float, float, 256>", "k_join<float, 4>"]
+            assert launches[2][1][1] == -(-cols // 512) > 4
