@@ -7,7 +7,7 @@ import torch
 
 import matrix_aware_optimizer_libmuon_amd as muon
 from tests.gpu_helpers import DEV
-from tests.test_gpu_ops import TYPES, embed_ids, gen, ids_of, on_gpu
+from tests.test_gpu_ops import TYPES, embed_ids, gen, ids_of, int_case, on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,41 @@ def test_embed_gradient_of_wide_rows_is_exact_on_integers(kind, tokens, vocab, c
             out = on_gpu(base.to(dst), "odd")
             muon.embed_grad(on_gpu(dy.to(src), "odd"), ids.int().to(DEV), vocab, scale=0.5, out=out, accumulate=True)
             assert torch.equal(out.cpu(), (want + base.double()).float().to(dst)), (src, dst)
+
+
+# ------------------------------------------------- weight gradient, every plan ----
+# (tokens, n, k) by the tiles they take; some of the tiles whole and the last ones in token ranges, all whole, or all in ranges
+WGRAD_PLANS = [(2049, 4352, 4100), (2049, 4353, 4101), (9000, 2100, 2100), (3100, 4096, 4608),         # 256 x 256
+               (1000, 2048, 2304), (1001, 2047, 2301), (3000, 1104, 1296), (3001, 1101, 1303), (4000, 3000, 3000),  # 256 x 128
+               (2383, 5955, 1406), (6000, 520, 264)]                                                # 128 x 128
+
+
+@pytest.mark.parametrize("tokens,n,k", WGRAD_PLANS)
+def test_wgrad_of_every_plan_is_exact_on_integers(tokens, n, k):
+    dy, x = int_case(tokens, n, k)
+    want = dy.to(DEV).double().t().contiguous() @ x.to(DEV).double()
+    x8 = muon.act8_pack(x.to(DEV))
+    dy = dy.to(DEV)
+    assert torch.equal(muon.act8_wgrad(dy, x8).double(), want)
+    assert torch.equal(muon.act8_wgrad(dy, x8, dtype=torch.bfloat16), want.float().bfloat16())
+    gain = torch.exp2(torch.randint(-1, 2, (k,), generator=gen(5)).float()).to(DEV)
+    base = torch.randint(-50, 50, (n, k), generator=gen(6)).float()
+    for dtype in TYPES:                            # added to what is there, in a strided output
+        out = on_gpu(base.to(dtype), "odd")
+        muon.act8_wgrad(dy, x8, col_gain=gain, out=out, accumulate=True)
+        assert torch.equal(out, (base.to(DEV).double() + want * gain).float().to(dtype))
+
+
+@pytest.mark.parametrize("tokens,n,k", [(1, 80, 96), (33, 80, 96), (255, 264, 520), (4097, 24, 40), (2049, 4352, 4100), (3001, 1104, 1296)])
+def test_wgrad_ends_with_the_last_token(tokens, n, k):
+    """The loads reach past the last token; what lies there in the same buffers, NaN and the largest scale, must not count."""
+    dy, x = int_case(tokens, n, k)
+    want = dy.to(DEV).double().t().contiguous() @ x.to(DEV).double()
+    x8 = muon.act8_pack(x.to(DEV))
+    more = 256                                     # rows behind the last token, more than the loads run ahead
+    dys = torch.full((tokens + more, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+    codes = torch.full((tokens + more, -(-k // 32) * 32), 0x7F, dtype=torch.uint8, device=DEV)
+    scales = torch.full((tokens + more, -(-k // 32)), 255, dtype=torch.uint8, device=DEV)
+    dys[:tokens], codes[:tokens, :k], scales[:tokens] = dy.to(DEV), x8.codes.view(torch.uint8), x8.scales
+    got = muon.act8_wgrad(dys[:tokens], muon.Act8(codes.view(torch.float8_e4m3fn)[:tokens, :k], scales[:tokens]))
+    assert torch.equal(got.double(), want)
