@@ -2,12 +2,14 @@
 variants that only certain sizes select (tests/test_ops_launches.py names the
 kernels that each size takes), rows that have to be left alone, extremes.
 Tolerances as there; sums of integers have to be equal."""
+import numpy as np
 import pytest
 import torch
 
 import matrix_aware_optimizer_libmuon_amd as muon
+from oracle import ops_oracle as O
 from tests.gpu_helpers import DEV
-from tests.test_gpu_ops import TYPES, embed_ids, gen, ids_of, int_case, on_gpu
+from tests.test_gpu_ops import GATE, TYPES, U, check_pack_near, embed_ids, gen, ids_of, int_case, near, np64, on_gpu, randn, values
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +99,33 @@ def test_wgrad_ends_with_the_last_token(tokens, n, k):
     dys[:tokens], codes[:tokens, :k], scales[:tokens] = dy.to(DEV), x8.codes.view(torch.uint8), x8.scales
     got = muon.act8_wgrad(dys[:tokens], muon.Act8(codes.view(torch.float8_e4m3fn)[:tokens, :k], scales[:tokens]))
     assert torch.equal(got.double(), want)
+
+
+# ------------------------------------------------------------------ extremes ----
+def near_relative(got, ref, rel):
+    """fp32 results of normal size within rel of the 64-bit ones, without an absolute allowance."""
+    assert np.abs(ref).min() > 2.0 ** -120
+    near_ = np.abs(np64(got) - ref) <= (rel + U) * np.abs(ref)
+    assert near_.all(), (np64(got)[~near_], ref[~near_])
+
+
+def test_gate_of_very_negative_values():
+    """1 + exp(-gate) above 2^126, where its reciprocal is subnormal, against factors that bring the results back:
+    the results are normal numbers and have to be right relative to themselves."""
+    g = torch.tensor([[-87.25, -87.375, -87.5, -87.75, -88.0, -88.25, -88.5, -88.625]])
+    u = torch.full_like(g, 2.0 ** 100)
+    a = muon.swiglu_act8(g.to(DEV), u.to(DEV), save=False)
+    near_relative(a, O.swiglu(np64(g), np64(u)), GATE)
+    # backward: -88 is the one value of these that 8 bits hold
+    g = torch.full((1, 32), -88.0)
+    u = torch.full_like(g, 2.0 ** 100)
+    da = torch.full_like(g, 2.0 ** 10) * (1.0 + torch.arange(32) / 64)
+    _, gate8, up8 = muon.swiglu_act8(g.to(DEV), u.to(DEV))
+    assert np.array_equal(values(gate8), np64(g)) and np.array_equal(values(up8), np64(u))
+    dgate, _, a8 = muon.swiglu_act8_grad(da.to(DEV), gate8, up8)
+    dgo, _, ao = O.swiglu_grad(np64(da), np64(g), np64(u))
+    near_relative(dgate, dgo, 2 * GATE)             # (two terms of opposite sign, the larger 88 times the smaller)
+    check_pack_near(a8, ao, GATE)
+    da = torch.full_like(g, 2.0 ** 100)
+    _, dup, _ = muon.swiglu_act8_grad(da.to(DEV), gate8, up8)
+    near_relative(dup, O.swiglu_grad(np64(da), np64(g), np64(u))[1], GATE)
