@@ -224,3 +224,21 @@ def test_binding_refuses_cpu_tensors(lib):
             call()
     with pytest.raises(AttributeError):
         muon.no_such_operator
+
+
+@pytest.mark.parametrize("tokens,vocab,passes,log_buckets", [
+    (256, 1000, 0, 0), (257, 1000, 1, 8), (32768, 130815, 1, 8), (32768, 130816, 1, 9), (32768, 261631, 1, 9),
+    (32768, 261632, 2, 0), (32769, 511, 1, 0), (32769, 512, 2, 0), (32769, 262143, 2, 0), (32769, 262144, 3, 0), (700001, 300000, 3, 0)])
+@pytest.mark.parametrize("cols", [1, 40, 4099])
+def test_embedding_gradient_workspace_is_the_sum_of_its_parts(lib, tokens, vocab, passes, log_buckets, cols):
+    """Keys and tokens, once per pass but at most twice; the digits' counts of a sort by digits; the rows' first places;
+    two sums per 32 tokens.  Each part 256-byte aligned."""
+    up = lambda n: -(-4 * n // 256) * 256  # noqa: E731
+    want = 0
+    if passes:
+        want = min(passes, 2) * 2 * up(tokens)
+        if not log_buckets:
+            step = 1024 * -(-tokens // (1024 * 256))
+            want += up(-(-tokens // step) * 512)
+        want += up((((vocab >> log_buckets) + 1) << log_buckets) + 1) + up(-(-tokens // 32) * 2 * cols)
+    assert lib.muon_embed_grad_workspace_bytes(tokens, vocab, cols) == want
