@@ -380,8 +380,9 @@ int muon_adamw_step(const muon_adamw_tensor_t* tensors, int64_t n_tensors, float
  * the launches.  They may be captured into a graph, and the structs are read
  * during the call only.  Outputs must not overlap each other or an input
  * (MUON_EALIAS; column slices of one buffer with one row stride do not).
- * Sums run in fp32 in an order that depends on the shapes alone: the same
- * call on the same values gives the same bits.  Errors, the stream's device
+ * Sums run in fp32 in an order fixed by the sizes, the strides and alignments
+ * (which decide how the weight gradient is cut) and, in the embedding's
+ * gradient, the ids: the same call on the same values gives the same bits.  Errors, the stream's device
  * and MUON_DEBUG are as for muon_step (under MUON_DEBUG a workspace is filled
  * with NaN first; on a capturing stream the variable is ignored).  Phase
  * timing does not record them.

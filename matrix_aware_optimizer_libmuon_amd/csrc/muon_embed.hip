@@ -2,23 +2,24 @@
 //
 // The gradient adds the rows of dy by id without atomics, so that its sums do
 // not depend on scheduling.  The tokens are sorted by id, which puts each row's
-// side by side and in their own order: up to 32768 of them in one launch
-// (k_embed_buckets), more with a stable radix sort (9-bit digits, least significant
-// first: two passes up to 262143 rows) and k_starts, which notes where each row's
-// begin.  Tokens whose id is outside the table take the key `vocab`, which is no
-// row's.
+// side by side and in their own order: up to 32768 of them, in tables of up to
+// 261631 rows, in one launch (k_embed_buckets); else with a stable radix sort (9-bit
+// digits, least significant first: two passes up to 262143 rows) and k_starts, which
+// notes where each row's begin.  Tokens whose id is outside the table take the key
+// `vocab`, which is no row's.
 //
 // Ids are as frequent as words: a few have thousands of tokens, most none.
-//   Rows of up to kRun tokens (and empty ones, which are written as zeros) are a
-//   wave's or a block's, one each (4 or 8 each were 4 and 8 % slower: too few
-//   independent loads).
+//   Rows of up to kRun tokens (and empty ones, which are written as zeros unless the
+//   sums are added to what is there) are a wave's or a block's, one each (4 or 8 each
+//   were 4 and 8 % slower: too few independent loads).
 //   Longer runs are cut where the sorted order passes a multiple of kRun: each
 //   piece is summed into the workspace (by blocks of the same launch, k_sums), and
 //   k_join adds a run's pieces in order.  A piece lies in one chunk of kRun
 //   places; a chunk can hold two of them, the end of one run and the beginning of
 //   another.
 // Up to kDirect tokens none of that is needed: each wave of k_direct finds its
-// rows' tokens by comparing all ids.
+// rows' tokens by comparing all ids; it walks the whole table, also when it adds to
+// what is there and leaves the other rows alone.
 //
 // Bound by memory: dy is read once, the table's gradient written once.
 #include <algorithm>

@@ -212,7 +212,9 @@ __global__ __launch_bounds__(kDgainThreads) void k_dgain(const float* partial, i
 
 // f(RT, VPL) for the layout of a row: one vector a thread up to 8192 columns
 // (two a thread, with half the threads, need twice the registers: 115 us instead
-// of 90 for the backward pass of 16384 x 4096 bf16).
+// of 90 for the backward pass of 16384 x 4096 bf16).  Past 8192 columns there are no
+// more threads to take: two vectors each, where the backward pass needs more than the
+// 128 registers a thread then has, and spills (80 bytes a lane in bf16, 120 in fp32).
 template <class F>
 int by_width(int64_t cols, F&& f) {
   if (cols <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});

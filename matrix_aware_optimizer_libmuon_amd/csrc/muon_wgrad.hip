@@ -402,9 +402,12 @@ namespace {
 // the chip full, or with one block to a CU (us).  Larger tiles read less from LDS
 // per product, smaller ones waste less of a matrix and need fewer token ranges;
 // measured, in the order of the table (us):
-//   8192 x 4096 x 4096   213  262  297        16384 x 768 x 1536    55   52   59
-//   8192 x 4096 x 1024    77   81   89        16001 x  80 x 1536    29   26   21
-//   4096 x 2048 x 2048    53   49   51          256 x 256 x  768    24   15   10
+//   8192 x 4096 x 4096   231  281  310        16384 x 768 x 1536    56   54   59
+//   8192 x 4096 x 1024    77   79   88        16001 x  80 x 1536    30   26   21
+//   4096 x 2048 x 2048    53   49   51          256 x 256 x  768    25   16    9
+// The estimate takes the fastest of the three but for 8192 x 4096 x 1024 (256 x 128,
+// 2 % slower) and 4096 x 2048 x 2048 (128 x 128, 3 % slower): it overrates what
+// token ranges cost.
 struct WgradTile {
   int tn, tk;
   int64_t slots;

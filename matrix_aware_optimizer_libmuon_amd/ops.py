@@ -12,7 +12,9 @@ runs in libmuon.so, on the current stream of the tensors' device, or on
     table_grad = muon.embed_grad(dx, ids, vocab)
 
 Matrices are 2-D with unit column stride, float32 or bfloat16; rows may be
-strided (a column slice of a wider buffer is one).
+strided (a column slice of a wider buffer is one).  The operators take no part in
+autograd: what they return has no history, whether or not an argument requires a
+gradient; the backward pass is called, as examples/train_act8.py does.
 """
 from __future__ import annotations
 
