@@ -6,6 +6,7 @@ a GPU (launch_recorder.cpp).
 (kernel with its template arguments, grid, block).  A call's matrices lie at
 made-up addresses far apart, which nothing reads; its workspace has the size that
 the library asks for."""
+import atexit
 import ctypes
 import functools
 import json
@@ -25,7 +26,9 @@ def _recorder():
     cxx = shutil.which("g++")
     if cxx is None:
         return None
-    out = os.path.join(tempfile.mkdtemp(prefix="launch_recorder"), "recorder.so")
+    where = tempfile.mkdtemp(prefix="launch_recorder")
+    atexit.register(shutil.rmtree, where, ignore_errors=True)
+    out = os.path.join(where, "recorder.so")
     r = subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-shared", "-fPIC", os.path.join(ROOT, "tests", "launch_recorder.cpp"),
                         "-o", out], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
