@@ -286,7 +286,8 @@ def _plain_policy(s):
         d = s["ref"].double() - logp
         loss = loss + KL_COEF * (torch.expm1(d) - d)
         g = g - KL_COEF * torch.expm1(d)
-    out = dict(loss=(w * loss).float(), logp=logp.float())
+    # tokens of weight 0 take no part: their log-probabilities are 0 like their losses
+    out = dict(loss=(w * loss).float(), logp=torch.where(w != 0, logp, torch.zeros_like(logp)).float())
     if c["grad"]:
         g = (w * g)[:, None].float()
         p = e.div_(total.float()).mul_(-g)
@@ -390,7 +391,7 @@ def exact(case, seed):
             gap = s["ref"][rows].double() - logp
             loss = loss + KL_COEF * (torch.exp(gap) - gap - 1)
             slope = slope + KL_COEF * (1 - torch.exp(gap))
-        out["loss"][rows], out["logp"][rows] = w * loss, logp
+        out["loss"][rows], out["logp"][rows] = w * loss, logp * (w != 0)
         if case["grad"]:
             grad = torch.exp(logq) * -(w * slope)[:, None]
             grad[here, ids] += w * slope
