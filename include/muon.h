@@ -369,6 +369,8 @@ int muon_adamw_step(const muon_adamw_tensor_t* tensors, int64_t n_tensors, float
  *   muon_act8_pack / _unpack    the 8-bit form of any matrix, and back
  *   muon_act8_wgrad             weight gradient dY^T X from an 8-bit X
  *   muon_embed / _grad          embedding lookup and its gradient
+ *   muon_attention / _grad      attention over sequences of any lengths
+ *   muon_distill, muon_policy   losses with the gradient of the logits
  *
  * Matrices are row-major with unit column stride; each has its own row
  * stride ("ld", in elements, >= the row's length; not read where there is one
@@ -567,6 +569,140 @@ typedef struct {
 size_t muon_embed_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols);
 int muon_embed_grad(const muon_embed_grad_t* op, void* workspace, size_t workspace_bytes,
                     hipStream_t stream);
+
+/* A bf16 tensor of tokens x heads x dim: element (t, h, d) at
+ * data[t ld_token + h ld_head + d], strides in elements.  Heads and tokens must not
+ * overlap; the stride of an axis of length one is not read.  Slices of a fused
+ * projection and heads-first tensors are such. */
+typedef struct {
+  void*   data;
+  int64_t ld_token, ld_head;
+} muon_heads_t;
+
+/* Attention.  Query head h goes with key and value head h / (heads / kv_heads);
+ * query i of a sequence of nq queries and nk keys sees all its keys, or, if
+ * `causal`, keys j <= i + nk - nq:
+ *   S = scale q k^T,   lse = log sum_j exp S_ij,   o = sum_j exp(S_ij - lse) v_j.
+ * A query that sees no key gets zeros, lse -infinity, and no gradient.
+ *   starts    int32 [sequences + 1] in device memory: sequence s has the tokens
+ *             starts[s] .. starts[s+1] - 1 of q and o.  NULL: one sequence of all
+ *             tokens (sequences is then not read).  Not decreasing, from 0 to at
+ *             most `tokens`; what they hold is not checked, other values give
+ *             undefined results, but no access outside the tensors.
+ *   k_starts  the same of k and v; NULL: as starts (k_tokens == tokens then), not
+ *             NULL without starts
+ *   lse       fp32, heads x ld_lse >= tokens; may be NULL
+ *   zero_rest what to do with tokens behind the last sequence: 0 leaves them as they
+ *             are; MUON_ATTN_ZERO_O, _LSE write zeros (-infinity to lse)
+ * dim is a multiple of 8 up to 128; tokens, k_tokens 0 .. 2^30; with t the larger
+ * of them (t / 128 + sequences + 2) heads <= 2^23.  Products of bf16 summed in fp32,
+ * softmax in fp32; the probabilities are rounded to bf16 for the second product,
+ * outputs once.  A value that is not finite may reach every row of its sequence and
+ * head, masked or not, but no other sequence. */
+#define MUON_ATTN_MAX_DIM 128
+#define MUON_ATTN_ZERO_O 1
+#define MUON_ATTN_ZERO_LSE 2
+typedef struct {
+  muon_heads_t   q, k, v, o;
+  float*         lse;
+  const int32_t* starts;
+  const int32_t* k_starts;
+  int64_t        tokens, k_tokens, sequences;
+  int64_t        heads, kv_heads, dim;
+  int64_t        ld_lse;
+  float          scale;      /* > 0, finite */
+  int32_t        causal;     /* 0 or 1 */
+  int32_t        zero_rest;
+  int32_t        reserved;   /* must be 0 */
+} muon_attention_t;
+int muon_attention(const muon_attention_t* op, hipStream_t stream);
+
+/* Its backward pass; P is recomputed from lse:
+ *   P = exp(S - lse),  dS = P (dout v^T - rowsum(dout o)),
+ *   dq = scale dS k,   dk = scale dS^T q,   dv = P^T dout,
+ * dk and dv summed over the heads that share them.  P and dS are rounded to bf16 for
+ * the products.  No atomics: the same bits every time.
+ *   o, lse     as the forward pass left them
+ *   zero_rest  MUON_ATTN_ZERO_DQ, _DK, _DV: as above
+ *   workspace  muon_attention_grad_workspace_bytes(tokens, heads), 256-byte aligned */
+#define MUON_ATTN_ZERO_DQ 1
+#define MUON_ATTN_ZERO_DK 2
+#define MUON_ATTN_ZERO_DV 4
+typedef struct {
+  muon_heads_t   dout, q, k, v, o;
+  muon_heads_t   dq, dk, dv;
+  const float*   lse;
+  const int32_t* starts;
+  const int32_t* k_starts;
+  int64_t        tokens, k_tokens, sequences;
+  int64_t        heads, kv_heads, dim;
+  int64_t        ld_lse;
+  float          scale;
+  int32_t        causal;
+  int32_t        zero_rest;
+  int32_t        reserved;   /* must be 0 */
+} muon_attention_grad_t;
+size_t muon_attention_grad_workspace_bytes(int64_t tokens, int64_t heads);
+int muon_attention_grad(const muon_attention_grad_t* op, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+
+/* Distillation from a teacher's top logits, row by row, x = logits / temperature:
+ *   p    = softmax over the row's entries of teacher / temperature
+ *   loss = weight temperature^2 sum_k p_k (log p_k - log softmax(x)[ids_k])
+ *   dlogits = d loss / d logits = weight temperature (softmax(x) - sum of p at the ids)
+ * An entry whose id is outside 0 .. vocab - 1, or whose teacher logit is -infinity, is
+ * not there; entries of the same id add up.  A row of weight 0 or without entries
+ * has loss 0 and a gradient of zeros, whatever its logits hold.
+ *   logits   dtype, tokens x vocab (vocab <= MUON_MAX_DIM)
+ *   ids      int32 or int64 (id_bytes 4 or 8), tokens x top
+ *   teacher  teacher_dtype, tokens x top
+ *   weights  fp32 [tokens], NULL: 1
+ *   loss     fp32 [tokens];  dlogits  dtype, tokens x vocab, NULL: not wanted */
+#define MUON_DISTILL_MAX_TOP 1024
+typedef struct {
+  const void*  logits;
+  const void*  ids;
+  const void*  teacher;
+  const float* weights;
+  float*       loss;
+  void*        dlogits;
+  int64_t      tokens, vocab, top;   /* top 1 .. MUON_DISTILL_MAX_TOP */
+  int64_t      ld_logits, ld_ids, ld_teacher, ld_dlogits;
+  float        temperature;          /* 1e-6 .. 1e6 */
+  int32_t      dtype, teacher_dtype, id_bytes;
+} muon_distill_t;
+int muon_distill(const muon_distill_t* op, hipStream_t stream);
+
+/* Clipped policy loss with a KL term, token by token, x = logits / temperature:
+ *   logp = log softmax(x)[action],   r = exp(logp - old_logp),   d = ref_logp - logp
+ *   loss = weight (-min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(d) - d - 1))
+ *   g    = d loss / d logp = weight (-A r [r A <= clamp(r) A] + kl_coef (1 - exp(d)))
+ *   dlogits = g / temperature (onehot(action) - softmax(x))
+ * with A the advantage.  A token of weight 0, or whose action is outside 0 .. vocab - 1,
+ * has loss and logp 0 and a gradient of zeros, whatever its logits hold.
+ *   logits      dtype, tokens x vocab;  actions  int32 or int64 [tokens]
+ *   old_logp, advantages, ref_logp, weights  fp32 [tokens]; ref_logp NULL: no KL term;
+ *               weights NULL: 1
+ *   loss, logp  fp32 [tokens]; logp may be NULL
+ *   dlogits     dtype, NULL: not wanted */
+typedef struct {
+  const void*  logits;
+  const void*  actions;
+  const float* old_logp;
+  const float* advantages;
+  const float* ref_logp;
+  const float* weights;
+  float*       loss;
+  float*       logp;
+  void*        dlogits;
+  int64_t      tokens, vocab;
+  int64_t      ld_logits, ld_dlogits;
+  float        clip_low, clip_high;  /* 0 <= clip_low <= 1, clip_high >= 0 */
+  float        kl_coef;              /* finite */
+  float        temperature;          /* 1e-6 .. 1e6 */
+  int32_t      dtype, id_bytes;
+} muon_policy_t;
+int muon_policy(const muon_policy_t* op, hipStream_t stream);
 
 /* Phase timing with HIP events, for benchmarks.  When enabled, every launch
  * is bracketed by a pair of events on the call's stream, and a step keeps

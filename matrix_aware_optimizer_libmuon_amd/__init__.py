@@ -333,7 +333,8 @@ def timing_read() -> dict:
 # Training operators that make the gradients of a step (ops.py); resolved on
 # first use, so that importing the package does not import torch.
 _OPS = ("Act8", "act8_pack", "act8_unpack", "act8_wgrad", "rmsnorm_act8", "rmsnorm_act8_grad",
-        "swiglu_act8", "swiglu_act8_grad", "embed", "embed_grad")
+        "swiglu_act8", "swiglu_act8_grad", "embed", "embed_grad", "attention", "attention_grad",
+        "distill_loss", "policy_loss")
 
 
 def __getattr__(name):

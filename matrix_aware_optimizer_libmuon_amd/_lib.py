@@ -46,7 +46,9 @@ EXPORTED = ("muon_workspace_bytes", "muon_step", "muon_step_ex", "muon_plan_crea
             "muon_rmsnorm_act8", "muon_rmsnorm_act8_grad_workspace_bytes", "muon_rmsnorm_act8_grad",
             "muon_swiglu_act8", "muon_swiglu_act8_grad",
             "muon_act8_wgrad_workspace_bytes", "muon_act8_wgrad",
-            "muon_embed", "muon_embed_grad_workspace_bytes", "muon_embed_grad")
+            "muon_embed", "muon_embed_grad_workspace_bytes", "muon_embed_grad",
+            "muon_attention", "muon_attention_grad_workspace_bytes", "muon_attention_grad",
+            "muon_distill", "muon_policy")
 
 
 class MuonMatrix(ctypes.Structure):
@@ -145,6 +147,40 @@ class MuonEmbedGrad(ctypes.Structure):
                 ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class MuonHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld_token", ctypes.c_int64), ("ld_head", ctypes.c_int64)]
+
+
+_ATTENTION = [("starts", ctypes.c_void_p), ("k_starts", ctypes.c_void_p),
+              *_int64s("tokens", "k_tokens", "sequences", "heads", "kv_heads", "dim", "ld_lse"),
+              ("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("zero_rest", ctypes.c_int32),
+              ("reserved", ctypes.c_int32)]
+
+
+class MuonAttention(ctypes.Structure):
+    _fields_ = [*((n, MuonHeads) for n in ("q", "k", "v", "o")), ("lse", ctypes.c_void_p), *_ATTENTION]
+
+
+class MuonAttentionGrad(ctypes.Structure):
+    _fields_ = [*((n, MuonHeads) for n in ("dout", "q", "k", "v", "o", "dq", "dk", "dv")),
+                ("lse", ctypes.c_void_p), *_ATTENTION]
+
+
+class MuonDistill(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("logits", "ids", "teacher", "weights", "loss", "dlogits")),
+                *_int64s("tokens", "vocab", "top", "ld_logits", "ld_ids", "ld_teacher", "ld_dlogits"),
+                ("temperature", ctypes.c_float), ("dtype", ctypes.c_int32), ("teacher_dtype", ctypes.c_int32),
+                ("id_bytes", ctypes.c_int32)]
+
+
+class MuonPolicy(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("logits", "actions", "old_logp", "advantages", "ref_logp", "weights",
+                                                 "loss", "logp", "dlogits")),
+                *_int64s("tokens", "vocab", "ld_logits", "ld_dlogits"),
+                *((n, ctypes.c_float) for n in ("clip_low", "clip_high", "kl_coef", "temperature")),
+                ("dtype", ctypes.c_int32), ("id_bytes", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -222,7 +258,12 @@ def load() -> ctypes.CDLL:
             ("muon_act8_wgrad", ctypes.c_int, [P(MuonAct8Wgrad), ptr, size_t, ptr]),
             ("muon_embed", ctypes.c_int, [P(MuonEmbed), ptr]),
             ("muon_embed_grad_workspace_bytes", size_t, [i64, i64, i64]),
-            ("muon_embed_grad", ctypes.c_int, [P(MuonEmbedGrad), ptr, size_t, ptr])):
+            ("muon_embed_grad", ctypes.c_int, [P(MuonEmbedGrad), ptr, size_t, ptr]),
+            ("muon_attention", ctypes.c_int, [P(MuonAttention), ptr]),
+            ("muon_attention_grad_workspace_bytes", size_t, [i64, i64]),
+            ("muon_attention_grad", ctypes.c_int, [P(MuonAttentionGrad), ptr, size_t, ptr]),
+            ("muon_distill", ctypes.c_int, [P(MuonDistill), ptr]),
+            ("muon_policy", ctypes.c_int, [P(MuonPolicy), ptr])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     lib.muon_version.argtypes = []

@@ -35,6 +35,8 @@ SOURCES = [
     ("muon_norm.hip", []),
     ("muon_embed.hip", []),
     ("muon_wgrad.hip", []),
+    ("muon_loss.hip", []),
+    ("muon_attn.hip", []),
     ("muon_api.cpp", []),
     ("muon_ops.cpp", []),
 ]

@@ -15,6 +15,7 @@
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
 
+#include <cmath>
 #include <cstdint>
 #include <map>
 #include <string>
@@ -40,6 +41,11 @@ struct Entries {
   decltype(&muon_embed) embed = nullptr;
   decltype(&muon_embed_grad_workspace_bytes) embed_grad_ws = nullptr;
   decltype(&muon_embed_grad) embed_grad = nullptr;
+  decltype(&muon_attention) attention = nullptr;
+  decltype(&muon_attention_grad_workspace_bytes) attention_grad_ws = nullptr;
+  decltype(&muon_attention_grad) attention_grad = nullptr;
+  decltype(&muon_distill) distill = nullptr;
+  decltype(&muon_policy) policy = nullptr;
 } g_entry;
 
 void bind_ops(const std::map<std::string, uintptr_t>& at) {
@@ -56,6 +62,11 @@ void bind_ops(const std::map<std::string, uintptr_t>& at) {
   get("muon_embed", g_entry.embed);
   get("muon_embed_grad_workspace_bytes", g_entry.embed_grad_ws);
   get("muon_embed_grad", g_entry.embed_grad);
+  get("muon_attention", g_entry.attention);
+  get("muon_attention_grad_workspace_bytes", g_entry.attention_grad_ws);
+  get("muon_attention_grad", g_entry.attention_grad);
+  get("muon_distill", g_entry.distill);
+  get("muon_policy", g_entry.policy);
 }
 
 [[noreturn]] void bad_value(const char* name, const std::string& what) { throw py::value_error(std::string(name) + " " + what); }
@@ -360,6 +371,179 @@ py::tuple embed_grad(const at::Tensor& dy, const at::Tensor& ids, int64_t vocab,
   return py::make_tuple(st, o);
 }
 
+// tokens x heads x dim with unit column stride.
+muon_heads_t heads_of(const Call& c, const at::Tensor& t, const char* name, int64_t tokens = -1, int64_t heads = -1, int64_t dim = -1) {
+  if (t.dim() != 3) bad_value(name, "must be 3-D (tokens, heads, dim)");
+  c.on_device(t, name);
+  if (t.scalar_type() != at::kBFloat16) bad_type(name, "must be bfloat16");
+  if ((tokens >= 0 && t.size(0) != tokens) || (heads >= 0 && t.size(1) != heads) || (dim >= 0 && t.size(2) != dim))
+    bad_value(name, "must have shape (" + std::to_string(tokens < 0 ? t.size(0) : tokens) + ", " +
+                        std::to_string(heads < 0 ? t.size(1) : heads) + ", " + std::to_string(dim < 0 ? t.size(2) : dim) + "), got (" +
+                        std::to_string(t.size(0)) + ", " + std::to_string(t.size(1)) + ", " + std::to_string(t.size(2)) + ")");
+  if (t.size(1) < 1) bad_value(name, "must have a head");
+  if (t.size(2) < 8 || t.size(2) > MUON_ATTN_MAX_DIM || t.size(2) % 8)
+    bad_value(name, "must have a last axis that is a multiple of 8, at most " + std::to_string(MUON_ATTN_MAX_DIM));
+  if (t.stride(2) != 1) bad_value(name, "must have unit stride along its last axis");
+  return {t.data_ptr(), t.stride(0), t.stride(1)};
+}
+
+// starts and k_starts into the struct of either direction
+template <class Op>
+void put_starts(const Call& c, Op& op, const OptTensor& starts, const OptTensor& k_starts) {
+  auto vec = [&](const at::Tensor& t, const char* name) {
+    c.on_device(t, name);
+    if (t.scalar_type() != at::kInt) bad_type(name, "must be int32");
+    if (t.dim() != 1 || t.size(0) < 1 || !t.is_contiguous()) bad_value(name, "must be a contiguous vector with an entry");
+    return t.data_ptr<int32_t>();
+  };
+  if (starts) {
+    op.starts = vec(*starts, "starts");
+    op.sequences = starts->size(0) - 1;
+  }
+  if (k_starts) {
+    if (!starts) bad_value("k_starts", "must come with starts");
+    op.k_starts = vec(*k_starts, "k_starts");
+    if (k_starts->size(0) != op.sequences + 1) bad_value("k_starts", "must be as long as starts");
+  } else if (starts && op.tokens != op.k_tokens) {
+    bad_value("k_starts", "must be given where k has another number of tokens than q");
+  }
+}
+
+template <class Op>
+void put_attention(const Call& c, Op& op, const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, const OptTensor& starts,
+                   const OptTensor& k_starts, bool causal, c10::optional<double> scale) {
+  op.q = heads_of(c, q, "q");
+  op.tokens = q.size(0);
+  op.heads = q.size(1);
+  op.dim = q.size(2);
+  op.k = heads_of(c, k, "k", -1, -1, op.dim);
+  op.k_tokens = k.size(0);
+  op.kv_heads = k.size(1);
+  if (op.heads % op.kv_heads) bad_value("k", "must have a number of heads that divides that of q");
+  op.v = heads_of(c, v, "v", op.k_tokens, op.kv_heads, op.dim);
+  put_starts(c, op, starts, k_starts);
+  op.causal = causal ? 1 : 0;
+  op.scale = static_cast<float>(scale ? *scale : 1.0 / std::sqrt(static_cast<double>(op.dim)));
+}
+
+py::tuple attention(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, const OptTensor& starts, const OptTensor& k_starts,
+                    bool causal, c10::optional<double> scale, const OptTensor& out) {
+  Call c(q, "q");
+  muon_attention_t op{};
+  put_attention(c, op, q, k, v, starts, k_starts, causal, scale);
+  const at::Tensor o = out ? *out : c.empty({op.tokens, op.heads, op.dim}, at::kBFloat16);
+  op.o = heads_of(c, o, "out", op.tokens, op.heads, op.dim);
+  const at::Tensor lse = c.empty({op.heads, op.tokens}, at::kFloat);
+  op.lse = lse.data_ptr<float>();
+  op.ld_lse = op.tokens;
+  op.zero_rest = MUON_ATTN_ZERO_LSE | (out ? 0 : MUON_ATTN_ZERO_O);
+  const int st = g_entry.attention(&op, c.stream());
+  return py::make_tuple(st, o, lse);
+}
+
+py::tuple attention_grad(const at::Tensor& dout, const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, const at::Tensor& o,
+                         const at::Tensor& lse, const OptTensor& starts, const OptTensor& k_starts, bool causal,
+                         c10::optional<double> scale, const OptTensor& dq, const OptTensor& dk, const OptTensor& dv) {
+  Call c(dout, "do");
+  muon_attention_grad_t op{};
+  put_attention(c, op, q, k, v, starts, k_starts, causal, scale);
+  op.dout = heads_of(c, dout, "do", op.tokens, op.heads, op.dim);
+  op.o = heads_of(c, o, "o", op.tokens, op.heads, op.dim);
+  c.on_device(lse, "lse");
+  if (lse.scalar_type() != at::kFloat) bad_type("lse", "must be float32");
+  if (lse.dim() != 2 || lse.size(0) != op.heads || lse.size(1) != op.tokens || (op.tokens > 1 && lse.stride(1) != 1) ||
+      (op.heads > 1 && lse.stride(0) < op.tokens))
+    bad_value("lse", "must have shape " + sizes(op.heads, op.tokens) + " and rows that do not overlap");
+  op.lse = lse.data_ptr<float>();
+  op.ld_lse = op.heads > 1 ? lse.stride(0) : op.tokens;
+  const at::Tensor gq = dq ? *dq : c.empty({op.tokens, op.heads, op.dim}, at::kBFloat16);
+  const at::Tensor gk = dk ? *dk : c.empty({op.k_tokens, op.kv_heads, op.dim}, at::kBFloat16);
+  const at::Tensor gv = dv ? *dv : c.empty({op.k_tokens, op.kv_heads, op.dim}, at::kBFloat16);
+  op.dq = heads_of(c, gq, "dq", op.tokens, op.heads, op.dim);
+  op.dk = heads_of(c, gk, "dk", op.k_tokens, op.kv_heads, op.dim);
+  op.dv = heads_of(c, gv, "dv", op.k_tokens, op.kv_heads, op.dim);
+  op.zero_rest = (dq ? 0 : MUON_ATTN_ZERO_DQ) | (dk ? 0 : MUON_ATTN_ZERO_DK) | (dv ? 0 : MUON_ATTN_ZERO_DV);
+  const size_t bytes = g_entry.attention_grad_ws(op.tokens, op.heads);
+  const at::Tensor ws = c.workspace(bytes);
+  const int st = g_entry.attention_grad(&op, bytes ? ws.data_ptr() : nullptr, bytes, c.stream());
+  return py::make_tuple(st, gq, gk, gv);
+}
+
+// The gradient of the logits: given, new, or not wanted.
+template <class Op>
+at::Tensor put_dlogits(const Call& c, Op& op, const at::Tensor& logits, const OptTensor& out, bool want_grad) {
+  if (!want_grad) {
+    if (out) bad_value("out", "must not be given without want_grad");
+    return at::Tensor();
+  }
+  const at::Tensor d = out ? *out : c.empty({op.tokens, op.vocab}, logits.scalar_type());
+  op.ld_dlogits = c.matrix(d, "out", op.tokens, op.vocab);
+  same_type(d, logits, "out", "logits");
+  op.dlogits = d.data_ptr();
+  return d;
+}
+
+py::object or_none(const at::Tensor& t) { return t.defined() ? py::cast(t) : py::object(py::none()); }
+
+py::tuple distill_loss(const at::Tensor& logits, const at::Tensor& ids, const at::Tensor& teacher, const OptTensor& weights,
+                       const OptTensor& out, double temperature, bool want_grad) {
+  Call c(logits, "logits");
+  muon_distill_t op{};
+  op.ld_logits = c.matrix(logits, "logits");
+  op.tokens = logits.size(0);
+  op.vocab = logits.size(1);
+  op.dtype = code_of(logits.scalar_type(), "logits");
+  op.logits = logits.data_ptr();
+  op.ld_ids = c.matrix(ids, "ids", op.tokens);
+  if (ids.scalar_type() != at::kLong && ids.scalar_type() != at::kInt) bad_type("ids", "must be int32 or int64");
+  op.id_bytes = ids.scalar_type() == at::kLong ? 8 : 4;
+  op.ids = ids.data_ptr();
+  op.top = ids.size(1);
+  if (op.top > MUON_DISTILL_MAX_TOP) bad_value("ids", "must have at most " + std::to_string(MUON_DISTILL_MAX_TOP) + " columns");
+  op.ld_teacher = c.matrix(teacher, "teacher", op.tokens, op.top);
+  op.teacher_dtype = code_of(teacher.scalar_type(), "teacher");
+  op.teacher = teacher.data_ptr();
+  if (weights) op.weights = c.fp32_vector(*weights, "weights", op.tokens);
+  op.temperature = static_cast<float>(temperature);
+  const at::Tensor d = put_dlogits(c, op, logits, out, want_grad);
+  const at::Tensor loss = c.empty({op.tokens}, at::kFloat);
+  op.loss = loss.data_ptr<float>();
+  const int st = g_entry.distill(&op, c.stream());
+  return py::make_tuple(st, loss, or_none(d));
+}
+
+py::tuple policy_loss(const at::Tensor& logits, const at::Tensor& actions, const at::Tensor& old_logp, const at::Tensor& advantages,
+                      const OptTensor& ref_logp, const OptTensor& weights, const OptTensor& out, double clip_low, double clip_high,
+                      double kl_coef, double temperature, bool want_grad) {
+  Call c(logits, "logits");
+  muon_policy_t op{};
+  op.ld_logits = c.matrix(logits, "logits");
+  op.tokens = logits.size(0);
+  op.vocab = logits.size(1);
+  op.dtype = code_of(logits.scalar_type(), "logits");
+  op.logits = logits.data_ptr();
+  c.on_device(actions, "actions");
+  if (actions.scalar_type() != at::kLong && actions.scalar_type() != at::kInt) bad_type("actions", "must be int32 or int64");
+  if (actions.dim() != 1 || actions.size(0) != op.tokens || !actions.is_contiguous())
+    bad_value("actions", "must be a contiguous vector of " + std::to_string(op.tokens));
+  op.id_bytes = actions.scalar_type() == at::kLong ? 8 : 4;
+  op.actions = actions.data_ptr();
+  op.old_logp = c.fp32_vector(old_logp, "old_logp", op.tokens);
+  op.advantages = c.fp32_vector(advantages, "advantages", op.tokens);
+  if (ref_logp) op.ref_logp = c.fp32_vector(*ref_logp, "ref_logp", op.tokens);
+  if (weights) op.weights = c.fp32_vector(*weights, "weights", op.tokens);
+  op.clip_low = static_cast<float>(clip_low);
+  op.clip_high = static_cast<float>(clip_high);
+  op.kl_coef = static_cast<float>(kl_coef);
+  op.temperature = static_cast<float>(temperature);
+  const at::Tensor d = put_dlogits(c, op, logits, out, want_grad);
+  const at::Tensor loss = c.empty({op.tokens}, at::kFloat), logp = c.empty({op.tokens}, at::kFloat);
+  op.loss = loss.data_ptr<float>();
+  op.logp = logp.data_ptr<float>();
+  const int st = g_entry.policy(&op, c.stream());
+  return py::make_tuple(st, loss, logp, or_none(d));
+}
+
 }  // namespace
 
 void register_ops(py::module_& mod) {
@@ -373,9 +557,15 @@ void register_ops(py::module_& mod) {
   mod.def("act8_wgrad", &act8_wgrad);
   mod.def("embed", &embed);
   mod.def("embed_grad", &embed_grad);
+  mod.def("attention", &attention);
+  mod.def("attention_grad", &attention_grad);
+  mod.def("distill_loss", &distill_loss);
+  mod.def("policy_loss", &policy_loss);
   mod.attr("OP_BYTES") = std::map<std::string, size_t>{
       {"muon_act8_t", sizeof(muon_act8_t)}, {"muon_rmsnorm_t", sizeof(muon_rmsnorm_t)},
       {"muon_rmsnorm_grad_t", sizeof(muon_rmsnorm_grad_t)}, {"muon_swiglu_t", sizeof(muon_swiglu_t)},
       {"muon_swiglu_grad_t", sizeof(muon_swiglu_grad_t)}, {"muon_act8_wgrad_t", sizeof(muon_act8_wgrad_t)},
-      {"muon_embed_t", sizeof(muon_embed_t)}, {"muon_embed_grad_t", sizeof(muon_embed_grad_t)}};
+      {"muon_embed_t", sizeof(muon_embed_t)}, {"muon_embed_grad_t", sizeof(muon_embed_grad_t)},
+      {"muon_attention_t", sizeof(muon_attention_t)}, {"muon_attention_grad_t", sizeof(muon_attention_grad_t)},
+      {"muon_distill_t", sizeof(muon_distill_t)}, {"muon_policy_t", sizeof(muon_policy_t)}};
 }

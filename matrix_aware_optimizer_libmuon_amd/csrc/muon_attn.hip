@@ -1,0 +1,602 @@
+// Attention over sequences of any lengths, and its backward pass (gfx950):
+//   S = scale Q K^T (masked),  P = softmax(S),  O = P V,  lse = log sum exp S
+//   dP = dO V^T,  dS = P (dP - rowsum(dO O)),  dQ = scale dS K,
+//   dK = scale dS^T Q,  dV = P^T dO.
+// S and P never leave the registers.  The backward pass recomputes P from lse, in
+// two kernels, one that owns queries (dQ) and one that owns keys (dK, dV): seven
+// products instead of five, but no sums across blocks, so no atomics, and the same
+// bits every time.
+//
+// Layout.  A wave owns 32 queries (or keys), one per lane and half: it forms the
+// transposed product S^T = K Q^T with v_mfma_f32_32x32x16_bf16, whose result leaves
+// lane l with 16 of 32 keys of query l & 31.  A row's maximum and sum are then one
+// exchange between the wave's halves, its rescaling is one factor a lane, and P,
+// rounded to bf16, is already the second operand of O^T = V^T P^T: the instruction
+// sums over keys, so they may come in the order in which the lane holds them,
+//   element e of half h of 16-key step s  <->  key 16 s + 8 (e / 4) + 4 h + e % 4,
+// if V^T is read in the same order, which the transposing LDS read does at no cost.
+// The other products are of the same two kinds.
+//
+// Tiles of 64 rows lie in LDS as in memory, 16-byte chunk c of row r at c ^ swz(r):
+// the 16 rows that a 16-byte read serves in one cycle, and the 4 rows by 4 chunks of a
+// transposing read, then fall on distinct banks.  They are loaded straight into LDS
+// while the tile before is in work.  Rows past a sequence's end and columns past dim
+// are zeros there, so that nothing of a neighbour reaches a sum.
+#include <algorithm>
+
+#include <type_traits>
+
+#include "muon_act8.h"
+#include "muon_ops.h"
+
+namespace muon {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(16))) float f32x16_t;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kInf = __builtin_inff();
+constexpr int BN = 64;             // rows of a staged tile
+constexpr int BM = 128;            // rows that a block owns, 32 a wave
+constexpr int kThreads = 256;
+
+// DB blocks of 32 columns are computed: dim up to 64, 96 or 128.
+template <int DB>
+struct Geo {
+  static constexpr int KS = 2 * DB;                       // 16-column steps
+  static constexpr int COLS = DB <= 2 ? 64 : 128;         // columns of a row in LDS
+  static constexpr int ROWB = COLS * 2, CPR = COLS / 8;   // its bytes and chunks
+  static constexpr int TILE = BN * ROWB;
+  static constexpr int LOADS = TILE / 4096;               // 1 KB loads of a wave
+};
+
+template <int COLS>
+__device__ __forceinline__ int swz(int row) {
+  return COLS == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+}
+
+__device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Both halves' values in every lane.
+__device__ __forceinline__ u32x2 halves(float v) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+}
+__device__ __forceinline__ float halves_max(float v) {
+  const u32x2 r = halves(v);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  const u32x2 r = halves(v);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ void block_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// 16 (4) bytes a lane from buffer `srd` at voff + soff into LDS at lds_dst + 16 (4)
+// times the lane; zeros past the buffer's end.  An asm statement, because the
+// compiler would wait for all of them before every later LDS read; block_barrier()
+// waits.  The s_nop keeps the 5 wait states between a vector instruction's write of
+// a scalar register and this read of it (and the one after a write of m0).
+template <int BYTES>
+__device__ __forceinline__ void dma(u32x4 srd, uint32_t voff, uint32_t soff, uint32_t lds_dst) {
+  if constexpr (BYTES == 16)
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(lds_dst));
+  else
+    asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(srd), "s"(soff), "{m0}"(lds_dst));
+}
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
+}
+__device__ __forceinline__ u32x4 buffer(const void* p, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(p);
+  u32x4 srd;
+  srd[0] = uniform(static_cast<uint32_t>(b));
+  srd[1] = uniform(static_cast<uint32_t>(b >> 32) & 0xffffu);
+  srd[2] = uniform(bytes);
+  srd[3] = 0x00020000u;   // raw buffer of dwords
+  return srd;
+}
+
+// Tiles of one head's rows of a sequence, into LDS.  ALIGNED: rows begin on 16
+// bytes and 64 of them span less than 2^31 (attn_aligned): loads without registers,
+// in flight until block_barrier().  Else through registers at once.
+template <int DB, bool ALIGNED>
+struct Feed {
+  using G = Geo<DB>;
+  const uint16_t* p;
+  int64_t ld;
+  int rows, dim;                   // of the sequence; columns
+  uint32_t voff[G::LOADS];
+  int w, tid;
+
+  __device__ __forceinline__ Feed(const muon_heads_t& t, int64_t row0, int nrows, int head, int dim_, int tid_)
+      : p(static_cast<const uint16_t*>(t.data) + row0 * t.ld_token + head * t.ld_head), ld(t.ld_token), rows(nrows), dim(dim_), tid(tid_) {
+    w = uniform(tid >> 6);
+    if constexpr (ALIGNED) {
+      const int lane = tid & 63, rr = lane / G::CPR, pos = lane % G::CPR;
+#pragma unroll
+      for (int q = 0; q < G::LOADS; ++q) {
+        const int c = pos ^ swz<G::COLS>((w * G::LOADS + q) * (64 / G::CPR) + rr);
+        voff[q] = c * 8 < dim ? static_cast<uint32_t>(rr * ld * 2 + c * 16) : 0x80000000u;   // past every end
+      }
+    }
+  }
+  __device__ __forceinline__ void load(int row, char* dst) const {
+    const int left = min(rows - row, BN);
+    if (left <= 0) return;         // (uniform) no such tile: nobody reads it
+    const uint16_t* at = p + row * ld;
+    if constexpr (ALIGNED) {
+      const uint32_t ldb = static_cast<uint32_t>(ld * 2);
+      const u32x4 srd = buffer(at, (left - 1) * ldb + dim * 2);
+      const uint32_t to = lds_at(dst);
+#pragma unroll
+      for (int q = 0; q < G::LOADS; ++q) {
+        const int b = w * G::LOADS + q;
+        dma<16>(srd, voff[q], b * (64 / G::CPR) * ldb, to + b * 1024);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = tid; i < BN * G::CPR; i += kThreads) {
+        const int r = i / G::CPR, c = (i % G::CPR) ^ swz<G::COLS>(r);
+        u32x4 v{0, 0, 0, 0};
+        if (r < left && c * 8 < dim) v = gld<u32x4_a2>(at + r * ld + c * 8);
+        *reinterpret_cast<u32x4*>(dst + i * 16) = v;
+      }
+    }
+  }
+};
+
+// Fragments of a staged tile.  rows(): row rb + (lane & 31), columns 16 ks + 8 h ..;
+// cols(): column 32 db + (lane & 31), the rows of 16-row step s in the order above.
+template <int DB>
+struct Frags {
+  using G = Geo<DB>;
+  int r0, t0;
+  __device__ __forceinline__ explicit Frags(int lane) {
+    const int l = lane & 31, h = lane >> 5, j = lane & 15;
+    r0 = l * G::ROWB + ((h ^ swz<G::COLS>(l)) << 4);
+    const int row = 4 * h + (j >> 2), c = 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+    t0 = row * G::ROWB + ((c ^ swz<G::COLS>(row)) << 4) + (j & 1) * 8;
+  }
+  __device__ __forceinline__ bf16x8_t rows(const char* tile, int rb, int ks) const {
+    return *reinterpret_cast<const bf16x8_t*>(tile + rb * G::ROWB + (r0 ^ (ks << 5)));
+  }
+  __device__ __forceinline__ bf16x8_t cols(const char* tile, int s, int db) const {
+    // 8 rows on, bit 1 of the swizzle is set
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(tile + s * 16 * G::ROWB + (t0 ^ (db << 6))));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(tile + (s * 16 + 8) * G::ROWB + (t0 ^ (db << 6) ^ 32)));
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+
+// The wave's own 32 rows as a second operand: row lane & 31, columns 16 ks + 8 h ..
+template <int DB>
+__device__ __forceinline__ void own_rows(const muon_heads_t& t, int64_t row0, int row, int nrows, int head, int dim, int h,
+                                         bf16x8_t (&f)[2 * DB]) {
+  const uint16_t* p = static_cast<const uint16_t*>(t.data) + (row0 + row) * t.ld_token + head * t.ld_head;
+#pragma unroll
+  for (int ks = 0; ks < 2 * DB; ++ks) {
+    const int c = 16 * ks + 8 * h;
+    u32x4 v{0, 0, 0, 0};
+    if (row < nrows && c < dim) v = gld<u32x4_a2>(p + c);
+    f[ks] = __builtin_bit_cast(bf16x8_t, v);
+  }
+}
+
+// A lane's 8 values as an operand, rounded to bf16.
+__device__ __forceinline__ bf16x8_t pack8(const f32x16_t& v, int from) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = pack2(v[from + 2 * i], v[from + 2 * i + 1]);
+  return __builtin_bit_cast(bf16x8_t, r);
+}
+
+// Transposed sums (rows d, the lane's own row as column) times f, to the row: the
+// halves trade registers, so that each stores 16 bytes at a time.
+template <int DB>
+__device__ __forceinline__ void store_row(const muon_heads_t& t, int64_t row, int head, int dim, int h, bool live,
+                                          const f32x16_t (&acc)[DB], float f) {
+  uint16_t* p = static_cast<uint16_t*>(t.data) + row * t.ld_token + head * t.ld_head;
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int a = 0; a < 16; a += 8) {
+      u32x4 o;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x = pack2(acc[db][a + 2 * i] * f, acc[db][a + 2 * i + 1] * f);
+        const uint32_t y = pack2(acc[db][a + 4 + 2 * i] * f, acc[db][a + 4 + 2 * i + 1] * f);
+        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        o[i] = r[0];
+        o[2 + i] = r[1];
+      }
+      const int d = 32 * db + 2 * a + 8 * h;
+      if (live && d < dim) gst<u32x4_a2>(p + d, o);
+    }
+}
+
+// ------------------------------------------------------------ a block's rows ----
+struct Place {
+  int q0, nq, k0, nk;   // the sequence's first query and queries, first key and keys
+  int tile;             // the block's tile of them
+  bool found;
+  bool rest;            // rows behind the last sequence
+};
+
+// Unit `unit` of the tiles of BM queries (KEYS: keys) of all sequences, one after the
+// other; rows behind the last sequence are one more, without keys (queries), if they
+// are to be written.  Starts are brought into range and order first, so that bad ones
+// cannot lead outside the tensors.
+template <bool KEYS>
+__device__ __forceinline__ Place locate(const int32_t* starts, const int32_t* k_starts, int64_t sequences, int tokens, int k_tokens,
+                                        bool rest, int unit, int lane) {
+  if (!starts) {
+    const int n = KEYS ? k_tokens : tokens;
+    return {0, tokens, 0, k_tokens, unit, unit < (n + BM - 1) / BM, false};
+  }
+  if (!k_starts) k_starts = starts;
+  int before = 0;
+  for (int64_t base = 0; base <= sequences; base += 64) {
+    const int64_t i = base + lane;
+    int q0 = 0, nq = 0, k0 = 0, nk = 0;
+    if (i <= sequences) {
+      const int64_t next = i < sequences ? i + 1 : i;
+      q0 = min(max(gld<int32_t>(starts + i), 0), tokens);
+      k0 = min(max(gld<int32_t>(k_starts + i), 0), k_tokens);
+      nq = min(max(gld<int32_t>(starts + next), q0), tokens) - q0;
+      nk = min(max(gld<int32_t>(k_starts + next), k0), k_tokens) - k0;
+      if (i == sequences && rest) (KEYS ? nk : nq) = KEYS ? k_tokens - k0 : tokens - q0;
+    }
+    const int tiles = ((KEYS ? nk : nq) + BM - 1) / BM;
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += v;
+    }
+    const uint64_t past = __ballot(before + upto > unit);
+    if (past) {
+      const int f = __builtin_ctzll(past);
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, f); };
+      return {of(q0), of(nq), of(k0), of(nk), unit - before - of(upto - tiles), true, base + f == sequences};
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return {0, 0, 0, 0, 0, false, false};
+}
+
+// ------------------------------------------------------------- forward pass ----
+// Rescaling is put off while no row's maximum has grown by more than 2^kSlack since the
+// last one: P then reaches 2^kSlack at most, which costs no precision, and the sums are
+// multiplied in few of the tiles instead of all.
+constexpr float kSlack = 8.f;
+
+template <int DB, bool ALIGNED>
+__global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint32_t units) {
+  using G = Geo<DB>;
+  __shared__ __attribute__((aligned(256))) char smem[4 * G::TILE];      // K, V; K, V of the next tile
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
+  // neighbouring blocks of an XCD share a head; the longest rows of a causal mask first
+  const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
+  const int head = at / units, unit = units - 1 - at % units;
+  const Place pl = locate<false>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, op.zero_rest != 0, unit, lane);
+  if (!pl.found) return;
+  const int kv = head / static_cast<int>(op.heads / op.kv_heads), dim = op.dim;
+  const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31);   // the wave's first query, the lane's
+  const int offset = pl.nk - pl.nq;                                      // key i + offset is query i's last (causal)
+  const int block_last = min(pl.tile * BM + BM, pl.nq) - 1 + offset;
+  const int keys = op.causal ? max(0, min(pl.nk, block_last + 1)) : pl.nk;   // that any query of the block sees
+
+  bf16x8_t qf[G::KS];
+  own_rows<DB>(op.q, pl.q0, mine, pl.nq, head, dim, h, qf);
+  const Feed<DB, ALIGNED> fk(op.k, pl.k0, keys, kv, dim, tid), fv(op.v, pl.k0, keys, kv, dim, tid);
+  const Frags<DB> fr(lane);
+  f32x16_t o[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) o[db] = f32x16_t{};
+  float top = -kInf, sum = 0.f;                // top: the maximum that P is taken against; sum: of this half's keys
+  const float c = op.scale * kLog2e;
+
+  fk.load(0, smem);
+  fv.load(0, smem + G::TILE);
+  block_barrier();
+  const int tiles = (keys + BN - 1) / BN;
+  auto step = [&](int j, const char* now, char* next) __attribute__((always_inline)) {
+    fk.load((j + 1) * BN, next);
+    fv.load((j + 1) * BN, next + G::TILE);
+    const int k0 = j * BN;
+    // no query of the wave sees the tile
+    if (!(op.causal && k0 > first + 31 + offset) && first < pl.nq) {
+      f32x16_t s[2] = {};
+#pragma unroll
+      for (int ks = 0; ks < G::KS; ++ks)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) s[kb] = mfma(fr.rows(now, 32 * kb, ks), qf[ks], s[kb]);
+      if (k0 + BN > pl.nk || (op.causal && k0 + BN - 1 > first + offset)) {
+        const int last = op.causal ? min(pl.nk - 1, mine + offset) : pl.nk - 1;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (k0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 > last) s[kb][i] = -kInf;
+      }
+      float m = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+      for (int i = 1; i < 16; ++i) m = fmaxf(m, fmaxf(s[0][i], s[1][i]));
+      m = halves_max(m);
+      if (__any((m - top) * c > kSlack)) {     // (-inf - -inf is NaN: no)
+        const float grown = fmaxf(m, top);
+        const float f = grown == -kInf ? 0.f : exp2_fast((top - grown) * c);
+        top = grown;
+        sum *= f;
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[db] *= f;
+      }
+      const float base = top == -kInf ? 0.f : top * c;
+      float part[4] = {};
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[kb][i] = exp2_fast(s[kb][i] * c - base);
+          part[i & 3] += s[kb][i];
+        }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        const bf16x8_t pf = pack8(s[st / 2], 8 * (st % 2));
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[db] = mfma(fr.cols(now + G::TILE, st, db), pf, o[db]);
+      }
+    }
+    block_barrier();
+  };
+  for (int j = 0; j < tiles; j += 2) {
+    step(j, smem, smem + 2 * G::TILE);
+    if (j + 1 < tiles) step(j + 1, smem + 2 * G::TILE, smem);
+  }
+  sum = halves_sum(sum);
+  const bool live = mine < pl.nq;
+  store_row<DB>(op.o, pl.q0 + mine, head, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_O)), o, sum == 0.f ? 0.f : 1.f / sum);
+  if (op.lse && live && h == 0 && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_LSE)))
+    gst<float>(op.lse + head * op.ld_lse + pl.q0 + mine, sum == 0.f ? -kInf : (top * c + __builtin_amdgcn_logf(sum)) * kLn2);
+}
+
+// ------------------------------------------------------------ backward: dQ ----
+// As the forward pass, with both S^T = K Q^T and dP^T = V dO^T; the row's lse and
+// rowsum(dO O) are one value a lane, left for the other kernel (rows x 2: lse in
+// powers of two, +inf where the row sees nothing, so that its P is 0).
+template <int DB, bool ALIGNED>
+__global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t op, uint32_t units, float* stats) {
+  using G = Geo<DB>;
+  __shared__ __attribute__((aligned(256))) char smem[4 * G::TILE];
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
+  const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
+  const int head = at / units, unit = units - 1 - at % units;
+  const Place pl = locate<false>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, (op.zero_rest & MUON_ATTN_ZERO_DQ) != 0,
+                                   unit, lane);
+  if (!pl.found) return;
+  const int kv = head / static_cast<int>(op.heads / op.kv_heads), dim = op.dim;
+  const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31), offset = pl.nk - pl.nq;
+  const int block_last = min(pl.tile * BM + BM, pl.nq) - 1 + offset;
+  const int keys = op.causal ? max(0, min(pl.nk, block_last + 1)) : pl.nk;
+
+  const Feed<DB, ALIGNED> fk(op.k, pl.k0, keys, kv, dim, tid), fv(op.v, pl.k0, keys, kv, dim, tid);
+  fk.load(0, smem);
+  fv.load(0, smem + G::TILE);
+  bf16x8_t qf[G::KS], gf[G::KS];
+  float delta = 0.f, base = 0.f;
+  {
+    own_rows<DB>(op.o, pl.q0, mine, pl.nq, head, dim, h, qf);
+    own_rows<DB>(op.dout, pl.q0, mine, pl.nq, head, dim, h, gf);
+#pragma unroll
+    for (int ks = 0; ks < G::KS; ++ks)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta += static_cast<float>(qf[ks][e]) * static_cast<float>(gf[ks][e]);
+    delta = halves_sum(delta);
+    if (mine < pl.nq) {
+      const int64_t row = pl.q0 + mine;
+      const float l = gld<float>(op.lse + head * op.ld_lse + row);
+      base = l == -kInf ? kInf : l * kLog2e;
+      if (h == 0) {
+        gst<float>(stats + head * op.tokens + row, base);
+        gst<float>(stats + (op.heads + head) * op.tokens + row, delta);
+      }
+    }
+    own_rows<DB>(op.q, pl.q0, mine, pl.nq, head, dim, h, qf);
+  }
+  const Frags<DB> fr(lane);
+  f32x16_t dq[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) dq[db] = f32x16_t{};
+  const float c = op.scale * kLog2e;
+
+  block_barrier();
+  const int tiles = (keys + BN - 1) / BN;
+  auto step = [&](int j, const char* now, char* next) __attribute__((always_inline)) {
+    fk.load((j + 1) * BN, next);
+    fv.load((j + 1) * BN, next + G::TILE);
+    const int k0 = j * BN;
+    if (!(op.causal && k0 > first + 31 + offset) && first < pl.nq) {
+      const bool partial = k0 + BN > pl.nk || (op.causal && k0 + BN - 1 > first + offset);
+      const int last = op.causal ? min(pl.nk - 1, mine + offset) : pl.nk - 1;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        f32x16_t s{}, dp{};
+#pragma unroll
+        for (int ks = 0; ks < G::KS; ++ks) {
+          s = mfma(fr.rows(now, 32 * kb, ks), qf[ks], s);
+          dp = mfma(fr.rows(now + G::TILE, 32 * kb, ks), gf[ks], dp);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = exp2_fast(s[i] * c - base) * (dp[i] - delta);
+        if (partial) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (k0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 > last) s[i] = 0.f;
+        }
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const bf16x8_t sf = pack8(s, 8 * st);
+#pragma unroll
+          for (int db = 0; db < DB; ++db) dq[db] = mfma(fr.cols(now, 2 * kb + st, db), sf, dq[db]);
+        }
+      }
+    }
+    block_barrier();
+  };
+  for (int j = 0; j < tiles; j += 2) {
+    step(j, smem, smem + 2 * G::TILE);
+    if (j + 1 < tiles) step(j + 1, smem + 2 * G::TILE, smem);
+  }
+  store_row<DB>(op.dq, pl.q0 + mine, head, dim, h, mine < pl.nq, dq, op.scale);
+}
+
+// ------------------------------------------------------- backward: dK and dV ----
+// A wave owns 32 keys, one per lane and half, and walks the queries of every head that
+// shares them: S = Q K^T and dP = dO V^T leave a lane with 16 of 32 queries of its key,
+// in whose order dV^T = dO^T P and dK^T = Q^T dS then take them.  lse and rowsum(dO O) come
+// with the tile.  A query past the sequence's end has zeros everywhere and adds nothing.
+template <int DB, bool ALIGNED>
+__global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(muon_attention_grad_t op, uint32_t units, const float* stats) {
+  using G = Geo<DB>;
+  constexpr int STAGE = 2 * G::TILE + 2 * BN * 4;       // Q, dO, lse, delta
+  __shared__ __attribute__((aligned(256))) char smem[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
+  const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
+  const int kv = at / units, unit = at % units;
+  const Place pl = locate<true>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens,
+                                  (op.zero_rest & (MUON_ATTN_ZERO_DK | MUON_ATTN_ZERO_DV)) != 0, unit, lane);
+  if (!pl.found) return;
+  const int share = op.heads / op.kv_heads, dim = op.dim;
+  const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31), offset = pl.nk - pl.nq;
+  // the first query that sees a key of the block, and of the wave
+  const int from = op.causal ? max(0, pl.tile * BM - offset) : 0;
+  const int j0 = from / BN, tiles = (pl.nq + BN - 1) / BN;
+
+  bf16x8_t kf[G::KS], vf[G::KS];
+  own_rows<DB>(op.k, pl.k0, mine, pl.nk, kv, dim, h, kf);
+  own_rows<DB>(op.v, pl.k0, mine, pl.nk, kv, dim, h, vf);
+  const Frags<DB> fr(lane);
+  f32x16_t dk[DB], dv[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16_t{};
+  const float c = op.scale * kLog2e;
+
+  for (int head = kv * share; head < (kv + 1) * share; ++head) {
+    const Feed<DB, ALIGNED> fq(op.q, pl.q0, pl.nq, head, dim, tid), fg(op.dout, pl.q0, pl.nq, head, dim, tid);
+    const float* rows = stats + head * op.tokens + pl.q0 + (w == 1 ? op.heads * op.tokens : 0);   // wave 0: lse, 1: delta
+    auto load = [&](int j, char* to) __attribute__((always_inline)) {
+      fq.load(j * BN, to);
+      fg.load(j * BN, to + G::TILE);
+      const int left = min(pl.nq - j * BN, BN);
+      if (w < 2 && left > 0)
+        dma<4>(buffer(rows + j * BN, left * 4), lane * 4, 0, lds_at(to + 2 * G::TILE + w * BN * 4));
+    };
+    auto step = [&](int j, const char* now, char* next) __attribute__((always_inline)) {
+      load(j + 1, next);
+#pragma unroll
+      for (int qb = 0; qb < 2; ++qb) {
+        const int q0 = j * BN + 32 * qb;
+        // none of the queries sees a key of the wave, or there are none
+        if ((op.causal && q0 + 31 + offset < first) || q0 >= pl.nq || first >= pl.nk) continue;
+        f32x16_t s{}, dp{};
+#pragma unroll
+        for (int ks = 0; ks < G::KS; ++ks) {
+          s = mfma(fr.rows(now, 32 * qb, ks), kf[ks], s);
+          dp = mfma(fr.rows(now + G::TILE, 32 * qb, ks), vf[ks], dp);
+        }
+        const bool partial = op.causal && q0 + offset < first + 31;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const char* at_q = now + 2 * G::TILE + (32 * qb + 8 * g + 4 * h) * 4;
+          const f32x4_t l = *reinterpret_cast<const f32x4_t*>(at_q), d = *reinterpret_cast<const f32x4_t*>(at_q + BN * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * g + e;
+            float p = exp2_fast(s[i] * c - l[e]), x = p * (dp[i] - d[e]);
+            if (partial && mine > q0 + 8 * g + 4 * h + e + offset) p = x = 0.f;
+            s[i] = p;
+            dp[i] = x;
+          }
+        }
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const bf16x8_t pf = pack8(s, 8 * st), xf = pack8(dp, 8 * st);
+#pragma unroll
+          for (int db = 0; db < DB; ++db) {
+            dv[db] = mfma(fr.cols(now + G::TILE, 2 * qb + st, db), pf, dv[db]);
+            dk[db] = mfma(fr.cols(now, 2 * qb + st, db), xf, dk[db]);
+          }
+        }
+      }
+      block_barrier();
+    };
+    load(j0, smem);
+    block_barrier();
+    for (int j = j0; j < tiles; j += 2) {
+      step(j, smem, smem + STAGE);
+      if (j + 1 < tiles) step(j + 1, smem + STAGE, smem);
+    }
+  }
+  const bool live = mine < pl.nk;
+  store_row<DB>(op.dk, pl.k0 + mine, kv, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_DK)), dk, op.scale);
+  store_row<DB>(op.dv, pl.k0 + mine, kv, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_DV)), dv, 1.f);
+}
+
+// ---------------------------------------------------------------- dispatch ----
+uint32_t units_of(int64_t tokens, int64_t sequences, bool ragged) {
+  return static_cast<uint32_t>((tokens + BM - 1) / BM + (ragged ? sequences + 1 : 0));
+}
+
+bool aligned16(const muon_heads_t& t) {
+  return reinterpret_cast<uintptr_t>(t.data) % 16 == 0 && t.ld_token % 8 == 0 && t.ld_head % 8 == 0 && t.ld_token < (1 << 24);
+}
+
+// f(blocks of 32 columns, whether rows can be loaded straight into LDS)
+template <class F>
+int by_shape(int64_t dim, bool aligned, F&& f) {
+  auto with = [&](auto db) { return aligned ? f(db, std::true_type{}) : f(db, std::false_type{}); };
+  if (dim <= 64) return with(std::integral_constant<int, 2>{});
+  if (dim <= 96) return with(std::integral_constant<int, 3>{});
+  return with(std::integral_constant<int, 4>{});
+}
+
+}  // namespace
+
+int launch_attention(const muon_attention_t& op, void* stream) {
+  const uint32_t units = units_of(op.tokens, op.sequences, op.starts != nullptr);
+  return by_shape(op.dim, aligned16(op.k) && aligned16(op.v), [&](auto db, auto al) {
+    hipLaunchKernelGGL((k_attn<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.heads)), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), op, units);
+    return static_cast<int>(hipGetLastError());
+  });
+}
+
+int launch_attention_dq(const muon_attention_grad_t& op, float* stats, void* stream) {
+  const uint32_t units = units_of(op.tokens, op.sequences, op.starts != nullptr);
+  return by_shape(op.dim, aligned16(op.k) && aligned16(op.v), [&](auto db, auto al) {
+    hipLaunchKernelGGL((k_attn_dq<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.heads)), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), op, units, stats);
+    return static_cast<int>(hipGetLastError());
+  });
+}
+
+int launch_attention_dkv(const muon_attention_grad_t& op, const float* stats, void* stream) {
+  const uint32_t units = units_of(op.k_tokens, op.sequences, op.starts != nullptr);
+  return by_shape(op.dim, aligned16(op.q) && aligned16(op.dout), [&](auto db, auto al) {
+    hipLaunchKernelGGL((k_attn_dkv<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.kv_heads)), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), op, units, stats);
+    return static_cast<int>(hipGetLastError());
+  });
+}
+
+}  // namespace muon

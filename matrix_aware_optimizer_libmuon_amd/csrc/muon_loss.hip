@@ -1,0 +1,412 @@
+// Losses over a row of logits with the gradient of the logits (gfx950):
+// distillation from a teacher's top logits, and the clipped policy loss.
+//
+// Both need, of a token's row x = z / temperature, the softmax's maximum and sum
+// and a few single entries, and their gradient is
+//   dz = a softmax(x)  plus a value at each of those few entries.
+// A block takes a row.  Up to Regs<T>::cols columns the row stays in registers, so
+// the logits are read once and the gradient written once; a longer row is read
+// again for the gradient (from the caches: the rows that the chip has in work at
+// one time, at most 256 MB, fit the last one).  Bound by memory.
+//
+// Numbers.  x - max is taken before the factor log2(e) / temperature, so that rows
+// of the type's lowest value stay finite; sums run in fp32, up to 128 terms a
+// thread, then over the wave and the waves in a fixed order.  The gradient is
+// rounded once, to the logits' type.
+#include <type_traits>
+
+#include "muon_act8.h"
+#include "muon_ops.h"
+
+namespace muon {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }   // 1 ulp
+__device__ __forceinline__ float log2_fast(float v) { return __builtin_amdgcn_logf(v); }
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+__device__ __forceinline__ float wave_add(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// A maximum to subtract: 0 where there is nothing but -inf, so that exp gives 0.
+__device__ __forceinline__ float base_of(float m) { return m == kNegInf ? 0.f : m; }
+// What a sum taken against the maximum `from` is multiplied by for a larger one (a sum
+// of nothing but -inf is 0 and stays it).
+__device__ __forceinline__ float shrink(float from, float to, float k) {
+  return from == kNegInf ? 0.f : exp2_fast((from - to) * k);
+}
+
+// Maximum and sum of 2^((v - m) k) over some values.
+struct Soft {
+  float m, s;
+};
+
+// Sum of two: the smaller one's is brought to the larger maximum.
+__device__ __forceinline__ Soft wave_join(Soft a, float k) {
+  const float m = wave_max(a.m);
+  return {m, wave_add(a.s * shrink(a.m, m, k))};
+}
+
+template <int RT>
+struct Shared {
+  static constexpr int W = RT / 64;
+  float m[2][W], s[2][W], part[W];
+};
+
+// Over the block's waves, from what each has left in shared memory.
+template <int RT>
+__device__ __forceinline__ Soft block_join(const Shared<RT>& sh, int which, float k) {
+  float m = kNegInf, s = 0.f;
+#pragma unroll
+  for (int w = 0; w < RT / 64; ++w) m = fmaxf(m, sh.m[which][w]);
+#pragma unroll
+  for (int w = 0; w < RT / 64; ++w) s += sh.s[which][w] * shrink(sh.m[which][w], m, k);
+  return {m, s};
+}
+
+// Columns behind the row's end count as -inf.
+__device__ __forceinline__ void fill_behind(Vec8<float>& v, int n) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i >= n) v.r[i >> 2][i & 3] = 0xff800000u;
+}
+__device__ __forceinline__ void fill_behind(Vec8<uint16_t>& v, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (2 * i >= n) v.r[i] = 0xff80ff80u;
+    else if (2 * i + 1 >= n) v.r[i] = (v.r[i] & 0xffffu) | 0xff800000u;
+  }
+}
+template <class T>
+__device__ __forceinline__ void settle_row(Vec8<T>& v, int c, int n) {
+  if (n < 8) {
+    settle8(v, c, n);
+    fill_behind(v, n);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ float value_at(const T* p) {
+  if constexpr (sizeof(T) == 2) return bf2f(gld<uint16_t>(p));
+  else return gld<float>(p);
+}
+template <class T>
+__device__ __forceinline__ void put_value(T* p, float v) {
+  if constexpr (sizeof(T) == 2) gst<uint16_t>(p, f2bf(v));
+  else gst<float>(p, v);
+}
+__device__ __forceinline__ int64_t id_at(const void* ids, int64_t i, int32_t id_bytes) {
+  return id_bytes == 8 ? gld<int64_t>(static_cast<const int64_t*>(ids) + i)
+                       : static_cast<int64_t>(gld<int32_t>(static_cast<const int32_t*>(ids) + i));
+}
+
+// A row of VPL vectors a thread in registers; VPL = 0: any length, in passes of kPass
+// vectors.  Thread t has the vectors t, t + RT ...
+constexpr int kPass = 4;
+template <class T, int RT, int VPL>
+struct Row {
+  static constexpr int N = VPL ? VPL : kPass;
+  const T* p;
+  int cols, t;
+  Vec8<T> x[N];
+
+  __device__ __forceinline__ void fetch(int base) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int c = base + (t + j * RT) * 8;
+      fetch8(x[j], p + c, c, cols - c);
+    }
+  }
+  __device__ __forceinline__ void settle(int base) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int c = base + (t + j * RT) * 8;
+      settle_row(x[j], c, cols - c);
+    }
+  }
+  __device__ __forceinline__ float top() const {
+    float m = kNegInf;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, x[j].get(i));
+    return m;
+  }
+  __device__ __forceinline__ float sum(float base, float k) const {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = exp2_fast((x[j].get(i) - base) * k);
+      s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    }
+    return s;
+  }
+  // the thread's maximum and sum; the first loads have been issued
+  __device__ __forceinline__ Soft stats(float k) {
+    if constexpr (VPL > 0) {
+      settle(0);
+      const float m = wave_max(top());
+      return {m, sum(base_of(m), k)};
+    } else {
+      Soft a{kNegInf, 0.f};
+      for (int at = 0; at < cols; at += RT * 8 * N) {
+        if (at) fetch(at);
+        settle(at);
+        const float m = fmaxf(a.m, top());
+        a.s = a.s * shrink(a.m, m, k) + sum(base_of(m), k);
+        a.m = m;
+      }
+      return a;
+    }
+  }
+  // out[c] = a 2^((x[c] - base) k)
+  __device__ __forceinline__ void scaled(T* out, float base, float k, float a) {
+    for (int at = 0; at < cols; at += RT * 8 * N) {
+      if constexpr (VPL == 0) {
+        fetch(at);
+        settle(at);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = at + (t + j * RT) * 8;
+        float g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = a * exp2_fast((x[j].get(i) - base) * k);
+        Vec8<T>::store(out + c, cols - c, g);
+      }
+      if constexpr (VPL > 0) break;
+    }
+  }
+};
+
+template <class T, int RT>
+__device__ __forceinline__ void zero_row(T* out, int cols, int t) {
+  const float z[8] = {};
+  for (int c = t * 8; c < cols; c += RT * 8) Vec8<T>::store(out + c, cols - c, z);
+}
+
+// ------------------------------------------------------------ distillation ----
+// The entries' ids and teacher logits lie in LDS.  Their columns are written with
+// all others and then once more, behind a barrier, by the thread that has the entry:
+// softmax minus the sum of p over the entries of the same id, in their order (so
+// threads of one id write the same value).
+template <class T, int RT, int VPL>
+__global__ __launch_bounds__(RT) void k_distill(muon_distill_t op) {
+  constexpr int top_max = MUON_DISTILL_MAX_TOP;
+  __shared__ Shared<RT> sh;
+  __shared__ __attribute__((aligned(16))) int id[top_max];
+  __shared__ __attribute__((aligned(16))) float pt[top_max];   // teacher logits, then p
+  const int t = static_cast<int>(threadIdx.x), wave = t >> 6, top = static_cast<int>(op.top);
+  const int padded = (top + 3) & ~3;
+  const float k = kLog2e / op.temperature;
+  for (int64_t row = blockIdx.x; row < op.tokens; row += gridDim.x) {
+    const T* p = static_cast<const T*>(op.logits) + row * op.ld_logits;
+    T* out = op.dlogits ? static_cast<T*>(op.dlogits) + row * op.ld_dlogits : nullptr;
+    const float weight = op.weights ? gld<float>(op.weights + row) : 1.f;
+    if (weight == 0.f) {
+      if (out) zero_row<T, RT>(out, static_cast<int>(op.vocab), t);
+      if (t == 0) gst<float>(op.loss + row, 0.f);
+      continue;
+    }
+    Row<T, RT, VPL> x{p, static_cast<int>(op.vocab), t};
+    x.fetch(0);
+    Soft teach{kNegInf, 0.f};
+    for (int e = t; e < padded; e += RT) {
+      int64_t i = -1;
+      float v = kNegInf;
+      if (e < top) {
+        i = id_at(op.ids, row * op.ld_ids + e, op.id_bytes);
+        v = op.teacher_dtype == MUON_BF16 ? value_at(static_cast<const uint16_t*>(op.teacher) + row * op.ld_teacher + e)
+                                          : value_at(static_cast<const float*>(op.teacher) + row * op.ld_teacher + e);
+        if (i < 0 || i >= op.vocab || v == kNegInf) {
+          i = -1;
+          v = kNegInf;
+        }
+      }
+      id[e] = static_cast<int>(i);
+      pt[e] = v;
+      const float m = fmaxf(teach.m, v);
+      teach.s = teach.s * shrink(teach.m, m, k) + exp2_fast((v - base_of(m)) * k);
+      teach.m = m;
+    }
+    teach = wave_join(teach, k);
+    const Soft mine = wave_join(x.stats(k), k);
+    if ((t & 63) == 0) {
+      sh.m[0][wave] = mine.m;
+      sh.s[0][wave] = mine.s;
+      sh.m[1][wave] = teach.m;
+      sh.s[1][wave] = teach.s;
+    }
+    __syncthreads();
+    const Soft q = block_join<RT>(sh, 0, k);
+    teach = block_join<RT>(sh, 1, k);
+    const bool none = teach.s == 0.f;               // no entry, no loss
+    const float base = base_of(q.m), lq = log2_fast(q.s), lt = log2_fast(teach.s), tbase = base_of(teach.m);
+    float part = 0.f;
+    for (int e = t; e < padded; e += RT) {
+      const int i = id[e];
+      float pe = 0.f;
+      if (i >= 0) {
+        const float le = (pt[e] - tbase) * k - lt;   // log2 of p
+        pe = exp2_fast(le);
+        if (pe != 0.f) part += pe * (le - ((value_at(p + i) - base) * k - lq));
+      }
+      pt[e] = pe;
+    }
+    part = wave_add(part);
+    if ((t & 63) == 0) sh.part[wave] = part;
+    const float a = weight * op.temperature;
+    if (out) {
+      if (none) zero_row<T, RT>(out, x.cols, t);
+      else x.scaled(out, base, k, a / q.s);
+    }
+    __syncthreads();
+    if (t == 0) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < RT / 64; ++w) sum += sh.part[w];
+      gst<float>(op.loss + row, none ? 0.f : a * op.temperature * kLn2 * sum);
+    }
+    if (out && !none)
+      for (int e = t; e < top; e += RT) {
+        const int i = id[e];
+        if (i < 0) continue;
+        float sum = 0.f;
+        for (int f = 0; f < padded; f += 4) {
+          const int4 ids = *reinterpret_cast<const int4*>(id + f);
+          const float4 ps = *reinterpret_cast<const float4*>(pt + f);
+          sum += ids.x == i ? ps.x : 0.f;
+          sum += ids.y == i ? ps.y : 0.f;
+          sum += ids.z == i ? ps.z : 0.f;
+          sum += ids.w == i ? ps.w : 0.f;
+        }
+        put_value(out + i, a * (exp2_fast((value_at(p + i) - base) * k) / q.s - sum));
+      }
+    if (row + gridDim.x < op.tokens) __syncthreads();   // (uniform) before the next row's entries
+  }
+}
+
+// ------------------------------------------------------------- policy loss ----
+// exp(d) - 1 - d, which d^2 / 2 ... carries where the difference would cancel.
+__device__ __forceinline__ float exp_less_linear(float d) {
+  if (fabsf(d) > 0.25f) return expm1f(d) - d;
+  return d * d * (0.5f + d * (1.f / 6 + d * (1.f / 24 + d * (1.f / 120 + d * (1.f / 720 + d * (1.f / 5040))))));
+}
+
+template <class T, int RT, int VPL>
+__global__ __launch_bounds__(RT) void k_policy(muon_policy_t op) {
+  __shared__ Shared<RT> sh;
+  const int t = static_cast<int>(threadIdx.x), wave = t >> 6;
+  const float k = kLog2e / op.temperature;
+  for (int64_t row = blockIdx.x; row < op.tokens; row += gridDim.x) {
+    const T* p = static_cast<const T*>(op.logits) + row * op.ld_logits;
+    T* out = op.dlogits ? static_cast<T*>(op.dlogits) + row * op.ld_dlogits : nullptr;
+    const float weight = op.weights ? gld<float>(op.weights + row) : 1.f;
+    const int64_t act = id_at(op.actions, row, op.id_bytes);
+    if (weight == 0.f || act < 0 || act >= op.vocab) {
+      if (out) zero_row<T, RT>(out, static_cast<int>(op.vocab), t);
+      if (t == 0) {
+        gst<float>(op.loss + row, 0.f);
+        if (op.logp) gst<float>(op.logp + row, 0.f);
+      }
+      continue;
+    }
+    Row<T, RT, VPL> x{p, static_cast<int>(op.vocab), t};
+    x.fetch(0);
+    const float xa = value_at(p + act), adv = gld<float>(op.advantages + row), old = gld<float>(op.old_logp + row),
+                ref = op.ref_logp ? gld<float>(op.ref_logp + row) : 0.f;
+    const Soft mine = wave_join(x.stats(k), k);
+    if ((t & 63) == 0) {
+      sh.m[0][wave] = mine.m;
+      sh.s[0][wave] = mine.s;
+    }
+    __syncthreads();
+    const Soft q = block_join<RT>(sh, 0, k);
+    const float base = base_of(q.m), la = (xa - base) * k;
+    const float logp = (la - log2_fast(q.s)) * kLn2;
+    const float ratio = expf(logp - old);
+    // an advantage of 0 has no part, whatever the ratio
+    const float free = adv == 0.f ? 0.f : ratio * adv;
+    const float held = fminf(fmaxf(ratio, 1.f - op.clip_low), 1.f + op.clip_high) * adv;
+    // a comparison that NaN fails lets it through
+    float loss = held < free ? -held : -free, slope = held < free ? 0.f : -free;
+    if (op.ref_logp) {
+      const float d = ref - logp;
+      loss += op.kl_coef * exp_less_linear(d);
+      slope -= op.kl_coef * expm1f(d);
+    }
+    if (t == 0) {
+      gst<float>(op.loss + row, weight * loss);
+      if (op.logp) gst<float>(op.logp + row, logp);
+    }
+    if (out) {
+      const float g = weight * slope / op.temperature;
+      x.scaled(out, base, k, -g / q.s);
+      // the action's column once more, by the thread that has just written it
+      if (static_cast<int>((act >> 3) % RT) == t) put_value(out + act, g * (1.f - exp2_fast(la) / q.s));
+    }
+    if (row + gridDim.x < op.tokens) __syncthreads();   // (uniform) before the next row's sums
+  }
+}
+
+// ---------------------------------------------------------------- dispatch ----
+// f(threads of a row, vectors of 8 columns a thread): few threads for short rows,
+// then as many vectors as registers hold beside two blocks a CU.
+template <class T, class F>
+int by_width(int64_t cols, F&& f) {
+  using std::integral_constant;
+  if (cols <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (cols <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  if (cols <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  if (cols <= 16384) return f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  if (cols <= 32768) return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+  if (cols <= 65536) return f(integral_constant<int, 1024>{}, integral_constant<int, 8>{});
+  if constexpr (sizeof(T) == 2)
+    if (cols <= 131072) return f(integral_constant<int, 1024>{}, integral_constant<int, 16>{});
+  return f(integral_constant<int, 1024>{}, integral_constant<int, 0>{});
+}
+
+constexpr int64_t kMaxGrid = int64_t(1) << 21;   // threads of a grid stay below 2^32
+
+unsigned rows_grid(int64_t tokens) { return static_cast<unsigned>(tokens < kMaxGrid ? tokens : kMaxGrid); }
+
+}  // namespace
+
+int launch_distill(const muon_distill_t& op, void* stream) {
+  auto run = [&](auto type) {
+    using T = decltype(type);
+    return by_width<T>(op.vocab, [&](auto rt, auto vpl) {
+      constexpr int RT = decltype(rt)::value, VPL = decltype(vpl)::value;
+      hipLaunchKernelGGL((k_distill<T, RT, VPL>), dim3(rows_grid(op.tokens)), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
+      return static_cast<int>(hipGetLastError());
+    });
+  };
+  return op.dtype == MUON_BF16 ? run(uint16_t{}) : run(float{});
+}
+
+int launch_policy(const muon_policy_t& op, void* stream) {
+  auto run = [&](auto type) {
+    using T = decltype(type);
+    return by_width<T>(op.vocab, [&](auto rt, auto vpl) {
+      constexpr int RT = decltype(rt)::value, VPL = decltype(vpl)::value;
+      hipLaunchKernelGGL((k_policy<T, RT, VPL>), dim3(rows_grid(op.tokens)), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
+      return static_cast<int>(hipGetLastError());
+    });
+  };
+  return op.dtype == MUON_BF16 ? run(uint16_t{}) : run(float{});
+}
+
+}  // namespace muon

@@ -63,6 +63,20 @@ class Args {
     return mat(a.codes, rows, cols, a.ld_codes, 1, written) &&
            mat(a.scales, rows, (cols + MUON_ACT8_GROUP - 1) / MUON_ACT8_GROUP, a.ld_scales, 1, written);
   }
+  // A tokens x heads x dim tensor of bf16.  As rows that `overlap` can tell apart
+  // where its axes allow it (heads side by side, in steps of one stride, or one after
+  // the other); else as everything from its first byte to its last.
+  bool heads(const muon_heads_t& t, int64_t tokens, int64_t heads, int64_t dim, bool written) {
+    const int64_t lt = t.ld_token, lh = t.ld_head;
+    if (tokens == 0 || heads == 1) return mat(t.data, tokens, dim, lt, 2, written);
+    if (tokens == 1) return mat(t.data, heads, dim, lh, 2, written);
+    if (lt < dim || lh < dim || lt > kMaxSpan / tokens || lh > kMaxSpan / heads) return false;
+    if (lh == dim) return mat(t.data, tokens, heads * dim, lt, 2, written);
+    if (lt == heads * lh) return mat(t.data, tokens * heads, dim, lh, 2, written);
+    if (lh == tokens * lt) return mat(t.data, tokens * heads, dim, lt, 2, written);
+    if (lt < (heads - 1) * lh + dim && lh < (tokens - 1) * lt + dim) return false;
+    return mat(t.data, 1, (tokens - 1) * lt + (heads - 1) * lh + dim, 0, 2, written);
+  }
   bool vec(const void* p, int64_t n, size_t esize, bool written, bool need) { return n == 0 || mat(p, 1, n, n, esize, written, need); }
   bool clash() const {
     for (int i = 0; i < n_out_; ++i) {
@@ -75,7 +89,7 @@ class Args {
   }
 
  private:
-  Span in_[10], out_[10];   // more than any call notes
+  Span in_[12], out_[10];   // more than any call notes
   int n_in_ = 0, n_out_ = 0;
 };
 
@@ -119,6 +133,35 @@ class Launcher {
 
 bool workspace_ok(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws && have >= need && is_aligned(ws, 256));
+}
+
+// Sizes and options that both directions of attention have.
+template <class Op>
+bool attention_ok(const Op* op, int32_t zero_bits) {
+  constexpr int64_t max_tokens = int64_t(1) << 30, max_blocks = int64_t(1) << 23;
+  if (!op || op->reserved || op->tokens < 0 || op->tokens > max_tokens || op->k_tokens < 0 || op->k_tokens > max_tokens ||
+      op->heads < 1 || op->heads > max_blocks || op->kv_heads < 1 || op->heads % op->kv_heads || op->dim < 8 ||
+      op->dim > MUON_ATTN_MAX_DIM || op->dim % 8 || !(op->scale > 0.f) || !std::isfinite(op->scale) ||
+      (op->causal != 0 && op->causal != 1) || (op->zero_rest & ~zero_bits))
+    return false;
+  if (!op->starts ? op->k_starts != nullptr
+                  : op->sequences < 0 || op->sequences > max_blocks || (!op->k_starts && op->tokens != op->k_tokens))
+    return false;
+  const int64_t rows = op->tokens > op->k_tokens ? op->tokens : op->k_tokens;
+  return (rows / 128 + (op->starts ? op->sequences : 0) + 2) * op->heads <= max_blocks;
+}
+
+// Strides of axes of length one are not read: the kernels get ones that fit.
+muon_heads_t heads_strides(muon_heads_t t, int64_t tokens, int64_t heads) {
+  if (tokens <= 1) t.ld_token = MUON_ATTN_MAX_DIM;
+  if (heads <= 1) t.ld_head = 0;
+  return t;
+}
+
+template <class Op>
+bool note_starts(Args& a, const Op* op) {
+  return a.vec(op->starts, op->starts ? op->sequences + 1 : 0, 4, false, false) &&
+         a.vec(op->k_starts, op->k_starts ? op->sequences + 1 : 0, 4, false, false);
 }
 
 }  // namespace
@@ -341,6 +384,99 @@ int muon_embed_grad(const muon_embed_grad_t* op, void* workspace, size_t workspa
   }
   if (int rc = l.run("embedding gradient, sums", [&](void* st) { return launch_embed_sums(*op, p, ws, st); })) return rc;
   return l.run("embedding gradient, join", [&](void* st) { return launch_embed_join(*op, p, ws, st); });
+}
+
+int muon_attention(const muon_attention_t* op, hipStream_t stream) {
+  Args a;
+  if (!attention_ok(op, MUON_ATTN_ZERO_O | MUON_ATTN_ZERO_LSE)) return MUON_EINVAL;
+  const int64_t n = op->tokens, nk = op->k_tokens;
+  if (!a.heads(op->q, n, op->heads, op->dim, false) || !a.heads(op->k, nk, op->kv_heads, op->dim, false) ||
+      !a.heads(op->v, nk, op->kv_heads, op->dim, false) || !a.heads(op->o, n, op->heads, op->dim, true) ||
+      (n > 0 && !a.mat(op->lse, op->heads, n, op->ld_lse, 4, true, false)) || !note_starts(a, op))
+    return MUON_EINVAL;
+  if (a.clash()) return MUON_EALIAS;
+  if (n == 0) return MUON_OK;
+  muon_attention_t in = *op;
+  in.q = heads_strides(op->q, n, op->heads);
+  in.o = heads_strides(op->o, n, op->heads);
+  in.k = heads_strides(op->k, nk, op->kv_heads);
+  in.v = heads_strides(op->v, nk, op->kv_heads);
+  Launcher l(stream);
+  if (int rc = l.open()) return rc;
+  return l.run("attention", [&](void* st) { return launch_attention(in, st); });
+}
+
+size_t muon_attention_grad_workspace_bytes(int64_t tokens, int64_t heads) {
+  if (tokens < 0 || heads < 1 || tokens > (int64_t(1) << 30) || heads > (int64_t(1) << 23)) return 0;
+  return static_cast<size_t>(tokens) * static_cast<size_t>(heads) * 2 * sizeof(float);
+}
+
+int muon_attention_grad(const muon_attention_grad_t* op, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  Args a;
+  if (!attention_ok(op, MUON_ATTN_ZERO_DQ | MUON_ATTN_ZERO_DK | MUON_ATTN_ZERO_DV)) return MUON_EINVAL;
+  const int64_t n = op->tokens, nk = op->k_tokens, h = op->heads, kv = op->kv_heads, d = op->dim;
+  if (!a.heads(op->dout, n, h, d, false) || !a.heads(op->q, n, h, d, false) || !a.heads(op->o, n, h, d, false) ||
+      !a.heads(op->k, nk, kv, d, false) || !a.heads(op->v, nk, kv, d, false) || !a.heads(op->dq, n, h, d, true) ||
+      !a.heads(op->dk, nk, kv, d, true) || !a.heads(op->dv, nk, kv, d, true) ||
+      (n > 0 && !a.mat(op->lse, h, n, op->ld_lse, 4, false)) || !note_starts(a, op))
+    return MUON_EINVAL;
+  const size_t need = muon_attention_grad_workspace_bytes(n, h);
+  if (!workspace_ok(workspace, workspace_bytes, need)) return MUON_EWORKSPACE;
+  if (need && !a.mat(workspace, 1, static_cast<int64_t>(need), 0, 1, true)) return MUON_EWORKSPACE;
+  if (a.clash()) return MUON_EALIAS;
+  if (n == 0 && nk == 0) return MUON_OK;
+  muon_attention_grad_t in = *op;
+  for (muon_heads_t* t : {&in.dout, &in.q, &in.o, &in.dq}) *t = heads_strides(*t, n, h);
+  for (muon_heads_t* t : {&in.k, &in.v, &in.dk, &in.dv}) *t = heads_strides(*t, nk, kv);
+  Launcher l(stream);
+  if (int rc = l.open()) return rc;
+  if (int rc = l.poison(workspace, need)) return rc;
+  float* stats = static_cast<float*>(workspace);
+  if (n > 0)
+    if (int rc = l.run("attention gradient, queries", [&](void* st) { return launch_attention_dq(in, stats, st); })) return rc;
+  if (nk == 0) return MUON_OK;
+  return l.run("attention gradient, keys", [&](void* st) { return launch_attention_dkv(in, stats, st); });
+}
+
+static bool temperature_ok(float t) { return t >= 1e-6f && t <= 1e6f; }
+
+int muon_distill(const muon_distill_t* op, hipStream_t stream) {
+  Args a;
+  if (!op || !type_ok(op->dtype) || !type_ok(op->teacher_dtype) || !size_ok(op->tokens, op->vocab) || op->top < 1 ||
+      op->top > MUON_DISTILL_MAX_TOP || (op->id_bytes != 4 && op->id_bytes != 8) || !temperature_ok(op->temperature))
+    return MUON_EINVAL;
+  const int64_t n = op->tokens;
+  const size_t es = type_size(op->dtype);
+  if (!a.mat(op->logits, n, op->vocab, op->ld_logits, es, false) || !a.mat(op->ids, n, op->top, op->ld_ids, op->id_bytes, false) ||
+      !a.mat(op->teacher, n, op->top, op->ld_teacher, type_size(op->teacher_dtype), false) ||
+      !a.vec(op->weights, n, 4, false, false) || !a.vec(op->loss, n, 4, true, true) ||
+      !a.mat(op->dlogits, n, op->vocab, op->ld_dlogits, es, true, false))
+    return MUON_EINVAL;
+  if (a.clash()) return MUON_EALIAS;
+  if (n == 0) return MUON_OK;
+  Launcher l(stream);
+  if (int rc = l.open()) return rc;
+  return l.run("distillation loss", [&](void* st) { return launch_distill(*op, st); });
+}
+
+int muon_policy(const muon_policy_t* op, hipStream_t stream) {
+  Args a;
+  if (!op || !type_ok(op->dtype) || !size_ok(op->tokens, op->vocab) || (op->id_bytes != 4 && op->id_bytes != 8) ||
+      !temperature_ok(op->temperature) || !(op->clip_low >= 0.f && op->clip_low <= 1.f) || !(op->clip_high >= 0.f) ||
+      !std::isfinite(op->clip_high) || !std::isfinite(op->kl_coef))
+    return MUON_EINVAL;
+  const int64_t n = op->tokens;
+  const size_t es = type_size(op->dtype);
+  if (!a.mat(op->logits, n, op->vocab, op->ld_logits, es, false) || !a.vec(op->actions, n, op->id_bytes, false, true) ||
+      !a.vec(op->old_logp, n, 4, false, true) || !a.vec(op->advantages, n, 4, false, true) ||
+      !a.vec(op->ref_logp, n, 4, false, false) || !a.vec(op->weights, n, 4, false, false) || !a.vec(op->loss, n, 4, true, true) ||
+      !a.vec(op->logp, n, 4, true, false) || !a.mat(op->dlogits, n, op->vocab, op->ld_dlogits, es, true, false))
+    return MUON_EINVAL;
+  if (a.clash()) return MUON_EALIAS;
+  if (n == 0) return MUON_OK;
+  Launcher l(stream);
+  if (int rc = l.open()) return rc;
+  return l.run("policy loss", [&](void* st) { return launch_policy(*op, st); });
 }
 
 }  // extern "C"

@@ -76,4 +76,14 @@ int launch_embed_starts(const muon_embed_grad_t& op, const EmbedSortPlan& p, cha
 int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
 int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
 
+// muon_attn.hip.  stats: heads x tokens of lse and of rowsum(dout o), left by the
+// first kernel of the backward pass for the second.
+int launch_attention(const muon_attention_t& op, void* stream);
+int launch_attention_dq(const muon_attention_grad_t& op, float* stats, void* stream);
+int launch_attention_dkv(const muon_attention_grad_t& op, const float* stats, void* stream);
+
+// muon_loss.hip
+int launch_distill(const muon_distill_t& op, void* stream);
+int launch_policy(const muon_policy_t& op, void* stream);
+
 }  // namespace muon

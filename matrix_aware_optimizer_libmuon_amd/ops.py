@@ -11,6 +11,14 @@ runs in libmuon.so, on the current stream of the tensors' device, or on
     dx, dgain = muon.rmsnorm_act8_grad(dy, n8, rstd, gain, dres=dh)
     table_grad = muon.embed_grad(dx, ids, vocab)
 
+Beside them attention with its backward pass and two losses that return the
+gradient of the logits:
+
+    o, lse = muon.attention(q, k, v, starts=starts)
+    dq, dk, dv = muon.attention_grad(do, q, k, v, o, lse, starts=starts)
+    loss, dlogits = muon.distill_loss(logits, ids, teacher, temperature=2.0)
+    loss, logp, dlogits = muon.policy_loss(logits, actions, old_logp, advantages)
+
 Matrices are 2-D with unit column stride, float32 or bfloat16; rows may be
 strided (a column slice of a wider buffer is one).  The operators take no part in
 autograd: what they return has no history, whether or not an argument requires a
@@ -43,7 +51,8 @@ def _calls():
     if _bound is None:
         m, lib = _marshaller(), _lib.load()
         m.bind_ops({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
-                    for n in _lib.EXPORTED if n.startswith(("muon_act8", "muon_rmsnorm", "muon_swiglu", "muon_embed"))})
+                    for n in _lib.EXPORTED if n.startswith(("muon_act8", "muon_rmsnorm", "muon_swiglu", "muon_embed", "muon_attention",
+                                      "muon_distill", "muon_policy"))})
         _bound = m
     return _bound
 
@@ -140,3 +149,58 @@ def embed_grad(dy, ids, vocab: int, *, scale: float = 1.0, out=None, dtype=torch
     row of the result is written; with ``accumulate`` the sums are added to
     ``out``, of which only the rows that have tokens are touched."""
     return _run("embed_grad", dy, stream, dy, ids, int(vocab), float(scale), out, dtype, bool(accumulate))[0]
+
+
+def attention(q, k, v, *, starts=None, k_starts=None, causal: bool = True, scale: float | None = None, out=None, stream=None):
+    """Softmax attention: (o, lse) of bfloat16 q (tokens, heads, dim) and k, v
+    (k_tokens, kv_heads, dim); query head h reads key and value head
+    h // (heads // kv_heads).  dim: a multiple of 8, at most 128.  The last axis has
+    unit stride; tokens and heads may be strided (slices of a fused projection).
+
+    ``starts`` (int32, on the GPU, from 0, not decreasing) holds the first token of
+    each sequence and the end of the last; None is one sequence.  ``k_starts``: that
+    of k and v, where it differs.  ``causal``: query i of nq sees keys j <= i + nk - nq.
+    ``scale``: 1 / sqrt(dim) if None.  lse (float32, (heads, tokens)) is each row's log
+    of the sum of exponentials, for the backward pass; a query that sees no key gets
+    zeros and -infinity.  Tokens behind the last sequence: left as they are in
+    ``out``, zeros in a new tensor; their lse is -infinity."""
+    return tuple(_run("attention", q, stream, q, k, v, starts, k_starts, bool(causal), None if scale is None else float(scale), out))
+
+
+def attention_grad(do, q, k, v, o, lse, *, starts=None, k_starts=None, causal: bool = True, scale: float | None = None, dq=None,
+                   dk=None, dv=None, stream=None):
+    """(dq, dk, dv) of attention() for the gradient ``do`` of o, from what it took and
+    returned; the probabilities are computed again.  ``dq``, ``dk`` and ``dv`` may be
+    given, e.g. as slices of one buffer."""
+    return tuple(_run("attention_grad", do, stream, do, q, k, v, o, lse, starts, k_starts, bool(causal),
+                      None if scale is None else float(scale), dq, dk, dv))
+
+
+def distill_loss(logits, ids, teacher, *, temperature: float = 1.0, weights=None, want_grad: bool = True, out=None, stream=None):
+    """Distillation from a teacher's top logits: (loss, dlogits).  Row by row, with
+    p the softmax of ``teacher`` / temperature (tokens, top) and q that of all
+    ``logits`` / temperature (tokens, vocab):
+
+        loss = weight * temperature^2 * sum_k p_k (log p_k - log q[ids_k])
+
+    float32 per token, and ``dlogits`` the gradient of loss.sum(), in the logits'
+    type (None if not wanted).  ``ids``: int32 or int64; an entry outside the
+    vocabulary (-1) is not there; at most 1024 entries a token.  ``weights``: float32
+    per token, e.g. a mask over the number of tokens; at 0 the logits are not read."""
+    return tuple(_run("distill_loss", logits, stream, logits, ids, teacher, weights, out, float(temperature), bool(want_grad)))
+
+
+def policy_loss(logits, actions, old_logp, advantages, *, ref_logp=None, clip: float = 0.2, clip_high: float | None = None,
+                kl_coef: float = 0.0, temperature: float = 1.0, weights=None, want_grad: bool = True, out=None, stream=None):
+    """Clipped policy loss with a KL term: (loss, logp, dlogits).  Token by token,
+    with logp the action's log-probability under softmax(logits / temperature), r =
+    exp(logp - old_logp) and d = ref_logp - logp:
+
+        loss = weight * (-min(r A, clamp(r, 1 - clip, 1 + clip_high) A) + kl_coef (exp(d) - d - 1))
+
+    float32 per token, and ``dlogits`` the gradient of loss.sum(), in the logits' type
+    (None if not wanted).  No KL term without ``ref_logp``; ``clip_high``: clip if None.
+    ``weights``: float32 per token; a token of weight 0, or whose action is outside
+    the vocabulary, has loss and logp 0, and its logits are not read."""
+    return tuple(_run("policy_loss", logits, stream, logits, actions, old_logp, advantages, ref_logp, weights, out, float(clip),
+                      float(clip if clip_high is None else clip_high), float(kl_coef), float(temperature), bool(want_grad)))

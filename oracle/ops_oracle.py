@@ -119,3 +119,77 @@ def embed_grad(dy, ids, vocab, scale, base=None):
         if 0 <= i < vocab:
             out[i] += dy[t] * scale
     return out
+
+
+def visible(nq, nk, causal):
+    """Which keys each query sees (a causal mask is aligned at the end)."""
+    if not causal:
+        return np.ones((nq, nk), dtype=bool)
+    return np.arange(nk)[None, :] <= np.arange(nq)[:, None] + (nk - nq)
+
+
+def attention(q, k, v, scale, causal):
+    """(o, lse) of one sequence and head."""
+    s = np.where(visible(len(q), len(k), causal), scale * (q @ k.T), -np.inf)
+    top = s.max(1, initial=-np.inf, keepdims=True)
+    base = np.where(np.isfinite(top), top, 0.0)
+    e = np.exp(s - base)
+    total = e.sum(1, keepdims=True)
+    with np.errstate(divide="ignore"):
+        lse = np.where(total > 0, base + np.log(total), -np.inf)
+    return (e / np.where(total > 0, total, 1.0)) @ v, lse[:, 0]
+
+
+def attention_grad(do, q, k, v, o, lse, scale, causal):
+    """(dq, dk, dv) of one sequence and head, from the rows' o and lse."""
+    see = visible(len(q), len(k), causal)
+    with np.errstate(invalid="ignore", over="ignore"):
+        p = np.where(see, np.exp(scale * (q @ k.T) - lse[:, None]), 0.0)
+    ds = p * (do @ v.T - (do * o).sum(1, keepdims=True))
+    return scale * (ds @ k), scale * (ds.T @ q), p.T @ do
+
+
+def log_softmax(x):
+    top = x.max(1, keepdims=True)
+    return x - top - np.log(np.exp(x - top).sum(1, keepdims=True))
+
+
+def distill(logits, ids, teacher, temperature, weights):
+    """(loss, dlogits), row by row, entry by entry."""
+    loss, grad = np.zeros(len(logits)), np.zeros(logits.shape)
+    for t, w in enumerate(weights):
+        live = (ids[t] >= 0) & (ids[t] < logits.shape[1]) & (teacher[t] != -np.inf)
+        if w == 0 or not live.any():
+            continue
+        logp = log_softmax(teacher[t:t + 1, live] / temperature)[0]
+        logq = log_softmax(logits[t:t + 1] / temperature)[0]
+        grad[t] = np.exp(logq)
+        for i, lp in zip(ids[t][live], logp):
+            if np.exp(lp) > 0:
+                loss[t] += np.exp(lp) * (lp - logq[i])
+            grad[t, i] -= np.exp(lp)
+        loss[t] *= w * temperature ** 2
+        grad[t] *= w * temperature
+    return loss, grad
+
+
+def policy(logits, actions, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef, temperature, weights):
+    """(loss, logp, dlogits), row by row."""
+    loss, logp, grad = np.zeros(len(logits)), np.zeros(len(logits)), np.zeros(logits.shape)
+    for t, (a, w, adv) in enumerate(zip(actions, weights, advantages)):
+        if w == 0 or not 0 <= a < logits.shape[1]:
+            continue
+        logq = log_softmax(logits[t:t + 1] / temperature)[0]
+        logp[t] = logq[a]
+        r = np.exp(logq[a] - old_logp[t])
+        held = np.clip(r, 1 - clip_low, 1 + clip_high)
+        loss[t], g = -min(r * adv, held * adv), -adv * r * (r * adv <= held * adv)
+        if ref_logp is not None:
+            d = ref_logp[t] - logq[a]
+            loss[t] += kl_coef * (np.exp(d) - d - 1)
+            g += kl_coef * (1 - np.exp(d))
+        loss[t] *= w
+        grad[t] = -np.exp(logq)
+        grad[t, a] += 1
+        grad[t] *= w * g / temperature
+    return loss, logp, grad

@@ -71,7 +71,45 @@ def _child():
     def act8(cols):
         return L.MuonAct8(ptr(), ptr(), cols, -(-cols // 32))
 
-    def call(entry, rows=0, cols=0, tokens=0, vocab=0, n=0, k=0, dtype="f32", accumulate=0):
+    def heads(n, dim):
+        return L.MuonHeads(ptr(), n * dim, dim)
+
+    def attention(entry, tokens, k_tokens, heads_, kv, dim, sequences, odd=False, layout=None):
+        ends = dict(starts=ptr() if sequences else None, k_starts=ptr() if sequences else None, sequences=sequences, tokens=tokens,
+                    k_tokens=k_tokens, heads=heads_, kv_heads=kv, dim=dim, ld_lse=max(tokens, 1), scale=1.0, causal=1, zero_rest=3)
+        own, shared = (lambda: heads(heads_, dim)), (lambda: heads(kv, dim))
+        q, k, v = own(), shared(), shared()
+        if layout:                                   # all heads of a kind in one buffer (tokens == k_tokens, heads_ == kv)
+            base, places = ptr(), iter(range(9))
+            own = shared = {  # noqa: E731
+                "side by side": lambda: L.MuonHeads(base + 2 * next(places) * heads_ * dim, 9 * heads_ * dim, dim),
+                "in steps": lambda: L.MuonHeads(base + 2 * next(places) * dim, heads_ * 9 * dim, 9 * dim),
+                "one after the other": lambda: L.MuonHeads(base + 2 * next(places) * heads_ * tokens * dim, dim, tokens * dim)}[layout]
+            q, k, v = own(), own(), own()
+        if odd:                                      # rows on 2 bytes
+            q.data += 2
+            v.data += 2
+        if entry == "attention":
+            return lib.muon_attention(ctypes.byref(L.MuonAttention(q=q, k=k, v=v, o=own(), lse=ptr(), **ends)), None)
+        op = L.MuonAttentionGrad(dout=own(), q=q, k=k, v=v, o=own(), dq=own(), dk=shared(), dv=shared(), lse=ptr(), **ends)
+        return lib.muon_attention_grad(ctypes.byref(op), ctypes.c_void_p(1 << 60),
+                                       lib.muon_attention_grad_workspace_bytes(tokens, heads_), None)
+
+    def loss(entry, tokens, vocab, dtype):
+        t = L.MUON_BF16 if dtype == "bf16" else L.MUON_F32
+        if entry == "distill":
+            return lib.muon_distill(ctypes.byref(L.MuonDistill(
+                logits=ptr(), ids=ptr(), teacher=ptr(), loss=ptr(), dlogits=ptr(), tokens=tokens, vocab=vocab, top=4, ld_logits=vocab,
+                ld_ids=4, ld_teacher=4, ld_dlogits=vocab, temperature=1.0, dtype=t, teacher_dtype=L.MUON_F32, id_bytes=4)), None)
+        return lib.muon_policy(ctypes.byref(L.MuonPolicy(
+            logits=ptr(), actions=ptr(), old_logp=ptr(), advantages=ptr(), loss=ptr(), dlogits=ptr(), tokens=tokens, vocab=vocab,
+            ld_logits=vocab, ld_dlogits=vocab, temperature=1.0, dtype=t, id_bytes=4)), None)
+
+    def call(entry, rows=0, cols=0, tokens=0, vocab=0, n=0, k=0, dtype="f32", accumulate=0, **more):
+        if entry.startswith("attention"):
+            return attention(entry, tokens, **more)
+        if entry in ("distill", "policy"):
+            return loss(entry, tokens, vocab, dtype)
         t, ws = L.MUON_BF16 if dtype == "bf16" else L.MUON_F32, ctypes.c_void_p(1 << 60)
         ref = ctypes.byref
         if entry == "act8_pack":

@@ -242,3 +242,122 @@ def test_embedding_gradient_workspace_is_the_sum_of_its_parts(lib, tokens, vocab
             want += up(-(-tokens // step) * 512)
         want += up((((vocab >> log_buckets) + 1) << log_buckets) + 1) + up(-(-tokens // 32) * 2 * cols)
     assert lib.muon_embed_grad_workspace_bytes(tokens, vocab, cols) == want
+
+
+def heads(n=4, dim=64, **kw):
+    return with_(L.MuonHeads(ptr(), n * dim, dim), **kw)
+
+
+SIZES = dict(tokens=40, k_tokens=40, heads=4, kv_heads=2, dim=64, ld_lse=40, scale=0.125, causal=1)
+
+
+def attn(**kw):
+    return with_(L.MuonAttention(q=heads(), k=heads(2), v=heads(2), o=heads(), lse=ptr(), **SIZES), **kw)
+
+
+def attn_grad(**kw):
+    return with_(L.MuonAttentionGrad(dout=heads(), q=heads(), k=heads(2), v=heads(2), o=heads(), dq=heads(), dk=heads(2), dv=heads(2),
+                                     lse=ptr(), **SIZES), **kw)
+
+
+def test_struct_layouts_of_attention_and_losses_match_header(lib):
+    sizes = muon._marshaller().OP_BYTES
+    for name, cls in (("muon_attention_t", L.MuonAttention), ("muon_attention_grad_t", L.MuonAttentionGrad),
+                      ("muon_distill_t", L.MuonDistill), ("muon_policy_t", L.MuonPolicy)):
+        assert sizes[name] == ctypes.sizeof(cls), name
+
+
+BAD_ATTENTION = [
+    dict(tokens=-1), dict(tokens=(1 << 30) + 1), dict(k_tokens=-1), dict(heads=0), dict(kv_heads=0), dict(kv_heads=3), dict(dim=0),
+    dict(dim=60), dict(dim=136), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(causal=2),
+    dict(zero_rest=8), dict(zero_rest=-1), dict(reserved=1), dict(k_starts=1 << 40), dict(starts=1 << 40, sequences=-1),
+    dict(starts=(1 << 40) + 2, sequences=1), dict(starts=1 << 40, sequences=1, k_tokens=39), dict(starts=1 << 40, sequences=1 << 22),
+    dict(ld_lse=39), dict(lse=(1 << 41) + 1), dict(q=heads(data=0)), dict(k=heads(2, data=0)), dict(v=heads(2, data=(1 << 41) + 1)),
+    dict(q=heads(ld_token=0)), dict(q=heads(ld_head=0)), dict(k=heads(2, ld_token=64)), dict(k=heads(2, ld_token=128, ld_head=65)),
+    dict(q=heads(ld_token=1 << 60)), dict(q=heads(ld_head=1 << 60)), dict(q=heads(ld_token=-256))]
+
+
+def test_attention_refuses(lib):
+    def fwd(**kw):
+        return lib.muon_attention(ctypes.byref(attn(**kw)), None)
+
+    assert lib.muon_attention(None, None) == EINVAL
+    for bad in [*BAD_ATTENTION, dict(o=heads(data=0)), dict(zero_rest=4), dict(o=heads(ld_token=64))]:
+        assert fwd(**bad) == EINVAL, bad
+    p = ptr()
+    assert fwd(q=heads(data=p), o=heads(data=p)) == EALIAS and fwd(o=heads(data=p), lse=p + 64) == EALIAS
+    assert fwd(starts=p, sequences=3, lse=p + 12) == EALIAS
+    # slices of one buffer, side by side, in steps of one stride, one after the other: shifted by 8 columns they overlap
+    # (tests/test_ops_launches.py: unshifted they do not)
+    wide = lambda at: heads(4, data=p + 2 * at, ld_token=10 * 64)  # noqa: E731
+    mixed = lambda at: heads(4, data=p + 2 * at, ld_token=4 * 192, ld_head=192)  # noqa: E731
+    first = lambda at: heads(4, data=p + 2 * at, ld_token=64, ld_head=40 * 64)  # noqa: E731
+    for make, apart in ((wide, 256), (mixed, 64), (first, 4 * 40 * 64)):
+        assert fwd(q=make(0), o=make(apart - 8)) == EALIAS and fwd(q=make(apart - 8), o=make(0)) == EALIAS
+    # nothing to do
+    assert fwd(tokens=0, q=heads(data=0), o=heads(data=0), lse=0) == 0
+
+
+def test_attention_gradient_refuses(lib):
+    need = lib.muon_attention_grad_workspace_bytes(40, 4)
+    assert need == 2 * 4 * 40 * 4 and lib.muon_attention_grad_workspace_bytes(0, 4) == 0
+    assert lib.muon_attention_grad_workspace_bytes(-1, 4) == 0 and lib.muon_attention_grad_workspace_bytes(4, 0) == 0
+
+    def bwd(ws=WS, ws_bytes=need, **kw):
+        return lib.muon_attention_grad(ctypes.byref(attn_grad(**kw)), ws, ws_bytes, None)
+
+    assert lib.muon_attention_grad(None, WS, need, None) == EINVAL
+    for bad in [*BAD_ATTENTION, dict(lse=0), dict(dout=heads(data=0)), dict(o=heads(data=0)), dict(dq=heads(data=0)),
+                dict(dk=heads(2, data=0)), dict(dv=heads(2, ld_token=64))]:
+        assert bwd(**bad) == EINVAL, bad
+    assert bwd(ws=None) == EWORKSPACE and bwd(ws_bytes=need - 1) == EWORKSPACE and bwd(ws=ctypes.c_void_p((1 << 42) + 8)) == EWORKSPACE
+    p = ptr()
+    assert bwd(dq=heads(data=1 << 42)) == EALIAS and bwd(dk=heads(2, data=p), dv=heads(2, data=p)) == EALIAS
+    assert bwd(q=heads(data=p), dq=heads(data=p)) == EALIAS and bwd(lse=p, dv=heads(2, data=p)) == EALIAS
+    assert bwd(tokens=0, k_tokens=0, ws=None, ws_bytes=0) == 0
+
+
+def distill(**kw):
+    return with_(L.MuonDistill(logits=ptr(), ids=ptr(), teacher=ptr(), weights=ptr(), loss=ptr(), dlogits=ptr(), tokens=9, vocab=50, top=4,
+                               ld_logits=50, ld_ids=4, ld_teacher=4, ld_dlogits=50, temperature=1.0, dtype=F32, teacher_dtype=F32,
+                               id_bytes=8), **kw)
+
+
+def policy(**kw):
+    return with_(L.MuonPolicy(logits=ptr(), actions=ptr(), old_logp=ptr(), advantages=ptr(), ref_logp=ptr(), weights=ptr(), loss=ptr(),
+                              logp=ptr(), dlogits=ptr(), tokens=9, vocab=50, ld_logits=50, ld_dlogits=50, clip_low=0.2, clip_high=0.2,
+                              kl_coef=0.1, temperature=1.0, dtype=F32, id_bytes=8), **kw)
+
+
+def test_losses_refuse(lib):
+    def dis(**kw):
+        return lib.muon_distill(ctypes.byref(distill(**kw)), None)
+
+    def pol(**kw):
+        return lib.muon_policy(ctypes.byref(policy(**kw)), None)
+
+    assert lib.muon_distill(None, None) == EINVAL and lib.muon_policy(None, None) == EINVAL
+    nan, inf = float("nan"), float("inf")
+    both = [dict(logits=0), dict(loss=0), dict(tokens=-1), dict(tokens=1 << 31), dict(vocab=0), dict(vocab=(1 << 20) + 1), dict(dtype=5),
+            dict(id_bytes=2), dict(ld_logits=49), dict(ld_dlogits=49), dict(temperature=0.0), dict(temperature=-1.0),
+            dict(temperature=nan), dict(temperature=inf), dict(logits=(1 << 41) + 2), dict(loss=(1 << 41) + 2),
+            dict(weights=(1 << 41) + 1)]
+    for bad in [*both, dict(ids=0), dict(teacher=0), dict(top=0), dict(top=1025), dict(teacher_dtype=3), dict(ld_ids=3), dict(ld_teacher=3),
+                dict(ids=(1 << 41) + 4)]:
+        assert dis(**bad) == EINVAL, bad
+    for bad in [*both, dict(actions=0), dict(old_logp=0), dict(advantages=0), dict(clip_low=-0.1), dict(clip_low=1.1), dict(clip_low=nan),
+                dict(clip_high=-1.0), dict(clip_high=inf), dict(kl_coef=nan), dict(kl_coef=inf), dict(logp=(1 << 41) + 2)]:
+        assert pol(**bad) == EINVAL, bad
+    p = ptr()
+    assert dis(logits=p, dlogits=p) == EALIAS and dis(loss=p, weights=p) == EALIAS and dis(ids=p, dlogits=p + 64) == EALIAS
+    assert pol(logits=p, dlogits=p) == EALIAS and pol(loss=p, logp=p + 32) == EALIAS and pol(logp=p, old_logp=p) == EALIAS
+    assert dis(tokens=0, logits=0, loss=0) == 0 and pol(tokens=0, logits=0, actions=0) == 0
+
+
+def test_binding_of_attention_and_losses_refuses_cpu_tensors(lib):
+    q, x, v = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 64), torch.zeros(4)
+    i = torch.zeros(4, dtype=torch.int64)
+    for call in (lambda: muon.attention(q, q, q), lambda: muon.attention_grad(q, q, q, q, q, x), lambda: muon.distill_loss(x, i[:, None], x),
+                 lambda: muon.policy_loss(x, i, v, v)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()

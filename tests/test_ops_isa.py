@@ -45,3 +45,16 @@ def test_weight_gradient_keeps_the_wait_states(tmp_path):
     # and the one wait state after a scalar write of m0
     assert len(re.findall(r"s_nop 0\s+buffer_load_\w+ .* offen lds", text)) == n
     assert not bad, [(h.load, h.writer, h.wait_states) for h in bad[:5]]
+
+
+@pytest.mark.skipif(not (os.path.exists(HIPCC) or shutil.which(HIPCC)), reason="hipcc not available")
+def test_attention_keeps_the_wait_states(tmp_path):
+    """Every load to LDS comes behind 5 wait states of its own."""
+    src, extra = next(s for s in build.SOURCES if s[0] == "muon_attn.hip")
+    out = str(tmp_path / "attn.s")
+    r = subprocess.run([HIPCC, *build.FLAGS, *extra, "--offload-device-only", "-S", "-o", out, os.path.join(build.CSRC, src)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    text = open(out).read()
+    loads = re.findall(r"buffer_load_\w+ .* offen lds", text)
+    assert len(loads) > 100 and len(re.findall(r"s_nop 4\s+buffer_load_\w+ .* offen lds", text)) == len(loads)

@@ -64,3 +64,46 @@ def test_weight_gradient_plans_of_the_tested_sizes():
         (3000, 1104, 1296): ((256, 128), "none", 4, False), (3001, 1101, 1303): ((256, 128), "none", 4, True),
         (4000, 3000, 3000): ((256, 128), "some", 5, False), (2383, 5955, 1406): ((128, 128), "some", 15, True),
         (6000, 520, 264): ((128, 128), "none", 16, False)}
+
+
+ATTN_MAX = 1 << 30                                # tokens of attention
+
+
+@pytest.mark.parametrize("entry", ["attention", "attention_grad"])
+@pytest.mark.parametrize("args", [
+    dict(tokens=ATTN_MAX - 128 * 3, k_tokens=ATTN_MAX - 128 * 3, heads_=1, kv=1, dim=64, sequences=0),
+    dict(tokens=1, k_tokens=1, heads_=4, kv=2, dim=128, sequences=(1 << 21) - 2),
+    dict(tokens=1 << 20, k_tokens=(1 << 20) - 5, heads_=512, kv=512, dim=80, sequences=1000),
+], ids=lambda v: "x".join(str(x) for x in v.values()))
+def test_the_largest_attention_can_be_launched(entry, args):
+    (status, launches), = record([(entry, args)])
+    assert status == 0 and len(launches) == (1 if entry == "attention" else 2)
+    for kernel, grid, block in launches:
+        assert 0 < grid[0] * block[0] < 1 << 32 and grid[1:] == (1, 1), (kernel, grid, block)
+
+
+@pytest.mark.parametrize("entry", ["distill", "policy"])
+@pytest.mark.parametrize("args", [dict(tokens=MAX, vocab=40), dict(tokens=MAX, vocab=40, dtype="bf16"), dict(tokens=1 << 20, vocab=1 << 20)],
+                         ids=lambda v: "x".join(str(x) for x in v.values()))
+def test_the_largest_losses_can_be_launched(entry, args):
+    (status, launches), = record([(entry, args)])
+    assert status == 0 and len(launches) == 1
+    assert all(0 < g * b < 1 << 32 for g, b in zip(*launches[0][1:]))
+
+
+def test_attention_kernels_by_columns_and_alignment():
+    args = dict(tokens=300, k_tokens=300, heads_=2, kv=1, sequences=0)
+    for dim, blocks in ((8, 2), (64, 2), (72, 3), (96, 3), (104, 4), (128, 4)):
+        for odd in (False, True):
+            got = record([(e, dict(args, dim=dim, odd=odd)) for e in ("attention", "attention_grad")])
+            names = [kernel for _, launches in got for kernel, _, _ in launches]
+            al = "false" if odd else "true"
+            assert names == [f"k_attn<{blocks}, {al}>", f"k_attn_dq<{blocks}, {al}>", f"k_attn_dkv<{blocks}, {al}>"]
+
+
+@pytest.mark.parametrize("layout", ["side by side", "in steps", "one after the other"])
+def test_attention_takes_slices_of_one_buffer(layout):
+    """Heads of q, k, v, o and their gradients side by side in one buffer overlap nothing."""
+    args = dict(tokens=40, k_tokens=40, heads_=4, kv=4, dim=64, sequences=0, layout=layout)
+    for status, launches in record([("attention", args), ("attention_grad", args)]):
+        assert status == 0 and launches

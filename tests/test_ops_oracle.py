@@ -90,3 +90,50 @@ def test_gate_wgrad_and_embed_gradients_by_differences():
     grad = O.embed_grad(de, ids, 7, 1.5)
     for i in range(table.size):
         assert abs(_difference(lambda v: (O.embed(v, ids, 1.5) * de).sum(), table, i, 1e-4) - grad.flat[i]) < 1e-9
+
+
+@pytest.mark.parametrize("nq,nk,causal", [(5, 5, True), (4, 6, True), (6, 4, True), (3, 7, False), (2, 0, False)])
+def test_attention_against_loops_and_differences(nq, nk, causal):
+    rng = np.random.default_rng(nq * 10 + nk)
+    q, k, v, do = (rng.normal(size=(n, 3)) for n in (nq, nk, nk, nq))
+    o, lse = O.attention(q, k, v, 0.7, causal)
+    for i in range(nq):
+        seen = [j for j in range(nk) if not causal or j <= i + nk - nq]
+        e = [np.exp(0.7 * float(q[i] @ k[j])) for j in seen]
+        if not seen:
+            assert not o[i].any() and lse[i] == -np.inf
+            continue
+        assert abs(lse[i] - np.log(sum(e))) < 1e-12
+        assert np.allclose(o[i], sum(w * v[j] for w, j in zip(e, seen)) / sum(e), rtol=1e-12)
+    grads = O.attention_grad(do, q, k, v, o, lse, 0.7, causal)
+    at = [q, k, v]
+    for which, g in enumerate(grads):
+        def value(x):
+            return (O.attention(*(x if n == which else t for n, t in enumerate(at)), 0.7, causal)[0] * do).sum()
+        for i in range(g.size):
+            assert abs(_difference(value, at[which], i, 1e-5) - g.flat[i]) < 1e-8
+
+
+def test_losses_against_torch_and_differences():
+    rng = np.random.default_rng(4)
+    z, w = rng.normal(size=(4, 9)), np.array([1.0, 0.0, 0.5, -2.0])
+    ids, teacher = np.array([[1, 1, 4], [0, 1, 2], [-1, 9, 3], [8, 0, 5]]), rng.normal(size=(4, 3))
+    loss, grad = O.distill(z, ids, teacher, 1.5, w)
+    for t in range(4):
+        live = [(i, x) for i, x in zip(ids[t], teacher[t]) if 0 <= i < 9]
+        p = torch.softmax(torch.tensor([x for _, x in live]) / 1.5, 0)
+        logq = torch.log_softmax(torch.from_numpy(z[t]) / 1.5, 0)
+        want = sum(float(a * (torch.log(a) - logq[i])) for a, (i, _) in zip(p, live)) * 2.25 * w[t]
+        assert abs(loss[t] - want) < 1e-12
+    actions, old, adv, ref = np.array([3, 1, 8, 9]), np.full(4, -2.2), np.array([1.0, 1.0, -0.5, 1.0]), np.full(4, -2.0)
+    args = (actions, old, adv, ref, 0.2, 0.3, 0.1, 1.5, w)
+    ploss, logp, pgrad = O.policy(z, *args)
+    assert not ploss[[1, 3]].any() and not pgrad[[1, 3]].any()
+    for t in (0, 2):
+        lp = float(torch.log_softmax(torch.from_numpy(z[t]) / 1.5, 0)[actions[t]])
+        r = np.exp(lp - old[t])
+        want = -min(r * adv[t], min(max(r, 0.8), 1.3) * adv[t]) + 0.1 * (np.exp(ref[t] - lp) - (ref[t] - lp) - 1)
+        assert abs(logp[t] - lp) < 1e-12 and abs(ploss[t] - w[t] * want) < 1e-12
+    for i in range(z.size):
+        assert abs(_difference(lambda x: O.distill(x, ids, teacher, 1.5, w)[0].sum(), z, i, 1e-5) - grad.flat[i]) < 1e-8
+        assert abs(_difference(lambda x: O.policy(x, *args)[0].sum(), z, i, 1e-5) - pgrad.flat[i]) < 1e-8
