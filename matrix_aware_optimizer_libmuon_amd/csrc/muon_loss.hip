@@ -4,10 +4,12 @@
 // Both need, of a token's row x = z / temperature, the softmax's maximum and sum
 // and a few single entries, and their gradient is
 //   dz = a softmax(x)  plus a value at each of those few entries.
-// A block takes a row.  Up to Regs<T>::cols columns the row stays in registers, so
-// the logits are read once and the gradient written once; a longer row is read
-// again for the gradient (from the caches: the rows that the chip has in work at
-// one time, at most 256 MB, fit the last one).  Bound by memory.
+// A block takes a row.  Up to 131072 columns in bf16 and 65536 in fp32 the row stays in
+// registers, so the logits are read once and the gradient written once; a longer row is
+// read again for the gradient (from the caches, which hold the rows in work).  Bound by
+// memory: distillation 16384 x 32000 bf16 405 us (4.9 TB/s), policy loss with 30 % of the
+// rows masked 331 us (5.4); a large copy runs at 4.8.  A single row is bound by one CU's
+// exponentials, a quarter of the rate of other instructions, twice 32000 of them in 8 us.
 //
 // Numbers.  x - max is taken before the factor log2(e) / temperature, so that rows
 // of the type's lowest value stay finite; sums run in fp32, up to 128 terms a
@@ -28,15 +30,28 @@ constexpr float kNegInf = -__builtin_inff();
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }   // 1 ulp
 __device__ __forceinline__ float log2_fast(float v) { return __builtin_amdgcn_logf(v); }
 
+// Over the wave, in every lane: within rows of 16 by data-parallel moves, then across them
+// by exchanges of rows (a sixth of the latency of permutations through LDS).
+template <class F>
+__device__ __forceinline__ float wave_all(float v, F f) {
+  auto moved = [](float x, auto ctrl) {
+    return __uint_as_float(static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(x)), decltype(ctrl)::value, 0xf, 0xf, true)));
+  };
+  v = f(v, moved(v, std::integral_constant<int, 0xB1>{}));    // lanes 1 0 3 2
+  v = f(v, moved(v, std::integral_constant<int, 0x4E>{}));    // lanes 2 3 0 1
+  v = f(v, moved(v, std::integral_constant<int, 0x141>{}));   // 8 lanes mirrored
+  v = f(v, moved(v, std::integral_constant<int, 0x140>{}));   // 16 lanes mirrored
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+  return wave_all(v, [](float x, float y) { return fmaxf(x, y); });
 }
 __device__ __forceinline__ float wave_add(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  return wave_all(v, [](float x, float y) { return x + y; });
 }
 
 // A maximum to subtract: 0 where there is nothing but -inf, so that exp gives 0.
@@ -88,6 +103,11 @@ __device__ __forceinline__ void fill_behind(Vec8<uint16_t>& v, int n) {
     else if (2 * i + 1 >= n) v.r[i] = (v.r[i] & 0xffffu) | 0xff800000u;
   }
 }
+// The row stays as loaded: without this the compiler keeps the unpacked floats of the
+// first pass for the second, in twice the registers.
+__device__ __forceinline__ void keep_raw(Vec8<float>& v) { asm volatile("" : "+v"(v.r[0]), "+v"(v.r[1])); }
+__device__ __forceinline__ void keep_raw(Vec8<uint16_t>& v) { asm volatile("" : "+v"(v.r)); }
+
 template <class T>
 __device__ __forceinline__ void settle_row(Vec8<T>& v, int c, int n) {
   if (n < 8) {
@@ -111,86 +131,139 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int64_t i, int32_t id_
                        : static_cast<int64_t>(gld<int32_t>(static_cast<const int32_t*>(ids) + i));
 }
 
-// A row of VPL vectors a thread in registers; VPL = 0: any length, in passes of kPass
-// vectors.  Thread t has the vectors t, t + RT ...
-constexpr int kPass = 4;
+// N vectors' maximum, and sum of 2^((x - base) k).
+template <class T, int N>
+__device__ __forceinline__ float top_of(const Vec8<T> (&x)[N]) {
+  float m = kNegInf;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, x[j].get(i));
+  return m;
+}
+template <class T, int N>
+__device__ __forceinline__ float sum_of(Vec8<T> (&x)[N], float base, float k) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    keep_raw(x[j]);
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = exp2_fast((x[j].get(i) - base) * k);
+    s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+  }
+  return s;
+}
+// n (8 or more: all) of the vector's columns at out: a 2^((x - base) k)
+template <class T>
+__device__ __forceinline__ void put_scaled(T* out, int n, Vec8<T>& x, float base, float k, float a) {
+  keep_raw(x);
+  float g[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = a * exp2_fast((x.get(i) - base) * k);
+  Vec8<T>::store(out, n, g);
+}
+
+// A row in the registers of RT threads: `step` of them have VPL vectors each, vector
+// t + j step the j-th of thread t.  All but the last lie inside the row (which has
+// (VPL - 1)^2 + VPL vectors at least), so that one scalar address and one offset a lane
+// do for them and only the last goes by its length.
 template <class T, int RT, int VPL>
 struct Row {
-  static constexpr int N = VPL ? VPL : kPass;
   const T* p;
-  int cols, t;
-  Vec8<T> x[N];
+  int cols, t, step;
+  Vec8<T> x[VPL];
 
-  __device__ __forceinline__ void fetch(int base) {
+  __device__ __forceinline__ Row(const T* p_, int cols_, int t_) : p(p_), cols(cols_), t(t_) {
+    step = (((cols + 7) >> 3) + VPL - 1) / VPL;
+  }
+  __device__ __forceinline__ int last() const { return ((VPL - 1) * step + t) * 8; }
+  __device__ __forceinline__ void fetch() {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int c = base + (t + j * RT) * 8;
-      fetch8(x[j], p + c, c, cols - c);
+    for (int j = 0; j < VPL; ++j) fill_behind(x[j], 0);
+    if (t < step) {
+#pragma unroll
+      for (int j = 0; j < VPL - 1; ++j) x[j].load(p + j * step * 8 + static_cast<uint32_t>(t * 8));
+      fetch8(x[VPL - 1], p + last(), last(), cols - last());
     }
   }
-  __device__ __forceinline__ void settle(int base) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int c = base + (t + j * RT) * 8;
-      settle_row(x[j], c, cols - c);
-    }
-  }
-  __device__ __forceinline__ float top() const {
-    float m = kNegInf;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, x[j].get(i));
-    return m;
-  }
-  __device__ __forceinline__ float sum(float base, float k) const {
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      float e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = exp2_fast((x[j].get(i) - base) * k);
-      s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-    }
-    return s;
-  }
-  // the thread's maximum and sum; the first loads have been issued
+  // the thread's maximum and sum
   __device__ __forceinline__ Soft stats(float k) {
-    if constexpr (VPL > 0) {
-      settle(0);
-      const float m = wave_max(top());
-      return {m, sum(base_of(m), k)};
-    } else {
-      Soft a{kNegInf, 0.f};
-      for (int at = 0; at < cols; at += RT * 8 * N) {
-        if (at) fetch(at);
-        settle(at);
-        const float m = fmaxf(a.m, top());
-        a.s = a.s * shrink(a.m, m, k) + sum(base_of(m), k);
-        a.m = m;
-      }
-      return a;
-    }
+    if (t < step) settle_row(x[VPL - 1], last(), cols - last());
+    const float m = wave_max(top_of(x));
+    return {m, sum_of(x, base_of(m), k)};
   }
   // out[c] = a 2^((x[c] - base) k)
   __device__ __forceinline__ void scaled(T* out, float base, float k, float a) {
-    for (int at = 0; at < cols; at += RT * 8 * N) {
-      if constexpr (VPL == 0) {
-        fetch(at);
-        settle(at);
-      }
+    if (t >= step) return;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int c = at + (t + j * RT) * 8;
-        float g[8];
+    for (int j = 0; j < VPL - 1; ++j) put_scaled(out + j * step * 8 + static_cast<uint32_t>(t * 8), 8, x[j], base, k, a);
+    put_scaled(out + last(), cols - last(), x[VPL - 1], base, k, a);
+  }
+  // whether this thread has written column c
+  __device__ __forceinline__ bool wrote(int c) const { return (c >> 3) % step == t; }
+};
+
+// A row of any length, read twice: kPass vectors a thread at a time, then single ones.
+constexpr int kPass = 4;
+template <class T, int RT>
+struct Row<T, RT, 0> {
+  const T* p;
+  int cols, t;
+  Vec8<T> x[kPass];
+
+  __device__ __forceinline__ Row(const T* p_, int cols_, int t_) : p(p_), cols(cols_), t(t_) {}
+  __device__ __forceinline__ void fetch() {}
+  __device__ __forceinline__ void load(int at) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = a * exp2_fast((x[j].get(i) - base) * k);
-        Vec8<T>::store(out + c, cols - c, g);
-      }
-      if constexpr (VPL > 0) break;
+    for (int j = 0; j < kPass; ++j) x[j].load(p + at + j * RT * 8 + static_cast<uint32_t>(t * 8));
+  }
+  __device__ __forceinline__ Soft stats(float k) {
+    Soft a{kNegInf, 0.f};
+    auto add = [&](float top, auto sum) {
+      const float m = fmaxf(a.m, top);
+      a.s = a.s * shrink(a.m, m, k) + sum(base_of(m));
+      a.m = m;
+    };
+    int at = 0;
+    for (; at + kPass * RT * 8 <= cols; at += kPass * RT * 8) {
+      load(at);
+      add(top_of(x), [&](float base) { return sum_of(x, base, k); });
+    }
+#pragma unroll 1
+    for (; at < cols; at += RT * 8) {
+      Vec8<T> v[1];
+      load8(v[0], p + at + t * 8, at + t * 8, cols - at - t * 8);
+      if (cols - at - t * 8 < 8) fill_behind(v[0], cols - at - t * 8);
+      add(top_of(v), [&](float base) { return sum_of(v, base, k); });
+    }
+    return a;
+  }
+  __device__ __forceinline__ void scaled(T* out, float base, float k, float a) {
+    int at = 0;
+    for (; at + kPass * RT * 8 <= cols; at += kPass * RT * 8) {
+      load(at);
+#pragma unroll
+      for (int j = 0; j < kPass; ++j) put_scaled(out + at + j * RT * 8 + static_cast<uint32_t>(t * 8), 8, x[j], base, k, a);
+    }
+#pragma unroll 1
+    for (; at < cols; at += RT * 8) {
+      const int c = at + t * 8;
+      Vec8<T> v;
+      load8(v, p + c, c, cols - c);
+      put_scaled(out + c, cols - c, v, base, k, a);
     }
   }
+  __device__ __forceinline__ bool wrote(int c) const { return (c >> 3) % RT == t; }
 };
+
+// Waves a SIMD, by the registers that the row takes of the 64, 80 or 128 they leave (16384
+// x 32000 in bf16: 6 waves 338 us, 8 with some of the row spilled 359, 4 521).
+template <class T, int VPL>
+constexpr int occupancy() {
+  constexpr int row = (VPL ? VPL : kPass) * static_cast<int>(sizeof(T)) * 2;
+  return row <= 16 ? 8 : row <= 32 ? 6 : 4;
+}
 
 template <class T, int RT>
 __device__ __forceinline__ void zero_row(T* out, int cols, int t) {
@@ -204,7 +277,7 @@ __device__ __forceinline__ void zero_row(T* out, int cols, int t) {
 // softmax minus the sum of p over the entries of the same id, in their order (so
 // threads of one id write the same value).
 template <class T, int RT, int VPL>
-__global__ __launch_bounds__(RT) void k_distill(muon_distill_t op) {
+__global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_distill(muon_distill_t op) {
   constexpr int top_max = MUON_DISTILL_MAX_TOP;
   __shared__ Shared<RT> sh;
   __shared__ __attribute__((aligned(16))) int id[top_max];
@@ -221,8 +294,8 @@ __global__ __launch_bounds__(RT) void k_distill(muon_distill_t op) {
       if (t == 0) gst<float>(op.loss + row, 0.f);
       continue;
     }
-    Row<T, RT, VPL> x{p, static_cast<int>(op.vocab), t};
-    x.fetch(0);
+    Row<T, RT, VPL> x(p, static_cast<int>(op.vocab), t);
+    x.fetch();
     Soft teach{kNegInf, 0.f};
     for (int e = t; e < padded; e += RT) {
       int64_t i = -1;
@@ -307,7 +380,7 @@ __device__ __forceinline__ float exp_less_linear(float d) {
 }
 
 template <class T, int RT, int VPL>
-__global__ __launch_bounds__(RT) void k_policy(muon_policy_t op) {
+__global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_policy(muon_policy_t op) {
   __shared__ Shared<RT> sh;
   const int t = static_cast<int>(threadIdx.x), wave = t >> 6;
   const float k = kLog2e / op.temperature;
@@ -324,8 +397,8 @@ __global__ __launch_bounds__(RT) void k_policy(muon_policy_t op) {
       }
       continue;
     }
-    Row<T, RT, VPL> x{p, static_cast<int>(op.vocab), t};
-    x.fetch(0);
+    Row<T, RT, VPL> x(p, static_cast<int>(op.vocab), t);
+    x.fetch();
     const float xa = value_at(p + act), adv = gld<float>(op.advantages + row), old = gld<float>(op.old_logp + row),
                 ref = op.ref_logp ? gld<float>(op.ref_logp + row) : 0.f;
     const Soft mine = wave_join(x.stats(k), k);
@@ -356,27 +429,45 @@ __global__ __launch_bounds__(RT) void k_policy(muon_policy_t op) {
       const float g = weight * slope / op.temperature;
       x.scaled(out, base, k, -g / q.s);
       // the action's column once more, by the thread that has just written it
-      if (static_cast<int>((act >> 3) % RT) == t) put_value(out + act, g * (1.f - exp2_fast(la) / q.s));
+      if (x.wrote(static_cast<int>(act))) put_value(out + act, g * (1.f - exp2_fast(la) / q.s));
     }
     if (row + gridDim.x < op.tokens) __syncthreads();   // (uniform) before the next row's sums
   }
 }
 
 // ---------------------------------------------------------------- dispatch ----
-// f(threads of a row, vectors of 8 columns a thread): few threads for short rows,
-// then as many vectors as registers hold beside two blocks a CU.
+constexpr int64_t kFewRows = 512;   // two blocks a CU
+
+// f(threads of a row, vectors of 8 columns a thread).  Few rows: as many threads to a
+// row as have work, for its latency.  Many: as few as hold it beside the other rows of a
+// CU, a wave up to 2048 columns, so that several rows are in flight (32768 x 5000 in
+// bf16: 256 threads 175 us, 512 244; 1 x 32000: 1024 threads and 512 the same 8 us, 37 x
+// 1000: 256 threads 4.0 us, a wave 5.4).
 template <class T, class F>
-int by_width(int64_t cols, F&& f) {
+int by_shape(int64_t rows, int64_t cols, F&& f) {
+  auto with = [&](auto rt, auto vpl) { return f(rt, vpl); };
   using std::integral_constant;
-  if (cols <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  if (cols <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  if (cols <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  if (cols <= 16384) return f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
-  if (cols <= 32768) return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
-  if (cols <= 65536) return f(integral_constant<int, 1024>{}, integral_constant<int, 8>{});
-  if constexpr (sizeof(T) == 2)
-    if (cols <= 131072) return f(integral_constant<int, 1024>{}, integral_constant<int, 16>{});
-  return f(integral_constant<int, 1024>{}, integral_constant<int, 0>{});
+#define MUON_ROW(RT, VPL) return with(integral_constant<int, RT>{}, integral_constant<int, VPL>{})
+  if (cols <= 512) MUON_ROW(64, 1);
+  if (rows <= kFewRows) {
+    if (cols <= 2048) MUON_ROW(256, 1);
+    if (cols <= 8192) MUON_ROW(1024, 1);
+    if (cols <= 16384) MUON_ROW(1024, 2);
+    if (cols <= 32768) MUON_ROW(1024, 4);
+    if (cols <= 65536) MUON_ROW(1024, 8);
+  }
+  if (cols <= 2048) MUON_ROW(64, 4);
+  if (cols <= 8192) MUON_ROW(256, 4);
+  if (cols <= 16384) MUON_ROW(512, 4);
+  if (cols <= 32768) MUON_ROW(512, 8);
+  if constexpr (sizeof(T) == 2) {
+    if (cols <= 65536) MUON_ROW(512, 16);
+    if (cols <= 131072) MUON_ROW(1024, 16);
+  } else {
+    if (cols <= 65536) MUON_ROW(1024, 8);
+  }
+  MUON_ROW(1024, 0);
+#undef MUON_ROW
 }
 
 constexpr int64_t kMaxGrid = int64_t(1) << 21;   // threads of a grid stay below 2^32
@@ -388,7 +479,7 @@ unsigned rows_grid(int64_t tokens) { return static_cast<unsigned>(tokens < kMaxG
 int launch_distill(const muon_distill_t& op, void* stream) {
   auto run = [&](auto type) {
     using T = decltype(type);
-    return by_width<T>(op.vocab, [&](auto rt, auto vpl) {
+    return by_shape<T>(op.tokens, op.vocab, [&](auto rt, auto vpl) {
       constexpr int RT = decltype(rt)::value, VPL = decltype(vpl)::value;
       hipLaunchKernelGGL((k_distill<T, RT, VPL>), dim3(rows_grid(op.tokens)), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
       return static_cast<int>(hipGetLastError());
@@ -400,7 +491,7 @@ int launch_distill(const muon_distill_t& op, void* stream) {
 int launch_policy(const muon_policy_t& op, void* stream) {
   auto run = [&](auto type) {
     using T = decltype(type);
-    return by_width<T>(op.vocab, [&](auto rt, auto vpl) {
+    return by_shape<T>(op.tokens, op.vocab, [&](auto rt, auto vpl) {
       constexpr int RT = decltype(rt)::value, VPL = decltype(vpl)::value;
       hipLaunchKernelGGL((k_policy<T, RT, VPL>), dim3(rows_grid(op.tokens)), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
       return static_cast<int>(hipGetLastError());
