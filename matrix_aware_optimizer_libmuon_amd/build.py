@@ -36,7 +36,8 @@ SOURCES = [
     ("muon_embed.hip", []),
     ("muon_wgrad.hip", []),
     ("muon_loss.hip", []),
-    ("muon_attn.hip", []),
+    # attention: maxima without a canonicalising instruction for each operand
+    ("muon_attn.hip", ["-fno-honor-nans", "-mno-amdgpu-ieee"]),
     ("muon_api.cpp", []),
     ("muon_ops.cpp", []),
 ]

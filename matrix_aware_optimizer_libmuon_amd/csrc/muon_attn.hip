@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "muon_act8.h"
+#include "muon_gemm.h"
 #include "muon_ops.h"
 
 namespace muon {
@@ -49,7 +50,6 @@ struct Geo {
   static constexpr int COLS = DB <= 2 ? 64 : 128;         // columns of a row in LDS
   static constexpr int ROWB = COLS * 2, CPR = COLS / 8;   // its bytes and chunks
   static constexpr int TILE = BN * ROWB;
-  static constexpr int LOADS = TILE / 4096;               // 1 KB loads of a wave
 };
 
 template <int COLS>
@@ -106,13 +106,14 @@ __device__ __forceinline__ u32x4 buffer(const void* p, uint32_t bytes) {
 // Tiles of one head's rows of a sequence, into LDS.  ALIGNED: rows begin on 16
 // bytes and 64 of them span less than 2^31 (attn_aligned): loads without registers,
 // in flight until block_barrier().  Else through registers at once.
-template <int DB, bool ALIGNED>
+template <int DB, bool ALIGNED, int WAVES = 4>
 struct Feed {
   using G = Geo<DB>;
+  static constexpr int LOADS = G::TILE / 1024 / WAVES;    // 1 KB loads of a wave
   const uint16_t* p;
   int64_t ld;
   int rows, dim;                   // of the sequence; columns
-  uint32_t voff[G::LOADS];
+  uint32_t voff[LOADS];
   int w, tid;
 
   __device__ __forceinline__ Feed(const muon_heads_t& t, int64_t row0, int nrows, int head, int dim_, int tid_)
@@ -121,8 +122,8 @@ struct Feed {
     if constexpr (ALIGNED) {
       const int lane = tid & 63, rr = lane / G::CPR, pos = lane % G::CPR;
 #pragma unroll
-      for (int q = 0; q < G::LOADS; ++q) {
-        const int c = pos ^ swz<G::COLS>((w * G::LOADS + q) * (64 / G::CPR) + rr);
+      for (int q = 0; q < LOADS; ++q) {
+        const int c = pos ^ swz<G::COLS>((w * LOADS + q) * (64 / G::CPR) + rr);
         voff[q] = c * 8 < dim ? static_cast<uint32_t>(rr * ld * 2 + c * 16) : 0x80000000u;   // past every end
       }
     }
@@ -136,13 +137,13 @@ struct Feed {
       const u32x4 srd = buffer(at, (left - 1) * ldb + dim * 2);
       const uint32_t to = lds_at(dst);
 #pragma unroll
-      for (int q = 0; q < G::LOADS; ++q) {
-        const int b = w * G::LOADS + q;
+      for (int q = 0; q < LOADS; ++q) {
+        const int b = w * LOADS + q;
         dma<16>(srd, voff[q], b * (64 / G::CPR) * ldb, to + b * 1024);
       }
     } else {
 #pragma unroll 1
-      for (int i = tid; i < BN * G::CPR; i += kThreads) {
+      for (int i = tid; i < BN * G::CPR; i += 64 * WAVES) {
         const int r = i / G::CPR, c = (i % G::CPR) ^ swz<G::COLS>(r);
         u32x4 v{0, 0, 0, 0};
         if (r < left && c * 8 < dim) v = gld<u32x4_a2>(at + r * ld + c * 8);
@@ -154,10 +155,18 @@ struct Feed {
 
 // Fragments of a staged tile.  rows(): row rb + (lane & 31), columns 16 ks + 8 h ..;
 // cols(): column 32 db + (lane & 31), the rows of 16-row step s in the order above.
-template <int DB>
+// FRESH: addresses are formed at each read, for a kernel whose registers do not hold
+// those of all steps.
+template <int DB, bool FRESH = false>
 struct Frags {
   using G = Geo<DB>;
   int r0, t0;
+  static __device__ __forceinline__ int flip(int v, int bits) {
+    if constexpr (!FRESH) return v ^ bits;
+    int r;
+    asm volatile("v_xor_b32 %0, %1, %2" : "=v"(r) : "n"(bits), "v"(v));
+    return r;
+  }
   __device__ __forceinline__ explicit Frags(int lane) {
     const int l = lane & 31, h = lane >> 5, j = lane & 15;
     r0 = l * G::ROWB + ((h ^ swz<G::COLS>(l)) << 4);
@@ -165,14 +174,14 @@ struct Frags {
     t0 = row * G::ROWB + ((c ^ swz<G::COLS>(row)) << 4) + (j & 1) * 8;
   }
   __device__ __forceinline__ bf16x8_t rows(const char* tile, int rb, int ks) const {
-    return *reinterpret_cast<const bf16x8_t*>(tile + rb * G::ROWB + (r0 ^ (ks << 5)));
+    return *reinterpret_cast<const bf16x8_t*>(tile + rb * G::ROWB + flip(r0, ks << 5));
   }
   __device__ __forceinline__ bf16x8_t cols(const char* tile, int s, int db) const {
     // 8 rows on, bit 1 of the swizzle is set
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)(tile + s * 16 * G::ROWB + (t0 ^ (db << 6))));
+        (__attribute__((address_space(3))) s16x4*)(tile + s * 16 * G::ROWB + flip(t0, db << 6)));
     const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)(tile + (s * 16 + 8) * G::ROWB + (t0 ^ (db << 6) ^ 32)));
+        (__attribute__((address_space(3))) s16x4*)(tile + (s * 16 + 8) * G::ROWB + flip(t0, (db << 6) ^ 32)));
     return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 };
@@ -191,11 +200,27 @@ __device__ __forceinline__ void own_rows(const muon_heads_t& t, int64_t row0, in
   }
 }
 
-// A lane's 8 values as an operand, rounded to bf16.
+// Fragments that have arrived.  Before a loop that issues loads of its own, or the
+// compiler waits for those too, at each use inside it that may be the first.
+template <int N>
+__device__ __forceinline__ void arrived(bf16x8_t (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    u32x4 v = __builtin_bit_cast(u32x4, f[i]);
+    asm volatile("" : "+v"(v));
+    f[i] = __builtin_bit_cast(bf16x8_t, v);
+  }
+}
+
+// Two values rounded to bf16 by one instruction; a lane's 8 as an operand.
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2));
+}
 __device__ __forceinline__ bf16x8_t pack8(const f32x16_t& v, int from) {
   u32x4 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = pack2(v[from + 2 * i], v[from + 2 * i + 1]);
+  for (int i = 0; i < 4; ++i) r[i] = pack(v[from + 2 * i], v[from + 2 * i + 1]);
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
@@ -212,8 +237,8 @@ __device__ __forceinline__ void store_row(const muon_heads_t& t, int64_t row, in
       u32x4 o;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t x = pack2(acc[db][a + 2 * i] * f, acc[db][a + 2 * i + 1] * f);
-        const uint32_t y = pack2(acc[db][a + 4 + 2 * i] * f, acc[db][a + 4 + 2 * i + 1] * f);
+        const uint32_t x = pack(acc[db][a + 2 * i] * f, acc[db][a + 2 * i + 1] * f);
+        const uint32_t y = pack(acc[db][a + 4 + 2 * i] * f, acc[db][a + 4 + 2 * i + 1] * f);
         const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
         o[i] = r[0];
         o[2 + i] = r[1];
@@ -231,16 +256,16 @@ struct Place {
   bool rest;            // rows behind the last sequence
 };
 
-// Unit `unit` of the tiles of BM queries (KEYS: keys) of all sequences, one after the
+// Unit `unit` of the tiles of OWN queries (KEYS: keys) of all sequences, one after the
 // other; rows behind the last sequence are one more, without keys (queries), if they
 // are to be written.  Starts are brought into range and order first, so that bad ones
 // cannot lead outside the tensors.
-template <bool KEYS>
-__device__ __forceinline__ Place locate(const int32_t* starts, const int32_t* k_starts, int64_t sequences, int tokens, int k_tokens,
+template <bool KEYS, int OWN>
+__device__ __forceinline__ Place place_of(const int32_t* starts, const int32_t* k_starts, int64_t sequences, int tokens, int k_tokens,
                                         bool rest, int unit, int lane) {
   if (!starts) {
     const int n = KEYS ? k_tokens : tokens;
-    return {0, tokens, 0, k_tokens, unit, unit < (n + BM - 1) / BM, false};
+    return {0, tokens, 0, k_tokens, unit, unit < (n + OWN - 1) / OWN, false};
   }
   if (!k_starts) k_starts = starts;
   int before = 0;
@@ -255,7 +280,7 @@ __device__ __forceinline__ Place locate(const int32_t* starts, const int32_t* k_
       nk = min(max(gld<int32_t>(k_starts + next), k0), k_tokens) - k0;
       if (i == sequences && rest) (KEYS ? nk : nq) = KEYS ? k_tokens - k0 : tokens - q0;
     }
-    const int tiles = ((KEYS ? nk : nq) + BM - 1) / BM;
+    const int tiles = ((KEYS ? nk : nq) + OWN - 1) / OWN;
     int upto = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -273,6 +298,14 @@ __device__ __forceinline__ Place locate(const int32_t* starts, const int32_t* k_
   return {0, 0, 0, 0, 0, false, false};
 }
 
+// The same in scalar registers, which the compiler does not see through the loop.
+template <bool KEYS, int OWN, class... Args>
+__device__ __forceinline__ Place locate(Args... args) {
+  const Place p = place_of<KEYS, OWN>(args...);
+  auto one = [](int v) { return static_cast<int>(uniform(static_cast<uint32_t>(v))); };
+  return {one(p.q0), one(p.nq), one(p.k0), one(p.nk), one(p.tile), one(p.found) != 0, one(p.rest) != 0};
+}
+
 // ------------------------------------------------------------- forward pass ----
 // Rescaling is put off while no row's maximum has grown by more than 2^kSlack since the
 // last one: P then reaches 2^kSlack at most, which costs no precision, and the sums are
@@ -286,10 +319,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint3
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
   // neighbouring blocks of an XCD share a head; the longest rows of a causal mask first
   const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
-  const int head = at / units, unit = units - 1 - at % units;
-  const Place pl = locate<false>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, op.zero_rest != 0, unit, lane);
+  const int head = uniform(at / units), unit = units - 1 - (at - head * units);
+  const Place pl = locate<false, BM>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, op.zero_rest != 0, unit, lane);
   if (!pl.found) return;
-  const int kv = head / static_cast<int>(op.heads / op.kv_heads), dim = op.dim;
+  const int kv = uniform(static_cast<uint32_t>(head) / static_cast<uint32_t>(op.heads / op.kv_heads)), dim = op.dim;
   const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31);   // the wave's first query, the lane's
   const int offset = pl.nk - pl.nq;                                      // key i + offset is query i's last (causal)
   const int block_last = min(pl.tile * BM + BM, pl.nq) - 1 + offset;
@@ -307,6 +340,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint3
 
   fk.load(0, smem);
   fv.load(0, smem + G::TILE);
+  arrived(qf);
   block_barrier();
   const int tiles = (keys + BN - 1) / BN;
   auto step = [&](int j, const char* now, char* next) __attribute__((always_inline)) {
@@ -380,11 +414,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t o
   __shared__ __attribute__((aligned(256))) char smem[4 * G::TILE];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
   const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
-  const int head = at / units, unit = units - 1 - at % units;
-  const Place pl = locate<false>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, (op.zero_rest & MUON_ATTN_ZERO_DQ) != 0,
+  const int head = uniform(at / units), unit = units - 1 - (at - head * units);
+  const Place pl = locate<false, BM>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, (op.zero_rest & MUON_ATTN_ZERO_DQ) != 0,
                                    unit, lane);
   if (!pl.found) return;
-  const int kv = head / static_cast<int>(op.heads / op.kv_heads), dim = op.dim;
+  const int kv = uniform(static_cast<uint32_t>(head) / static_cast<uint32_t>(op.heads / op.kv_heads)), dim = op.dim;
   const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31), offset = pl.nk - pl.nq;
   const int block_last = min(pl.tile * BM + BM, pl.nq) - 1 + offset;
   const int keys = op.causal ? max(0, min(pl.nk, block_last + 1)) : pl.nk;
@@ -419,6 +453,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t o
   for (int db = 0; db < DB; ++db) dq[db] = f32x16_t{};
   const float c = op.scale * kLog2e;
 
+  arrived(qf);
+  arrived(gf);
   block_barrier();
   const int tiles = (keys + BN - 1) / BN;
   auto step = [&](int j, const char* now, char* next) __attribute__((always_inline)) {
@@ -461,38 +497,68 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t o
 }
 
 // ------------------------------------------------------- backward: dK and dV ----
-// A wave owns 32 keys, one per lane and half, and walks the queries of every head that
-// shares them: S = Q K^T and dP = dO V^T leave a lane with 16 of 32 queries of its key,
-// in whose order dV^T = dO^T P and dK^T = Q^T dS then take them.  lse and rowsum(dO O) come
-// with the tile.  A query past the sequence's end has zeros everywhere and adds nothing.
+// A wave owns KB blocks of 32 keys, one per lane and half, and walks the queries of every
+// head that shares them, 32 at a time: S = Q K^T and dP = dO V^T leave a lane with 16 of 32
+// queries of its keys, in whose order dV^T = dO^T P and dK^T = Q^T dS then take them.  lse
+// and rowsum(dO O) come with the tile.  A query past the sequence's end has zeros
+// everywhere and adds nothing.
+//
+// The four products of a step are four phases of KS fragments of Q or dO, in a fixed
+// order: a fragment is read AHEAD of its use, the exponentials of P are spread over the
+// instructions of dP, those of dS over the ones of dV.  Sums, K and V of 128 columns are
+// more than a wave's 256 registers hold beside that: V then waits in LDS, 8 waves to a
+// block, so that two of them still share a SIMD.
+template <int DB>
+constexpr int kKeyWaves = DB == 4 ? 8 : 4;
+
 template <int DB, bool ALIGNED>
-__global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(muon_attention_grad_t op, uint32_t units, const float* stats) {
+__global__ __launch_bounds__(64 * kKeyWaves<DB>, 2) void k_attn_dkv(muon_attention_grad_t op, uint32_t units, const float* stats) {
   using G = Geo<DB>;
+  constexpr int KB = 1, KS = G::KS, AHEAD = 2, WAVES = kKeyWaves<DB>, OWN = 32 * WAVES;
   constexpr int STAGE = 2 * G::TILE + 2 * BN * 4;       // Q, dO, lse, delta
-  __shared__ __attribute__((aligned(256))) char smem[2 * STAGE];
+  constexpr bool V_LDS = DB == 4;                       // the registers hold K alone
+  __shared__ __attribute__((aligned(256))) char smem[2 * STAGE + (V_LDS ? OWN * G::ROWB : 0)];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
   const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
-  const int kv = at / units, unit = at % units;
-  const Place pl = locate<true>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens,
-                                  (op.zero_rest & (MUON_ATTN_ZERO_DK | MUON_ATTN_ZERO_DV)) != 0, unit, lane);
+  const int kv = uniform(at / units), unit = at - kv * units;
+  const Place pl = locate<true, OWN>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens,
+                                     (op.zero_rest & (MUON_ATTN_ZERO_DK | MUON_ATTN_ZERO_DV)) != 0, unit, lane);
   if (!pl.found) return;
-  const int share = op.heads / op.kv_heads, dim = op.dim;
-  const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31), offset = pl.nk - pl.nq;
-  // the first query that sees a key of the block, and of the wave
-  const int from = op.causal ? max(0, pl.tile * BM - offset) : 0;
+  const int share = uniform(static_cast<uint32_t>(op.heads) / static_cast<uint32_t>(op.kv_heads)), dim = op.dim;
+  const int first = pl.tile * OWN + 32 * KB * w, mine = first + (lane & 31), offset = pl.nk - pl.nq;
+  // the first query that sees a key of the block
+  const int from = op.causal ? max(0, pl.tile * OWN - offset) : 0;
   const int j0 = from / BN, tiles = (pl.nq + BN - 1) / BN;
 
-  bf16x8_t kf[G::KS], vf[G::KS];
-  own_rows<DB>(op.k, pl.k0, mine, pl.nk, kv, dim, h, kf);
-  own_rows<DB>(op.v, pl.k0, mine, pl.nk, kv, dim, h, vf);
-  const Frags<DB> fr(lane);
-  f32x16_t dk[DB], dv[DB];
+  bf16x8_t kf[KB][KS], vf[V_LDS ? 1 : KB][KS];
+  char* const own_v = smem + 2 * STAGE + w * (32 * KB) * G::ROWB;       // the wave's own rows of V, for itself
 #pragma unroll
-  for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16_t{};
+  for (int kb = 0; kb < KB; ++kb) {
+    own_rows<DB>(op.k, pl.k0, mine + 32 * kb, pl.nk, kv, dim, h, kf[kb]);
+    bf16x8_t (&v)[KS] = vf[V_LDS ? 0 : kb];
+    own_rows<DB>(op.v, pl.k0, mine + 32 * kb, pl.nk, kv, dim, h, v);
+    if constexpr (V_LDS) {
+      const int row = 32 * kb + (lane & 31);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        *reinterpret_cast<bf16x8_t*>(own_v + row * G::ROWB + (((2 * ks + h) ^ swz<G::COLS>(row)) << 4)) = v[ks];
+    }
+  }
+  const Frags<DB, (DB > 2)> fr(lane);
+  f32x16_t dk[KB][DB], dv[KB][DB];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int db = 0; db < DB; ++db) dk[kb][db] = dv[kb][db] = f32x16_t{};
   const float c = op.scale * kLog2e;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    arrived(kf[kb]);
+    if constexpr (!V_LDS) arrived(vf[kb]);
+  }
 
   for (int head = kv * share; head < (kv + 1) * share; ++head) {
-    const Feed<DB, ALIGNED> fq(op.q, pl.q0, pl.nq, head, dim, tid), fg(op.dout, pl.q0, pl.nq, head, dim, tid);
+    const Feed<DB, ALIGNED, WAVES> fq(op.q, pl.q0, pl.nq, head, dim, tid), fg(op.dout, pl.q0, pl.nq, head, dim, tid);
     const float* rows = stats + head * op.tokens + pl.q0 + (w == 1 ? op.heads * op.tokens : 0);   // wave 0: lse, 1: delta
     auto load = [&](int j, char* to) __attribute__((always_inline)) {
       fq.load(j * BN, to);
@@ -508,35 +574,62 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(muon_attention_grad_t 
         const int q0 = j * BN + 32 * qb;
         // none of the queries sees a key of the wave, or there are none
         if ((op.causal && q0 + 31 + offset < first) || q0 >= pl.nq || first >= pl.nk) continue;
-        f32x16_t s{}, dp{};
+        f32x16_t s[KB] = {}, dp[KB] = {};
+        bf16x8_t f[4 * KS], vl[V_LDS ? KB : 1][KS], pf[KB][2], xf[KB][2];
+        f32x4_t l[4], d[4];
+        auto fetch = [&](auto i) __attribute__((always_inline)) {
+          constexpr int phase = decltype(i)::value / KS, n = decltype(i)::value % KS;
+          if constexpr (phase == 1 && V_LDS)
+            static_for<KB>([&](auto kb) __attribute__((always_inline)) { vl[decltype(kb)::value][n] = fr.rows(own_v, 32 * decltype(kb)::value, n); });
+          if constexpr (phase < 2) f[decltype(i)::value] = fr.rows(now + phase * G::TILE, 32 * qb, n);
+          else f[decltype(i)::value] = fr.cols(now + (3 - phase) * G::TILE, 2 * qb + n / DB, n % DB);
+        };
+        // four rows' lse or delta, before their first use
+        auto fetch_rows = [&](f32x4_t (&to)[4], int which, int g) __attribute__((always_inline)) {
+          to[g] = *reinterpret_cast<const f32x4_t*>(now + 2 * G::TILE + which * BN * 4 + (32 * qb + 8 * g + 4 * h) * 4);
+        };
+        // the j-th value of P (then of dS): four queries of each key block in turn
+        auto element = [&](auto second, auto jc) __attribute__((always_inline)) {
+          constexpr int jj = decltype(jc)::value, g = jj / (4 * KB), kb = jj / 4 % KB, e = jj % 4, i = 4 * g + e;
+          if constexpr (!decltype(second)::value) s[kb][i] = exp2_fast(s[kb][i] * c - l[g][e]);
+          else dp[kb][i] = s[kb][i] * (dp[kb][i] - d[g][e]);
+          if constexpr (e == 3 && (g & 1)) (decltype(second)::value ? xf : pf)[kb][g / 2] = pack8(decltype(second)::value ? dp[kb] : s[kb], 8 * (g / 2));
+          if constexpr (e == 3 && kb == KB - 1 && g < 3) fetch_rows(decltype(second)::value ? d : l, decltype(second)::value, g + 1);
+        };
+        auto phase = [&](auto ph) __attribute__((always_inline)) {
+          constexpr int P = decltype(ph)::value;
+          static_for<KS>([&](auto nc) __attribute__((always_inline)) {
+            constexpr int n = decltype(nc)::value, at_f = P * KS + n;
+            if constexpr (at_f + AHEAD < 4 * KS) fetch(std::integral_constant<int, at_f + AHEAD>{});
+            if constexpr (n == KS - 2 && P < 2) fetch_rows(P ? d : l, P, 0);
+            static_for<KB>([&](auto kc) __attribute__((always_inline)) {
+              constexpr int kb = decltype(kc)::value, slot = n * KB + kb;
+              if constexpr (P == 0) s[kb] = mfma(f[at_f], kf[kb][n], s[kb]);
+              if constexpr (P == 1) dp[kb] = mfma(f[at_f], V_LDS ? vl[V_LDS ? kb : 0][n] : vf[V_LDS ? 0 : kb][n], dp[kb]);
+              if constexpr (P == 2) dv[kb][n % DB] = mfma(f[at_f], pf[kb][n / DB], dv[kb][n % DB]);
+              if constexpr (P == 3) dk[kb][n % DB] = mfma(f[at_f], xf[kb][n / DB], dk[kb][n % DB]);
+              if constexpr (P == 1 || P == 2) {
+                constexpr int j0_ = 16 * slot / KS, j1_ = 16 * (slot + 1) / KS;
+                static_for<j1_ - j0_>([&](auto u) __attribute__((always_inline)) {
+                  element(std::integral_constant<bool, P == 2>{}, std::integral_constant<int, j0_ + decltype(u)::value>{});
+                });
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            });
+          });
+        };
+        static_for<AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(i); });
+        phase(std::integral_constant<int, 0>{});
+        if (op.causal && q0 + offset < first + 32 * KB - 1) {
 #pragma unroll
-        for (int ks = 0; ks < G::KS; ++ks) {
-          s = mfma(fr.rows(now, 32 * qb, ks), kf[ks], s);
-          dp = mfma(fr.rows(now + G::TILE, 32 * qb, ks), vf[ks], dp);
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (mine + 32 * kb > q0 + 8 * (i / 4) + 4 * h + i % 4 + offset) s[kb][i] = -kInf;
         }
-        const bool partial = op.causal && q0 + offset < first + 31;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const char* at_q = now + 2 * G::TILE + (32 * qb + 8 * g + 4 * h) * 4;
-          const f32x4_t l = *reinterpret_cast<const f32x4_t*>(at_q), d = *reinterpret_cast<const f32x4_t*>(at_q + BN * 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = 4 * g + e;
-            float p = exp2_fast(s[i] * c - l[e]), x = p * (dp[i] - d[e]);
-            if (partial && mine > q0 + 8 * g + 4 * h + e + offset) p = x = 0.f;
-            s[i] = p;
-            dp[i] = x;
-          }
-        }
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const bf16x8_t pf = pack8(s, 8 * st), xf = pack8(dp, 8 * st);
-#pragma unroll
-          for (int db = 0; db < DB; ++db) {
-            dv[db] = mfma(fr.cols(now + G::TILE, 2 * qb + st, db), pf, dv[db]);
-            dk[db] = mfma(fr.cols(now, 2 * qb + st, db), xf, dk[db]);
-          }
-        }
+        phase(std::integral_constant<int, 1>{});
+        phase(std::integral_constant<int, 2>{});
+        phase(std::integral_constant<int, 3>{});
       }
       block_barrier();
     };
@@ -547,14 +640,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(muon_attention_grad_t 
       if (j + 1 < tiles) step(j + 1, smem + STAGE, smem);
     }
   }
-  const bool live = mine < pl.nk;
-  store_row<DB>(op.dk, pl.k0 + mine, kv, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_DK)), dk, op.scale);
-  store_row<DB>(op.dv, pl.k0 + mine, kv, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_DV)), dv, 1.f);
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    const int key = mine + 32 * kb;
+    const bool live = key < pl.nk;
+    store_row<DB>(op.dk, pl.k0 + key, kv, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_DK)), dk[kb], op.scale);
+    store_row<DB>(op.dv, pl.k0 + key, kv, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_DV)), dv[kb], 1.f);
+  }
 }
 
 // ---------------------------------------------------------------- dispatch ----
-uint32_t units_of(int64_t tokens, int64_t sequences, bool ragged) {
-  return static_cast<uint32_t>((tokens + BM - 1) / BM + (ragged ? sequences + 1 : 0));
+uint32_t units_of(int64_t tokens, int64_t sequences, bool ragged, int own = BM) {
+  return static_cast<uint32_t>((tokens + own - 1) / own + (ragged ? sequences + 1 : 0));
 }
 
 bool aligned16(const muon_heads_t& t) {
@@ -591,9 +688,9 @@ int launch_attention_dq(const muon_attention_grad_t& op, float* stats, void* str
 }
 
 int launch_attention_dkv(const muon_attention_grad_t& op, const float* stats, void* stream) {
-  const uint32_t units = units_of(op.k_tokens, op.sequences, op.starts != nullptr);
   return by_shape(op.dim, aligned16(op.q) && aligned16(op.dout), [&](auto db, auto al) {
-    hipLaunchKernelGGL((k_attn_dkv<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.kv_heads)), dim3(kThreads), 0,
+    const uint32_t units = units_of(op.k_tokens, op.sequences, op.starts != nullptr, 32 * kKeyWaves<decltype(db)::value>);
+    hipLaunchKernelGGL((k_attn_dkv<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.kv_heads)), dim3(64 * kKeyWaves<decltype(db)::value>), 0,
                        static_cast<hipStream_t>(stream), op, units, stats);
     return static_cast<int>(hipGetLastError());
   });
