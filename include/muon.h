@@ -597,7 +597,10 @@ typedef struct {
  * dim is a multiple of 8 up to 128; tokens, k_tokens 0 .. 2^30; with t the larger
  * of them (t / 128 + sequences + 2) heads <= 2^23.  Products of bf16 summed in fp32,
  * softmax in fp32; the probabilities are rounded to bf16 for the second product,
- * outputs once.  A value that is not finite may reach every row of its sequence and
+ * outputs once.  Few, long rows are cut into parts that a second launch joins.
+ *   workspace muon_attention_workspace_bytes(op) bytes, 256-byte aligned (may be 0, and
+ *             NULL then); depends on the sizes
+ * A value that is not finite may reach every row of its sequence and
  * head, masked or not, but no other sequence. */
 #define MUON_ATTN_MAX_DIM 128
 #define MUON_ATTN_ZERO_O 1
@@ -615,7 +618,9 @@ typedef struct {
   int32_t        zero_rest;
   int32_t        reserved;   /* must be 0 */
 } muon_attention_t;
-int muon_attention(const muon_attention_t* op, hipStream_t stream);
+size_t muon_attention_workspace_bytes(const muon_attention_t* op);
+int muon_attention(const muon_attention_t* op, void* workspace, size_t workspace_bytes,
+                   hipStream_t stream);
 
 /* Its backward pass; P is recomputed from lse:
  *   P = exp(S - lse),  dS = P (dout v^T - rowsum(dout o)),
@@ -624,7 +629,7 @@ int muon_attention(const muon_attention_t* op, hipStream_t stream);
  * the products.  No atomics: the same bits every time.
  *   o, lse     as the forward pass left them
  *   zero_rest  MUON_ATTN_ZERO_DQ, _DK, _DV: as above
- *   workspace  muon_attention_grad_workspace_bytes(tokens, heads), 256-byte aligned */
+ *   workspace  muon_attention_grad_workspace_bytes(op) bytes, 256-byte aligned */
 #define MUON_ATTN_ZERO_DQ 1
 #define MUON_ATTN_ZERO_DK 2
 #define MUON_ATTN_ZERO_DV 4
@@ -642,7 +647,7 @@ typedef struct {
   int32_t        zero_rest;
   int32_t        reserved;   /* must be 0 */
 } muon_attention_grad_t;
-size_t muon_attention_grad_workspace_bytes(int64_t tokens, int64_t heads);
+size_t muon_attention_grad_workspace_bytes(const muon_attention_grad_t* op);
 int muon_attention_grad(const muon_attention_grad_t* op, void* workspace, size_t workspace_bytes,
                         hipStream_t stream);
 

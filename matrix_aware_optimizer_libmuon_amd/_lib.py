@@ -47,7 +47,7 @@ EXPORTED = ("muon_workspace_bytes", "muon_step", "muon_step_ex", "muon_plan_crea
             "muon_swiglu_act8", "muon_swiglu_act8_grad",
             "muon_act8_wgrad_workspace_bytes", "muon_act8_wgrad",
             "muon_embed", "muon_embed_grad_workspace_bytes", "muon_embed_grad",
-            "muon_attention", "muon_attention_grad_workspace_bytes", "muon_attention_grad",
+            "muon_attention", "muon_attention_workspace_bytes", "muon_attention_grad_workspace_bytes", "muon_attention_grad",
             "muon_distill", "muon_policy")
 
 
@@ -259,8 +259,9 @@ def load() -> ctypes.CDLL:
             ("muon_embed", ctypes.c_int, [P(MuonEmbed), ptr]),
             ("muon_embed_grad_workspace_bytes", size_t, [i64, i64, i64]),
             ("muon_embed_grad", ctypes.c_int, [P(MuonEmbedGrad), ptr, size_t, ptr]),
-            ("muon_attention", ctypes.c_int, [P(MuonAttention), ptr]),
-            ("muon_attention_grad_workspace_bytes", size_t, [i64, i64]),
+            ("muon_attention_workspace_bytes", size_t, [P(MuonAttention)]),
+            ("muon_attention", ctypes.c_int, [P(MuonAttention), ptr, size_t, ptr]),
+            ("muon_attention_grad_workspace_bytes", size_t, [P(MuonAttentionGrad)]),
             ("muon_attention_grad", ctypes.c_int, [P(MuonAttentionGrad), ptr, size_t, ptr]),
             ("muon_distill", ctypes.c_int, [P(MuonDistill), ptr]),
             ("muon_policy", ctypes.c_int, [P(MuonPolicy), ptr])):

@@ -41,6 +41,7 @@ struct Entries {
   decltype(&muon_embed) embed = nullptr;
   decltype(&muon_embed_grad_workspace_bytes) embed_grad_ws = nullptr;
   decltype(&muon_embed_grad) embed_grad = nullptr;
+  decltype(&muon_attention_workspace_bytes) attention_ws = nullptr;
   decltype(&muon_attention) attention = nullptr;
   decltype(&muon_attention_grad_workspace_bytes) attention_grad_ws = nullptr;
   decltype(&muon_attention_grad) attention_grad = nullptr;
@@ -62,6 +63,7 @@ void bind_ops(const std::map<std::string, uintptr_t>& at) {
   get("muon_embed", g_entry.embed);
   get("muon_embed_grad_workspace_bytes", g_entry.embed_grad_ws);
   get("muon_embed_grad", g_entry.embed_grad);
+  get("muon_attention_workspace_bytes", g_entry.attention_ws);
   get("muon_attention", g_entry.attention);
   get("muon_attention_grad_workspace_bytes", g_entry.attention_grad_ws);
   get("muon_attention_grad", g_entry.attention_grad);
@@ -437,7 +439,9 @@ py::tuple attention(const at::Tensor& q, const at::Tensor& k, const at::Tensor& 
   op.lse = lse.data_ptr<float>();
   op.ld_lse = op.tokens;
   op.zero_rest = MUON_ATTN_ZERO_LSE | (out ? 0 : MUON_ATTN_ZERO_O);
-  const int st = g_entry.attention(&op, c.stream());
+  const size_t bytes = g_entry.attention_ws(&op);
+  const at::Tensor ws = c.workspace(bytes);
+  const int st = g_entry.attention(&op, bytes ? ws.data_ptr() : nullptr, bytes, c.stream());
   return py::make_tuple(st, o, lse);
 }
 
@@ -463,7 +467,7 @@ py::tuple attention_grad(const at::Tensor& dout, const at::Tensor& q, const at::
   op.dk = heads_of(c, gk, "dk", op.k_tokens, op.kv_heads, op.dim);
   op.dv = heads_of(c, gv, "dv", op.k_tokens, op.kv_heads, op.dim);
   op.zero_rest = (dq ? 0 : MUON_ATTN_ZERO_DQ) | (dk ? 0 : MUON_ATTN_ZERO_DK) | (dv ? 0 : MUON_ATTN_ZERO_DV);
-  const size_t bytes = g_entry.attention_grad_ws(op.tokens, op.heads);
+  const size_t bytes = g_entry.attention_grad_ws(&op);
   const at::Tensor ws = c.workspace(bytes);
   const int st = g_entry.attention_grad(&op, bytes ? ws.data_ptr() : nullptr, bytes, c.stream());
   return py::make_tuple(st, gq, gk, gv);

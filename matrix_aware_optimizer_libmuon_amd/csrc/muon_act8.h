@@ -8,6 +8,8 @@
 // it, 8 up to the row's end, and shifted down in registers, so that it costs no
 // further trip to memory; it is stored in pieces of 4, 2 and 1.
 #pragma once
+#include <type_traits>
+
 #include "muon_device.h"
 #include "muon.h"
 
@@ -153,6 +155,25 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   return x > y ? x : y;
 }
 
+// Over the wave, in every lane: within rows of 16 by data-parallel moves, then across them
+// by exchanges of rows (a sixth of the latency of permutations through LDS).
+template <class T, class F>
+__device__ __forceinline__ T wave_all(T v, F f) {
+  static_assert(sizeof(T) == 4);
+  auto bits = [](T x) { return __builtin_bit_cast(uint32_t, x); };
+  auto value = [](uint32_t x) { return __builtin_bit_cast(T, x); };
+  auto moved = [&](T x, auto ctrl) {
+    return value(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(bits(x)), decltype(ctrl)::value, 0xf, 0xf, true)));
+  };
+  v = f(v, moved(v, std::integral_constant<int, 0xB1>{}));    // lanes 1 0 3 2
+  v = f(v, moved(v, std::integral_constant<int, 0x4E>{}));    // lanes 2 3 0 1
+  v = f(v, moved(v, std::integral_constant<int, 0x141>{}));   // 8 lanes mirrored
+  v = f(v, moved(v, std::integral_constant<int, 0x140>{}));   // 16 lanes mirrored
+  const auto a = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+  v = f(value(a[0]), value(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+  return f(value(b[0]), value(b[1]));
+}
 // ---------------------------------------------------------------------------
 // 8-bit groups.  The scale's biased exponent is taken from the bits of the
 // largest finite magnitude: 448 = 1.75 * 2^8, so e = exponent - 8, and one more

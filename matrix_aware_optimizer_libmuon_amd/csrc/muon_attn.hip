@@ -42,6 +42,7 @@ constexpr float kInf = __builtin_inff();
 constexpr int BN = 64;             // rows of a staged tile
 constexpr int BM = 128;            // rows that a block owns, 32 a wave
 constexpr int kThreads = 256;
+constexpr int64_t kMaxParts = 16;  // of a block's steps
 
 // DB blocks of 32 columns are computed: dim up to 64, 96 or 128.
 template <int DB>
@@ -62,6 +63,19 @@ __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
 }
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The kernel's first argument, read where it is used: scalar registers do not hold all of
+// it over the loop.
+template <class Op>
+__device__ __forceinline__ const __attribute__((address_space(4))) Op* late() {
+  const uint64_t at = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  uint32_t lo = static_cast<uint32_t>(at), hi = static_cast<uint32_t>(at >> 32);
+  asm volatile("" : "+v"(lo), "+v"(hi));
+  return (const __attribute__((address_space(4))) Op*)(static_cast<uint64_t>(uniform(hi)) << 32 | uniform(lo));
+}
+__device__ __forceinline__ muon_heads_t copy(const __attribute__((address_space(4))) muon_heads_t& t) {
+  return {t.data, t.ld_token, t.ld_head};
+}
 
 // Both halves' values in every lane.
 __device__ __forceinline__ u32x2 halves(float v) {
@@ -248,7 +262,46 @@ __device__ __forceinline__ void store_row(const muon_heads_t& t, int64_t row, in
     }
 }
 
+// The same in fp32, to `to` (columns side by side).
+template <int DB>
+__device__ __forceinline__ void store_part(float* to, int dim, int h, bool live, const f32x16_t (&acc)[DB], float f) {
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = 32 * db + 8 * g + 4 * h;
+      if (live && d < dim)
+        gst<f32x4_t>(to + d, f32x4_t{acc[db][4 * g] * f, acc[db][4 * g + 1] * f, acc[db][4 * g + 2] * f, acc[db][4 * g + 3] * f});
+    }
+}
+
 // ------------------------------------------------------------ a block's rows ----
+// Neighbouring blocks of an XCD share a head where the heads can be dealt to the XCDs
+// evenly, and so its keys and values in the L2; else every head's tiles go to all of them,
+// the heaviest first.
+struct Deal {
+  int head, unit;
+};
+__device__ __forceinline__ Deal deal(uint32_t units) {
+  const uint32_t heads = uniform(gridDim.x / units), b = blockIdx.x;
+  if (heads % 8 == 0) {
+    const uint32_t at = static_cast<uint32_t>(xcd_remap(b, gridDim.x)), head = uniform(at / units);
+    return {static_cast<int>(head), static_cast<int>(at - head * units)};
+  }
+  const uint32_t unit = uniform(b / heads);
+  return {static_cast<int>(b - unit * heads), static_cast<int>(unit)};
+}
+
+// Part blockIdx.y of gridDim.y of n steps.
+struct Range {
+  int from, to;
+};
+__device__ __forceinline__ Range part_of(int n) {
+  const uint32_t parts = gridDim.y, each = uniform(static_cast<uint32_t>(n) / parts), more = n - each * parts;
+  auto cut = [&](uint32_t i) { return static_cast<int>(uniform(i * each + min(i, more))); };
+  return {cut(blockIdx.y), cut(blockIdx.y + 1)};
+}
+
 struct Place {
   int q0, nq, k0, nk;   // the sequence's first query and queries, first key and keys
   int tile;             // the block's tile of them
@@ -256,19 +309,23 @@ struct Place {
   bool rest;            // rows behind the last sequence
 };
 
-// Unit `unit` of the tiles of OWN queries (KEYS: keys) of all sequences, one after the
-// other; rows behind the last sequence are one more, without keys (queries), if they
-// are to be written.  Starts are brought into range and order first, so that bad ones
-// cannot lead outside the tensors.
+// Unit `unit` of the tiles of OWN queries (KEYS: keys) of all sequences; rows behind the
+// last sequence are one more, without keys (queries), if they are to be written.  Starts
+// are brought into range and order first, so that bad ones cannot lead outside the
+// tensors.  Tiles with the most work under a causal mask, the last queries and the first
+// keys, come first, over all sequences where there are fewer than 64 (4 x 4096 tokens, 8
+// heads: dK and dV 1330 us with each sequence's in turn, BALANCED with this), else sequence
+// by sequence.
 template <bool KEYS, int OWN>
 __device__ __forceinline__ Place place_of(const int32_t* starts, const int32_t* k_starts, int64_t sequences, int tokens, int k_tokens,
-                                        bool rest, int unit, int lane) {
+                                          bool rest, bool balance, int unit, int lane) {
+  // the tile with `work` tiles of its sequence at or behind it (KEYS: before it)
+  auto tile_of = [](int tiles, int work) { return KEYS ? tiles - work : work - 1; };
   if (!starts) {
-    const int n = KEYS ? k_tokens : tokens;
-    return {0, tokens, 0, k_tokens, unit, unit < (n + OWN - 1) / OWN, false};
+    const int tiles = ((KEYS ? k_tokens : tokens) + OWN - 1) / OWN;
+    return {0, tokens, 0, k_tokens, tile_of(tiles, tiles - unit), unit < tiles, false};
   }
   if (!k_starts) k_starts = starts;
-  int before = 0;
   for (int64_t base = 0; base <= sequences; base += 64) {
     const int64_t i = base + lane;
     int q0 = 0, nq = 0, k0 = 0, nk = 0;
@@ -281,19 +338,38 @@ __device__ __forceinline__ Place place_of(const int32_t* starts, const int32_t* 
       if (i == sequences && rest) (KEYS ? nk : nq) = KEYS ? k_tokens - k0 : tokens - q0;
     }
     const int tiles = ((KEYS ? nk : nq) + OWN - 1) / OWN;
-    int upto = tiles;
+    int f, work;
+    if (balance && sequences < 64) {
+      // the largest `work` of which fewer than unit + 1 tiles have more
+      const auto add = [](int a, int b) { return a + b; };
+      auto above = [&](int v) { return wave_all(max(tiles - v, 0), add); };
+      int lo = 0, hi = wave_all(tiles, [](int a, int b) { return max(a, b); });     // above(hi) == 0 <= unit
+      if (above(0) <= unit) break;
+      while (lo + 1 < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        (above(mid) <= unit ? hi : lo) = mid;
+      }
+      work = hi;
+      uint64_t with = __ballot(tiles >= work);
+      for (int skip = unit - above(work); skip > 0; --skip) with &= with - 1;
+      f = __builtin_ctzll(with);
+    } else {
+      int upto = tiles;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(upto, o, 64);
-      if (lane >= o) upto += v;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(upto, o, 64);
+        if (lane >= o) upto += v;
+      }
+      const uint64_t past = __ballot(upto > unit);
+      if (!past) {
+        unit -= __builtin_amdgcn_readlane(upto, 63);
+        continue;
+      }
+      f = __builtin_ctzll(past);
+      work = __builtin_amdgcn_readlane(upto, f) - unit;
     }
-    const uint64_t past = __ballot(before + upto > unit);
-    if (past) {
-      const int f = __builtin_ctzll(past);
-      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, f); };
-      return {of(q0), of(nq), of(k0), of(nk), unit - before - of(upto - tiles), true, base + f == sequences};
-    }
-    before += __builtin_amdgcn_readlane(upto, 63);
+    auto of = [&](int v) { return __builtin_amdgcn_readlane(v, f); };
+    return {of(q0), of(nq), of(k0), of(nk), tile_of(of(tiles), work), true, base + f == sequences};
   }
   return {0, 0, 0, 0, 0, false, false};
 }
@@ -313,14 +389,12 @@ __device__ __forceinline__ Place locate(Args... args) {
 constexpr float kSlack = 8.f;
 
 template <int DB, bool ALIGNED>
-__global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint32_t units) {
+__global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint32_t units, float* part_o, float* part_lse) {
   using G = Geo<DB>;
   __shared__ __attribute__((aligned(256))) char smem[4 * G::TILE];      // K, V; K, V of the next tile
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
-  // neighbouring blocks of an XCD share a head; the longest rows of a causal mask first
-  const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
-  const int head = uniform(at / units), unit = units - 1 - (at - head * units);
-  const Place pl = locate<false, BM>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, op.zero_rest != 0, unit, lane);
+  const auto [head, unit] = deal(units);
+  const Place pl = locate<false, BM>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, op.zero_rest != 0, op.causal != 0, unit, lane);
   if (!pl.found) return;
   const int kv = uniform(static_cast<uint32_t>(head) / static_cast<uint32_t>(op.heads / op.kv_heads)), dim = op.dim;
   const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31);   // the wave's first query, the lane's
@@ -338,11 +412,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint3
   float top = -kInf, sum = 0.f;                // top: the maximum that P is taken against; sum: of this half's keys
   const float c = op.scale * kLog2e;
 
-  fk.load(0, smem);
-  fv.load(0, smem + G::TILE);
+  const auto [j0, j1] = part_of((keys + BN - 1) / BN);
+  fk.load(j0 * BN, smem);
+  fv.load(j0 * BN, smem + G::TILE);
   arrived(qf);
   block_barrier();
-  const int tiles = (keys + BN - 1) / BN;
   auto step = [&](int j, const char* now, char* next) __attribute__((always_inline)) {
     fk.load((j + 1) * BN, next);
     fv.load((j + 1) * BN, next + G::TILE);
@@ -393,15 +467,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint3
     }
     block_barrier();
   };
-  for (int j = 0; j < tiles; j += 2) {
+  for (int j = j0; j < j1; j += 2) {
     step(j, smem, smem + 2 * G::TILE);
-    if (j + 1 < tiles) step(j + 1, smem + 2 * G::TILE, smem);
+    if (j + 1 < j1) step(j + 1, smem + 2 * G::TILE, smem);
   }
   sum = halves_sum(sum);
   const bool live = mine < pl.nq;
-  store_row<DB>(op.o, pl.q0 + mine, head, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_O)), o, sum == 0.f ? 0.f : 1.f / sum);
-  if (op.lse && live && h == 0 && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_LSE)))
-    gst<float>(op.lse + head * op.ld_lse + pl.q0 + mine, sum == 0.f ? -kInf : (top * c + __builtin_amdgcn_logf(sum)) * kLn2);
+  const auto* end = late<muon_attention_t>();
+  const int rest = pl.rest ? end->zero_rest : ~0;
+  if (gridDim.y > 1) {
+    const int64_t row = (static_cast<int64_t>(blockIdx.y) * end->tokens + pl.q0 + mine) * end->heads + head;
+    store_part<DB>(part_o + row * dim, dim, h, live, o, sum == 0.f ? 0.f : 1.f / sum);
+    if (live && h == 0) gst<float>(part_lse + row, sum == 0.f ? -kInf : (top * c + __builtin_amdgcn_logf(sum)) * kLn2);
+    return;
+  }
+  store_row<DB>(copy(end->o), pl.q0 + mine, head, dim, h, live && (rest & MUON_ATTN_ZERO_O), o, sum == 0.f ? 0.f : 1.f / sum);
+  if (end->lse && live && h == 0 && (rest & MUON_ATTN_ZERO_LSE))
+    gst<float>(end->lse + head * end->ld_lse + pl.q0 + mine, sum == 0.f ? -kInf : (top * c + __builtin_amdgcn_logf(sum)) * kLn2);
 }
 
 // ------------------------------------------------------------ backward: dQ ----
@@ -409,14 +491,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint3
 // rowsum(dO O) are one value a lane, left for the other kernel (rows x 2: lse in
 // powers of two, +inf where the row sees nothing, so that its P is 0).
 template <int DB, bool ALIGNED>
-__global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t op, uint32_t units, float* stats) {
+__global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t op, uint32_t units, float* stats, float* part_dq) {
   using G = Geo<DB>;
   __shared__ __attribute__((aligned(256))) char smem[4 * G::TILE];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
-  const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
-  const int head = uniform(at / units), unit = units - 1 - (at - head * units);
+  const auto [head, unit] = deal(units);
   const Place pl = locate<false, BM>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, (op.zero_rest & MUON_ATTN_ZERO_DQ) != 0,
-                                   unit, lane);
+                                   op.causal != 0, unit, lane);
   if (!pl.found) return;
   const int kv = uniform(static_cast<uint32_t>(head) / static_cast<uint32_t>(op.heads / op.kv_heads)), dim = op.dim;
   const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31), offset = pl.nk - pl.nq;
@@ -424,8 +505,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t o
   const int keys = op.causal ? max(0, min(pl.nk, block_last + 1)) : pl.nk;
 
   const Feed<DB, ALIGNED> fk(op.k, pl.k0, keys, kv, dim, tid), fv(op.v, pl.k0, keys, kv, dim, tid);
-  fk.load(0, smem);
-  fv.load(0, smem + G::TILE);
+  const auto [j0, j1] = part_of((keys + BN - 1) / BN);
+  fk.load(j0 * BN, smem);
+  fv.load(j0 * BN, smem + G::TILE);
   bf16x8_t qf[G::KS], gf[G::KS];
   float delta = 0.f, base = 0.f;
   {
@@ -440,7 +522,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t o
       const int64_t row = pl.q0 + mine;
       const float l = gld<float>(op.lse + head * op.ld_lse + row);
       base = l == -kInf ? kInf : l * kLog2e;
-      if (h == 0) {
+      if (h == 0 && blockIdx.y == 0) {
         gst<float>(stats + head * op.tokens + row, base);
         gst<float>(stats + (op.heads + head) * op.tokens + row, delta);
       }
@@ -456,7 +538,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t o
   arrived(qf);
   arrived(gf);
   block_barrier();
-  const int tiles = (keys + BN - 1) / BN;
   auto step = [&](int j, const char* now, char* next) __attribute__((always_inline)) {
     fk.load((j + 1) * BN, next);
     fv.load((j + 1) * BN, next + G::TILE);
@@ -489,11 +570,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t o
     }
     block_barrier();
   };
-  for (int j = 0; j < tiles; j += 2) {
+  for (int j = j0; j < j1; j += 2) {
     step(j, smem, smem + 2 * G::TILE);
-    if (j + 1 < tiles) step(j + 1, smem + 2 * G::TILE, smem);
+    if (j + 1 < j1) step(j + 1, smem + 2 * G::TILE, smem);
   }
-  store_row<DB>(op.dq, pl.q0 + mine, head, dim, h, mine < pl.nq, dq, op.scale);
+  const auto* end = late<muon_attention_grad_t>();
+  if (gridDim.y > 1) {
+    const int64_t row = (static_cast<int64_t>(blockIdx.y) * end->tokens + pl.q0 + mine) * end->heads + head;
+    store_part<DB>(part_dq + row * dim, dim, h, mine < pl.nq, dq, 1.f);
+    return;
+  }
+  store_row<DB>(copy(end->dq), pl.q0 + mine, head, dim, h, mine < pl.nq, dq, end->scale);
 }
 
 // ------------------------------------------------------- backward: dK and dV ----
@@ -512,23 +599,23 @@ template <int DB>
 constexpr int kKeyWaves = DB == 4 ? 8 : 4;
 
 template <int DB, bool ALIGNED>
-__global__ __launch_bounds__(64 * kKeyWaves<DB>, 2) void k_attn_dkv(muon_attention_grad_t op, uint32_t units, const float* stats) {
+__global__ __launch_bounds__(64 * kKeyWaves<DB>, 2) void k_attn_dkv(muon_attention_grad_t op, uint32_t units, const float* stats, float* part_dkv) {
   using G = Geo<DB>;
   constexpr int KB = 1, KS = G::KS, AHEAD = 2, WAVES = kKeyWaves<DB>, OWN = 32 * WAVES;
   constexpr int STAGE = 2 * G::TILE + 2 * BN * 4;       // Q, dO, lse, delta
   constexpr bool V_LDS = DB == 4;                       // the registers hold K alone
   __shared__ __attribute__((aligned(256))) char smem[2 * STAGE + (V_LDS ? OWN * G::ROWB : 0)];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
-  const uint32_t at = static_cast<uint32_t>(xcd_remap(blockIdx.x, gridDim.x));
-  const int kv = uniform(at / units), unit = at - kv * units;
+  const auto [kv, unit] = deal(units);
   const Place pl = locate<true, OWN>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens,
-                                     (op.zero_rest & (MUON_ATTN_ZERO_DK | MUON_ATTN_ZERO_DV)) != 0, unit, lane);
+                                     (op.zero_rest & (MUON_ATTN_ZERO_DK | MUON_ATTN_ZERO_DV)) != 0, op.causal != 0, unit, lane);
   if (!pl.found) return;
   const int share = uniform(static_cast<uint32_t>(op.heads) / static_cast<uint32_t>(op.kv_heads)), dim = op.dim;
   const int first = pl.tile * OWN + 32 * KB * w, mine = first + (lane & 31), offset = pl.nk - pl.nq;
   // the first query that sees a key of the block
   const int from = op.causal ? max(0, pl.tile * OWN - offset) : 0;
-  const int j0 = from / BN, tiles = (pl.nq + BN - 1) / BN;
+  const int first_tile = from / BN, tiles = max((pl.nq + BN - 1) / BN - first_tile, 0);
+  const auto [s0, s1] = part_of(share * tiles);          // steps: the heads' tiles, one head after the other
 
   bf16x8_t kf[KB][KS], vf[V_LDS ? 1 : KB][KS];
   char* const own_v = smem + 2 * STAGE + w * (32 * KB) * G::ROWB;       // the wave's own rows of V, for itself
@@ -557,9 +644,13 @@ __global__ __launch_bounds__(64 * kKeyWaves<DB>, 2) void k_attn_dkv(muon_attenti
     if constexpr (!V_LDS) arrived(vf[kb]);
   }
 
-  for (int head = kv * share; head < (kv + 1) * share; ++head) {
-    const Feed<DB, ALIGNED, WAVES> fq(op.q, pl.q0, pl.nq, head, dim, tid), fg(op.dout, pl.q0, pl.nq, head, dim, tid);
-    const float* rows = stats + head * op.tokens + pl.q0 + (w == 1 ? op.heads * op.tokens : 0);   // wave 0: lse, 1: delta
+  for (int turn = 0; turn < share; ++turn) {
+    const int head = kv * share + turn, j0 = uniform(first_tile + max(s0 - turn * tiles, 0)),
+              j1 = uniform(first_tile + min(s1 - turn * tiles, tiles));
+    if (j0 >= j1) continue;
+    const auto* in = late<muon_attention_grad_t>();
+    const Feed<DB, ALIGNED, WAVES> fq(copy(in->q), pl.q0, pl.nq, head, dim, tid), fg(copy(in->dout), pl.q0, pl.nq, head, dim, tid);
+    const float* rows = stats + head * in->tokens + pl.q0 + (w == 1 ? in->heads * in->tokens : 0);   // wave 0: lse, 1: delta
     auto load = [&](int j, char* to) __attribute__((always_inline)) {
       fq.load(j * BN, to);
       fg.load(j * BN, to + G::TILE);
@@ -635,18 +726,75 @@ __global__ __launch_bounds__(64 * kKeyWaves<DB>, 2) void k_attn_dkv(muon_attenti
     };
     load(j0, smem);
     block_barrier();
-    for (int j = j0; j < tiles; j += 2) {
+    for (int j = j0; j < j1; j += 2) {
       step(j, smem, smem + STAGE);
-      if (j + 1 < tiles) step(j + 1, smem + STAGE, smem);
+      if (j + 1 < j1) step(j + 1, smem + STAGE, smem);
     }
   }
+  const auto* end = late<muon_attention_grad_t>();
+  const int rest = pl.rest ? end->zero_rest : ~0;
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     const int key = mine + 32 * kb;
     const bool live = key < pl.nk;
-    store_row<DB>(op.dk, pl.k0 + key, kv, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_DK)), dk[kb], op.scale);
-    store_row<DB>(op.dv, pl.k0 + key, kv, dim, h, live && !(pl.rest && !(op.zero_rest & MUON_ATTN_ZERO_DV)), dv[kb], 1.f);
+    if (gridDim.y > 1) {
+      const int64_t rows = end->k_tokens * end->kv_heads, row = (pl.k0 + key) * end->kv_heads + kv;
+      store_part<DB>(part_dkv + (2 * blockIdx.y * rows + row) * dim, dim, h, live, dk[kb], 1.f);
+      store_part<DB>(part_dkv + ((2 * blockIdx.y + 1) * rows + row) * dim, dim, h, live, dv[kb], 1.f);
+      continue;
+    }
+    store_row<DB>(copy(end->dk), pl.k0 + key, kv, dim, h, live && (rest & MUON_ATTN_ZERO_DK), dk[kb], end->scale);
+    store_row<DB>(copy(end->dv), pl.k0 + key, kv, dim, h, live && (rest & MUON_ATTN_ZERO_DV), dv[kb], 1.f);
   }
+}
+
+// ------------------------------------------------------------------- parts ----
+// Joins the parts of a few long rows, in their order: 8 columns a thread of `rows` x `heads`
+// x `dim` (gridDim.y: 2 tensors, one behind the other in each part).  With lse, parts of
+// attention are weighted by exp(lse of the part - lse).
+struct Join {
+  muon_heads_t  out[2];
+  const float*  part;
+  const float*  part_lse;      // NULL: sums
+  float*        lse;           // may be NULL
+  const int32_t* starts;
+  int64_t       sequences, rows, heads, dim, ld_lse;
+  int           parts;
+  float         factor[2];
+  bool          all[2], all_lse;   // also rows behind the last sequence
+};
+
+__global__ __launch_bounds__(256) void k_attn_join(Join j) {
+  const int which = blockIdx.y;
+  const int64_t chunks = j.dim / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, at = i / chunks, row = at / j.heads;
+  if (row >= j.rows) return;
+  const int64_t head = at - row * j.heads, d = (i - at * chunks) * 8, end = j.starts ? gld<int32_t>(j.starts + j.sequences) : j.rows;
+  const bool inside = row < end;
+  float v[8] = {}, top = -kInf, total = 0.f;
+  if (j.part_lse)
+    for (int p = 0; p < j.parts; ++p) top = fmaxf(top, gld<float>(j.part_lse + (p * j.rows + row) * j.heads + head));
+  const float base = top == -kInf ? 0.f : top;
+  for (int p = 0; p < j.parts; ++p) {
+    const float* from = j.part + ((static_cast<int64_t>(p) * gridDim.y + which) * j.rows * j.heads + at) * j.dim + d;
+    const f32x4_t a = gld<f32x4_t>(from), b = gld<f32x4_t>(from + 4);
+    float f = 1.f;
+    if (j.part_lse) {
+      f = exp2_fast((gld<float>(j.part_lse + (p * j.rows + row) * j.heads + head) - base) * kLog2e);
+      total += f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] += f * a[e];
+      v[4 + e] += f * b[e];
+    }
+  }
+  const float f = j.part_lse ? (total == 0.f ? 0.f : 1.f / total) : j.factor[which];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= f;
+  if (inside || j.all[which])
+    Vec8<uint16_t>::store(static_cast<uint16_t*>(j.out[which].data) + row * j.out[which].ld_token + head * j.out[which].ld_head + d, 8, v);
+  if (j.lse && d == 0 && (inside || j.all_lse))
+    gst<float>(j.lse + head * j.ld_lse + row, total == 0.f ? -kInf : base + __builtin_amdgcn_logf(total) * kLn2);
 }
 
 // ---------------------------------------------------------------- dispatch ----
@@ -667,33 +815,140 @@ int by_shape(int64_t dim, bool aligned, F&& f) {
   return with(std::integral_constant<int, 4>{});
 }
 
+int key_rows(int64_t dim) { return dim > 96 ? 32 * kKeyWaves<4> : 32 * kKeyWaves<2>; }   // that a block of k_attn_dkv owns
+
+// Parts that the steps of `blocks` blocks are cut into, `steps` each on average: so many
+// that the chip's 512 places (two blocks a CU) are filled, of 4 steps at least.
+int parts_of(int64_t blocks, int64_t steps) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kMaxParts, 512 / std::max<int64_t>(blocks, 1), steps / 4})));
+}
+
+template <class Op>
+int64_t average_steps(const Op& op, int64_t rows) {
+  const int64_t n = rows / std::max<int64_t>(1, op.starts ? op.sequences : 1) / BN;
+  return op.causal ? n / 2 : n;
+}
+
+size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+template <class Op>
+int query_parts(const Op& op) {
+  return parts_of((op.tokens + BM - 1) / BM * op.heads, average_steps(op, op.k_tokens));
+}
+
 }  // namespace
 
-int launch_attention(const muon_attention_t& op, void* stream) {
+AttnPlan attention_plan(const muon_attention_t& op) {
+  AttnPlan p{};
+  p.parts = query_parts(op);
+  if (p.parts > 1) {
+    const size_t rows = static_cast<size_t>(p.parts) * op.tokens * op.heads;
+    p.lse_off = rounded(rows * op.dim * sizeof(float));
+    p.bytes = p.lse_off + rounded(rows * sizeof(float));
+  }
+  return p;
+}
+
+AttnGradPlan attention_grad_plan(const muon_attention_grad_t& op) {
+  AttnGradPlan p{};
+  const size_t q = static_cast<size_t>(op.tokens) * op.heads, k = static_cast<size_t>(op.k_tokens) * op.kv_heads;
+  p.parts_q = query_parts(op);
+  const int own = key_rows(op.dim);
+  p.parts_k = parts_of((op.k_tokens + own - 1) / own * op.kv_heads, op.heads / op.kv_heads * average_steps(op, op.tokens));
+  p.dq_off = rounded(2 * q * sizeof(float));
+  p.dkv_off = p.dq_off + (p.parts_q > 1 ? rounded(p.parts_q * q * op.dim * sizeof(float)) : 0);
+  p.bytes = p.dkv_off + (p.parts_k > 1 ? rounded(2 * p.parts_k * k * op.dim * sizeof(float)) : 0);
+  return p;
+}
+
+int launch_attention(const muon_attention_t& op, const AttnPlan& p, char* ws, void* stream) {
   const uint32_t units = units_of(op.tokens, op.sequences, op.starts != nullptr);
   return by_shape(op.dim, aligned16(op.k) && aligned16(op.v), [&](auto db, auto al) {
-    hipLaunchKernelGGL((k_attn<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.heads)), dim3(kThreads), 0,
-                       static_cast<hipStream_t>(stream), op, units);
+    hipLaunchKernelGGL((k_attn<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.heads), p.parts),
+                       dim3(kThreads), 0, static_cast<hipStream_t>(stream), op, units, reinterpret_cast<float*>(ws),
+                       reinterpret_cast<float*>(ws + p.lse_off));
     return static_cast<int>(hipGetLastError());
   });
 }
 
-int launch_attention_dq(const muon_attention_grad_t& op, float* stats, void* stream) {
+int launch_attention_dq(const muon_attention_grad_t& op, const AttnGradPlan& p, char* ws, void* stream) {
   const uint32_t units = units_of(op.tokens, op.sequences, op.starts != nullptr);
   return by_shape(op.dim, aligned16(op.k) && aligned16(op.v), [&](auto db, auto al) {
-    hipLaunchKernelGGL((k_attn_dq<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.heads)), dim3(kThreads), 0,
-                       static_cast<hipStream_t>(stream), op, units, stats);
+    hipLaunchKernelGGL((k_attn_dq<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.heads), p.parts_q),
+                       dim3(kThreads), 0, static_cast<hipStream_t>(stream), op, units, reinterpret_cast<float*>(ws),
+                       reinterpret_cast<float*>(ws + p.dq_off));
     return static_cast<int>(hipGetLastError());
   });
 }
 
-int launch_attention_dkv(const muon_attention_grad_t& op, const float* stats, void* stream) {
+int launch_attention_dkv(const muon_attention_grad_t& op, const AttnGradPlan& p, char* ws, void* stream) {
   return by_shape(op.dim, aligned16(op.q) && aligned16(op.dout), [&](auto db, auto al) {
-    const uint32_t units = units_of(op.k_tokens, op.sequences, op.starts != nullptr, 32 * kKeyWaves<decltype(db)::value>);
-    hipLaunchKernelGGL((k_attn_dkv<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.kv_heads)), dim3(64 * kKeyWaves<decltype(db)::value>), 0,
-                       static_cast<hipStream_t>(stream), op, units, stats);
+    constexpr int waves = kKeyWaves<decltype(db)::value>;
+    const uint32_t units = units_of(op.k_tokens, op.sequences, op.starts != nullptr, 32 * waves);
+    hipLaunchKernelGGL((k_attn_dkv<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.kv_heads), p.parts_k),
+                       dim3(64 * waves), 0, static_cast<hipStream_t>(stream), op, units, reinterpret_cast<const float*>(ws),
+                       reinterpret_cast<float*>(ws + p.dkv_off));
     return static_cast<int>(hipGetLastError());
   });
+}
+
+namespace {
+int launch_join(const Join& j, int tensors, void* stream) {
+  const int64_t threads = j.rows * j.heads * (j.dim / 8);
+  hipLaunchKernelGGL(k_attn_join, dim3(static_cast<unsigned>((threads + 255) / 256), tensors), dim3(256), 0, static_cast<hipStream_t>(stream), j);
+  return static_cast<int>(hipGetLastError());
+}
+}  // namespace
+
+int launch_attention_join(const muon_attention_t& op, const AttnPlan& p, const char* ws, void* stream) {
+  Join j{};
+  j.out[0] = op.o;
+  j.part = reinterpret_cast<const float*>(ws);
+  j.part_lse = reinterpret_cast<const float*>(ws + p.lse_off);
+  j.lse = op.lse;
+  j.ld_lse = op.ld_lse;
+  j.starts = op.starts;
+  j.sequences = op.sequences;
+  j.rows = op.tokens;
+  j.heads = op.heads;
+  j.dim = op.dim;
+  j.parts = p.parts;
+  j.all[0] = op.zero_rest & MUON_ATTN_ZERO_O;
+  j.all_lse = op.zero_rest & MUON_ATTN_ZERO_LSE;
+  return launch_join(j, 1, stream);
+}
+
+int launch_attention_dq_join(const muon_attention_grad_t& op, const AttnGradPlan& p, const char* ws, void* stream) {
+  Join j{};
+  j.out[0] = op.dq;
+  j.part = reinterpret_cast<const float*>(ws + p.dq_off);
+  j.starts = op.starts;
+  j.sequences = op.sequences;
+  j.rows = op.tokens;
+  j.heads = op.heads;
+  j.dim = op.dim;
+  j.parts = p.parts_q;
+  j.factor[0] = op.scale;
+  j.all[0] = op.zero_rest & MUON_ATTN_ZERO_DQ;
+  return launch_join(j, 1, stream);
+}
+
+int launch_attention_dkv_join(const muon_attention_grad_t& op, const AttnGradPlan& p, const char* ws, void* stream) {
+  Join j{};
+  j.out[0] = op.dk;
+  j.out[1] = op.dv;
+  j.part = reinterpret_cast<const float*>(ws + p.dkv_off);
+  j.starts = op.k_starts ? op.k_starts : op.starts;
+  j.sequences = op.sequences;
+  j.rows = op.k_tokens;
+  j.heads = op.kv_heads;
+  j.dim = op.dim;
+  j.parts = p.parts_k;
+  j.factor[0] = op.scale;
+  j.factor[1] = 1.f;
+  j.all[0] = op.zero_rest & MUON_ATTN_ZERO_DK;
+  j.all[1] = op.zero_rest & MUON_ATTN_ZERO_DV;
+  return launch_join(j, 2, stream);
 }
 
 }  // namespace muon

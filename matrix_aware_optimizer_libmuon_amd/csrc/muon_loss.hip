@@ -30,23 +30,6 @@ constexpr float kNegInf = -__builtin_inff();
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }   // 1 ulp
 __device__ __forceinline__ float log2_fast(float v) { return __builtin_amdgcn_logf(v); }
 
-// Over the wave, in every lane: within rows of 16 by data-parallel moves, then across them
-// by exchanges of rows (a sixth of the latency of permutations through LDS).
-template <class F>
-__device__ __forceinline__ float wave_all(float v, F f) {
-  auto moved = [](float x, auto ctrl) {
-    return __uint_as_float(static_cast<uint32_t>(
-        __builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(x)), decltype(ctrl)::value, 0xf, 0xf, true)));
-  };
-  v = f(v, moved(v, std::integral_constant<int, 0xB1>{}));    // lanes 1 0 3 2
-  v = f(v, moved(v, std::integral_constant<int, 0x4E>{}));    // lanes 2 3 0 1
-  v = f(v, moved(v, std::integral_constant<int, 0x141>{}));   // 8 lanes mirrored
-  v = f(v, moved(v, std::integral_constant<int, 0x140>{}));   // 16 lanes mirrored
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
 __device__ __forceinline__ float wave_max(float v) {
   return wave_all(v, [](float x, float y) { return fmaxf(x, y); });
 }

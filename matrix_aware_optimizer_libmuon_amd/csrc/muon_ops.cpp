@@ -386,7 +386,11 @@ int muon_embed_grad(const muon_embed_grad_t* op, void* workspace, size_t workspa
   return l.run("embedding gradient, join", [&](void* st) { return launch_embed_join(*op, p, ws, st); });
 }
 
-int muon_attention(const muon_attention_t* op, hipStream_t stream) {
+size_t muon_attention_workspace_bytes(const muon_attention_t* op) {
+  return attention_ok(op, MUON_ATTN_ZERO_O | MUON_ATTN_ZERO_LSE) ? attention_plan(*op).bytes : 0;
+}
+
+int muon_attention(const muon_attention_t* op, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   Args a;
   if (!attention_ok(op, MUON_ATTN_ZERO_O | MUON_ATTN_ZERO_LSE)) return MUON_EINVAL;
   const int64_t n = op->tokens, nk = op->k_tokens;
@@ -394,6 +398,9 @@ int muon_attention(const muon_attention_t* op, hipStream_t stream) {
       !a.heads(op->v, nk, op->kv_heads, op->dim, false) || !a.heads(op->o, n, op->heads, op->dim, true) ||
       (n > 0 && !a.mat(op->lse, op->heads, n, op->ld_lse, 4, true, false)) || !note_starts(a, op))
     return MUON_EINVAL;
+  const AttnPlan p = attention_plan(*op);
+  if (!workspace_ok(workspace, workspace_bytes, p.bytes)) return MUON_EWORKSPACE;
+  if (p.bytes && !a.mat(workspace, 1, static_cast<int64_t>(p.bytes), 0, 1, true)) return MUON_EWORKSPACE;
   if (a.clash()) return MUON_EALIAS;
   if (n == 0) return MUON_OK;
   muon_attention_t in = *op;
@@ -403,26 +410,31 @@ int muon_attention(const muon_attention_t* op, hipStream_t stream) {
   in.v = heads_strides(op->v, nk, op->kv_heads);
   Launcher l(stream);
   if (int rc = l.open()) return rc;
-  return l.run("attention", [&](void* st) { return launch_attention(in, st); });
+  if (int rc = l.poison(workspace, p.bytes)) return rc;
+  char* ws = static_cast<char*>(workspace);
+  if (int rc = l.run("attention", [&](void* st) { return launch_attention(in, p, ws, st); })) return rc;
+  if (p.parts == 1) return MUON_OK;
+  return l.run("attention, join", [&](void* st) { return launch_attention_join(in, p, ws, st); });
 }
 
-size_t muon_attention_grad_workspace_bytes(int64_t tokens, int64_t heads) {
-  if (tokens < 0 || heads < 1 || tokens > (int64_t(1) << 30) || heads > (int64_t(1) << 23)) return 0;
-  return static_cast<size_t>(tokens) * static_cast<size_t>(heads) * 2 * sizeof(float);
+static constexpr int32_t kGradZeros = MUON_ATTN_ZERO_DQ | MUON_ATTN_ZERO_DK | MUON_ATTN_ZERO_DV;
+
+size_t muon_attention_grad_workspace_bytes(const muon_attention_grad_t* op) {
+  return attention_ok(op, kGradZeros) ? attention_grad_plan(*op).bytes : 0;
 }
 
 int muon_attention_grad(const muon_attention_grad_t* op, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   Args a;
-  if (!attention_ok(op, MUON_ATTN_ZERO_DQ | MUON_ATTN_ZERO_DK | MUON_ATTN_ZERO_DV)) return MUON_EINVAL;
+  if (!attention_ok(op, kGradZeros)) return MUON_EINVAL;
   const int64_t n = op->tokens, nk = op->k_tokens, h = op->heads, kv = op->kv_heads, d = op->dim;
   if (!a.heads(op->dout, n, h, d, false) || !a.heads(op->q, n, h, d, false) || !a.heads(op->o, n, h, d, false) ||
       !a.heads(op->k, nk, kv, d, false) || !a.heads(op->v, nk, kv, d, false) || !a.heads(op->dq, n, h, d, true) ||
       !a.heads(op->dk, nk, kv, d, true) || !a.heads(op->dv, nk, kv, d, true) ||
       (n > 0 && !a.mat(op->lse, h, n, op->ld_lse, 4, false)) || !note_starts(a, op))
     return MUON_EINVAL;
-  const size_t need = muon_attention_grad_workspace_bytes(n, h);
-  if (!workspace_ok(workspace, workspace_bytes, need)) return MUON_EWORKSPACE;
-  if (need && !a.mat(workspace, 1, static_cast<int64_t>(need), 0, 1, true)) return MUON_EWORKSPACE;
+  const AttnGradPlan p = attention_grad_plan(*op);
+  if (!workspace_ok(workspace, workspace_bytes, p.bytes)) return MUON_EWORKSPACE;
+  if (p.bytes && !a.mat(workspace, 1, static_cast<int64_t>(p.bytes), 0, 1, true)) return MUON_EWORKSPACE;
   if (a.clash()) return MUON_EALIAS;
   if (n == 0 && nk == 0) return MUON_OK;
   muon_attention_grad_t in = *op;
@@ -430,12 +442,17 @@ int muon_attention_grad(const muon_attention_grad_t* op, void* workspace, size_t
   for (muon_heads_t* t : {&in.k, &in.v, &in.dk, &in.dv}) *t = heads_strides(*t, nk, kv);
   Launcher l(stream);
   if (int rc = l.open()) return rc;
-  if (int rc = l.poison(workspace, need)) return rc;
-  float* stats = static_cast<float*>(workspace);
-  if (n > 0)
-    if (int rc = l.run("attention gradient, queries", [&](void* st) { return launch_attention_dq(in, stats, st); })) return rc;
+  if (int rc = l.poison(workspace, p.bytes)) return rc;
+  char* ws = static_cast<char*>(workspace);
+  if (n > 0) {
+    if (int rc = l.run("attention gradient, queries", [&](void* st) { return launch_attention_dq(in, p, ws, st); })) return rc;
+    if (p.parts_q > 1)
+      if (int rc = l.run("attention gradient, queries' join", [&](void* st) { return launch_attention_dq_join(in, p, ws, st); })) return rc;
+  }
   if (nk == 0) return MUON_OK;
-  return l.run("attention gradient, keys", [&](void* st) { return launch_attention_dkv(in, stats, st); });
+  if (int rc = l.run("attention gradient, keys", [&](void* st) { return launch_attention_dkv(in, p, ws, st); })) return rc;
+  if (p.parts_k == 1) return MUON_OK;
+  return l.run("attention gradient, keys' join", [&](void* st) { return launch_attention_dkv_join(in, p, ws, st); });
 }
 
 static bool temperature_ok(float t) { return t >= 1e-6f && t <= 1e6f; }

@@ -76,11 +76,28 @@ int launch_embed_starts(const muon_embed_grad_t& op, const EmbedSortPlan& p, cha
 int launch_embed_sums(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
 int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char* ws, void* stream);
 
-// muon_attn.hip.  stats: heads x tokens of lse and of rowsum(dout o), left by the
-// first kernel of the backward pass for the second.
-int launch_attention(const muon_attention_t& op, void* stream);
-int launch_attention_dq(const muon_attention_grad_t& op, float* stats, void* stream);
-int launch_attention_dkv(const muon_attention_grad_t& op, const float* stats, void* stream);
+// muon_attn.hip.  Workspace: where few blocks have long rows, their steps are cut into
+// parts whose results a further launch joins.
+struct AttnPlan {
+  int parts;
+  size_t lse_off;      // each part's lse, behind its o
+  size_t bytes;
+};
+AttnPlan attention_plan(const muon_attention_t& op);
+int launch_attention(const muon_attention_t& op, const AttnPlan& p, char* ws, void* stream);
+int launch_attention_join(const muon_attention_t& op, const AttnPlan& p, const char* ws, void* stream);
+// and first of all lse and rowsum(dout o), heads x tokens each, which the kernel of dq
+// leaves for the one of dk and dv
+struct AttnGradPlan {
+  int parts_q, parts_k;
+  size_t dq_off, dkv_off;
+  size_t bytes;
+};
+AttnGradPlan attention_grad_plan(const muon_attention_grad_t& op);
+int launch_attention_dq(const muon_attention_grad_t& op, const AttnGradPlan& p, char* ws, void* stream);
+int launch_attention_dkv(const muon_attention_grad_t& op, const AttnGradPlan& p, char* ws, void* stream);
+int launch_attention_dq_join(const muon_attention_grad_t& op, const AttnGradPlan& p, const char* ws, void* stream);
+int launch_attention_dkv_join(const muon_attention_grad_t& op, const AttnGradPlan& p, const char* ws, void* stream);
 
 // muon_loss.hip
 int launch_distill(const muon_distill_t& op, void* stream);

@@ -74,9 +74,9 @@ def _child():
     def heads(n, dim):
         return L.MuonHeads(ptr(), n * dim, dim)
 
-    def attention(entry, tokens, k_tokens, heads_, kv, dim, sequences, odd=False, layout=None):
+    def attention(entry, tokens, k_tokens, heads_, kv, dim, sequences, odd=False, layout=None, causal=1):
         ends = dict(starts=ptr() if sequences else None, k_starts=ptr() if sequences else None, sequences=sequences, tokens=tokens,
-                    k_tokens=k_tokens, heads=heads_, kv_heads=kv, dim=dim, ld_lse=max(tokens, 1), scale=1.0, causal=1, zero_rest=3)
+                    k_tokens=k_tokens, heads=heads_, kv_heads=kv, dim=dim, ld_lse=max(tokens, 1), scale=1.0, causal=causal, zero_rest=3)
         own, shared = (lambda: heads(heads_, dim)), (lambda: heads(kv, dim))
         q, k, v = own(), shared(), shared()
         if layout:                                   # all heads of a kind in one buffer (tokens == k_tokens, heads_ == kv)
@@ -90,10 +90,11 @@ def _child():
             q.data += 2
             v.data += 2
         if entry == "attention":
-            return lib.muon_attention(ctypes.byref(L.MuonAttention(q=q, k=k, v=v, o=own(), lse=ptr(), **ends)), None)
+            op = L.MuonAttention(q=q, k=k, v=v, o=own(), lse=ptr(), **ends)
+            return lib.muon_attention(ctypes.byref(op), ctypes.c_void_p(1 << 60), lib.muon_attention_workspace_bytes(ctypes.byref(op)), None)
         op = L.MuonAttentionGrad(dout=own(), q=q, k=k, v=v, o=own(), dq=own(), dk=shared(), dv=shared(), lse=ptr(), **ends)
         return lib.muon_attention_grad(ctypes.byref(op), ctypes.c_void_p(1 << 60),
-                                       lib.muon_attention_grad_workspace_bytes(tokens, heads_), None)
+                                       lib.muon_attention_grad_workspace_bytes(ctypes.byref(op)), None)
 
     def loss(entry, tokens, vocab, dtype):
         t = L.MUON_BF16 if dtype == "bf16" else L.MUON_F32

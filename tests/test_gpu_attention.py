@@ -70,13 +70,20 @@ def exp_error(q, k, lse, scale):
 
 
 def check(q, k, v, nq_list, nk_list, causal, scale=None, seed=7, layout="plain", starts=True):
-    heads, kv, dim = q.shape[1], k.shape[1], q.shape[2]
+    dim = q.shape[2]
     c = float(np.float32(dim ** -0.5 if scale is None else scale))
     st = dict(starts=starts_of(nq_list) if starts else None,
               k_starts=starts_of(nk_list) if starts and nq_list is not nk_list else None, causal=causal, scale=scale)
     o, lse = muon.attention(q, k, v, **st)
     do = placed(torch.randn(q.shape, generator=gen(seed)).to(BF), layout)
     grads = muon.attention_grad(do, q, k, v, o, lse, **st)
+    compare(q, k, v, do, o, lse, grads, nq_list, nk_list, causal, c)
+    return (o, lse, *grads)
+
+
+def compare(q, k, v, do, o, lse, grads, nq_list, nk_list, causal, c):
+    """Outputs of both directions against the oracle; c: the scale."""
+    heads, kv, dim = q.shape[1], k.shape[1], q.shape[2]
     want = [np.zeros(t.shape) for t in (q, q, k, v)]
     tol = [np.zeros(t.shape) for t in (q, q, k, v)]
     lse_want, lse_tol = np.zeros(lse.shape), np.zeros(lse.shape)
@@ -113,9 +120,9 @@ def check(q, k, v, nq_list, nk_list, causal, scale=None, seed=7, layout="plain",
             near(got, ref, BF, 1.0, t)
         except AssertionError as err:
             raise AssertionError(f"{name}: {err}") from None
-    bad = ~((np.abs(l_ - lse_want) <= lse_tol + 4 * U * np.abs(lse_want)) | (l_ == lse_want))
-    assert not bad.any()
-    return (o, lse, *grads)
+    same = l_ == lse_want                                    # -infinity among them
+    off = np.abs(np.where(same, 0.0, l_) - np.where(same, 0.0, lse_want))
+    assert (off <= lse_tol + 4 * U * np.abs(np.where(same, 0.0, lse_want))).all()
 
 
 @pytest.mark.parametrize("causal", [True, False])
@@ -177,6 +184,26 @@ def test_sharp_and_flat_rows(sharp, scale):
 
 def test_single_queries_over_long_keys():
     check(*tensors(8, 3, 3000, 4, 1, 128), [1, 2], [1000, 2000], True)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,heads,kv,dim", [([40], [4096], 4, 2, 64), ([1], [5000], 2, 1, 128), ([3, 0, 70], [3000, 9, 2500], 2, 2, 80),
+                                                ([2500], [2500], 1, 1, 64), ([2100, 30], [2100, 30], 4, 1, 128), ([3000], [50], 2, 1, 40),
+                                                ([1500], [1400], 3, 3, 96)])
+def test_steps_cut_into_parts(nq, nk, heads, kv, dim, causal):
+    """Few blocks of many steps (tests/test_ops_launches.py has the launches that these sizes make)."""
+    check(*tensors(heads, sum(nq), sum(nk), heads, kv, dim), nq, nk, causal)
+    kept = torch.full((sum(nq) + 9, heads, dim), 7.0, dtype=BF, device=DEV)
+    q, k, v = tensors(heads, sum(nq) + 9, sum(nk) + 5, heads, kv, dim)
+    st = dict(starts=starts_of(nq), k_starts=starts_of(nk), causal=causal)
+    o, lse = muon.attention(q, k, v, out=kept, **st)
+    fresh, _ = muon.attention(q, k, v, **st)
+    assert (o[-9:] == 7).all() and not fresh[-9:].any() and torch.equal(o[:-9], fresh[:-9]) and (lse[:, -9:] == -float("inf")).all()
+    mine = [torch.full_like(t, 7.0) for t in (q, k, v)]
+    grads = muon.attention_grad(o, q, k, v, o, lse, dq=mine[0], dk=mine[1], dv=mine[2], **st)
+    news = muon.attention_grad(o, q, k, v, o, lse, **st)
+    for a, b, n in zip(grads, news, (9, 5, 5)):
+        assert (a[-n:] == 7).all() and not b[-n:].any() and torch.equal(a[:-n], b[:-n])
 
 
 def test_gradients_by_differences():
@@ -282,27 +309,26 @@ def test_the_same_bits_every_time():
 
 
 def test_offsets_past_32_bits():
-    """q, k, v of more than 2^32 bytes: the last sequence equals the same alone."""
-    n, heads, dim, tail = 1 << 20, 18, 128, 300
-    big = torch.zeros(n, heads, dim, dtype=BF, device=DEV)
+    """q, k, v of more than 2^32 bytes: the first and the last sequence."""
+    n, dim, tail = 1 << 20, 128, 300
+    big = torch.zeros(n, 18, dim, dtype=BF, device=DEV)
     st = torch.tensor([0, 64, n - tail, n], dtype=torch.int32, device=DEV)
-    st[2] = n - tail
-    g = gen(2)
-    last = [torch.randn(tail, h, dim, generator=g).to(BF).to(DEV) for h in (16, 1, 1, 16)]
-    big[n - tail:, :16], big[n - tail:, 16:17], big[n - tail:, 17:] = last[:3]
     # the long middle has no keys: two sets of starts
     ks = torch.tensor([0, 64, 64, 64 + tail], dtype=torch.int32, device=DEV)
-    q = big[:, :16]
-    k, v = big[n - 64 - tail:, 16:17], big[n - 64 - tail:, 17:]
+    ends = torch.cat([torch.arange(64), torch.arange(n - tail, n)]).to(DEV)
+    g = gen(2)
+    q, k, v = big[:, :16], big[n - 64 - tail:, 16:17], big[n - 64 - tail:, 17:]
+    q[ends] = torch.randn(64 + tail, 16, dim, generator=g).to(BF).to(DEV)
+    k.copy_(torch.randn(64 + tail, 1, dim, generator=g).to(BF))
+    v.copy_(torch.randn(64 + tail, 1, dim, generator=g).to(BF))
+    do = torch.zeros(n, 16, dim, dtype=BF, device=DEV)
+    do[ends] = torch.randn(64 + tail, 16, dim, generator=g).to(BF).to(DEV)
     o, lse = muon.attention(q, k, v, starts=st, k_starts=ks)
     say("attended")
-    o1, lse1 = muon.attention(*last[:3])
-    assert torch.equal(o[n - tail:], o1) and torch.equal(lse[:, n - tail:], lse1) and not o[64:n - tail].any()
-    do = torch.zeros_like(o)
-    do[n - tail:] = last[3]
     dq, dk, dv = muon.attention_grad(do, q, k, v, o, lse, starts=st, k_starts=ks)
-    want = muon.attention_grad(last[3], *last[:3], o1, lse1)
-    assert torch.equal(dq[n - tail:], want[0]) and torch.equal(dk[64:], want[1]) and torch.equal(dv[64:], want[2])
+    assert not o[64:n - tail].any() and not dq[64:n - tail].any()
+    compare(q[ends], k, v, do[ends], o[ends], lse[:, ends], (dq[ends], dk, dv), [64, tail], [64, tail], True,
+            float(np.float32(dim ** -0.5)))
 
 
 def test_refusals_name_the_argument():

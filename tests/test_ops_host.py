@@ -278,10 +278,10 @@ BAD_ATTENTION = [
 
 
 def test_attention_refuses(lib):
-    def fwd(**kw):
-        return lib.muon_attention(ctypes.byref(attn(**kw)), None)
+    def fwd(ws=WS, ws_bytes=1 << 40, **kw):
+        return lib.muon_attention(ctypes.byref(attn(**kw)), ws, ws_bytes, None)
 
-    assert lib.muon_attention(None, None) == EINVAL
+    assert lib.muon_attention(None, None, 0, None) == EINVAL and lib.muon_attention_workspace_bytes(None) == 0
     for bad in [*BAD_ATTENTION, dict(o=heads(data=0)), dict(zero_rest=4), dict(o=heads(ld_token=64))]:
         assert fwd(**bad) == EINVAL, bad
     p = ptr()
@@ -294,14 +294,24 @@ def test_attention_refuses(lib):
     first = lambda at: heads(4, data=p + 2 * at, ld_token=64, ld_head=40 * 64)  # noqa: E731
     for make, apart in ((wide, 256), (mixed, 64), (first, 4 * 40 * 64)):
         assert fwd(q=make(0), o=make(apart - 8)) == EALIAS and fwd(q=make(apart - 8), o=make(0)) == EALIAS
+    # few rows over many keys are cut into parts: o and lse of each in the workspace
+    long = dict(k_tokens=4096, causal=0)
+    need = lib.muon_attention_workspace_bytes(ctypes.byref(attn(**long)))
+    assert need == 16 * 40 * 4 * (64 + 1) * 4 and lib.muon_attention_workspace_bytes(ctypes.byref(attn())) == 0
+    assert lib.muon_attention_workspace_bytes(ctypes.byref(attn(**long, dim=60))) == 0
+    assert fwd(ws=None, **long) == EWORKSPACE and fwd(ws_bytes=need - 1, **long) == EWORKSPACE
+    assert fwd(ws=ctypes.c_void_p((1 << 42) + 8), **long) == EWORKSPACE and fwd(lse=1 << 42, **long) == EALIAS
     # nothing to do
     assert fwd(tokens=0, q=heads(data=0), o=heads(data=0), lse=0) == 0
 
 
 def test_attention_gradient_refuses(lib):
-    need = lib.muon_attention_grad_workspace_bytes(40, 4)
-    assert need == 2 * 4 * 40 * 4 and lib.muon_attention_grad_workspace_bytes(0, 4) == 0
-    assert lib.muon_attention_grad_workspace_bytes(-1, 4) == 0 and lib.muon_attention_grad_workspace_bytes(4, 0) == 0
+    size = lambda **kw: lib.muon_attention_grad_workspace_bytes(ctypes.byref(attn_grad(**kw)))  # noqa: E731
+    need = size()
+    assert need == 2 * 4 * 40 * 4 and size(tokens=0) == 0 and size(dim=60) == 0 and lib.muon_attention_grad_workspace_bytes(None) == 0
+    # lse and rowsum(dout o); parts of dq over many keys; parts of dk and dv over many queries
+    assert size(k_tokens=4096, causal=0) == need + 16 * 40 * 4 * 64 * 4
+    assert size(tokens=4096, causal=0) == 2 * 4 * 4096 * 4 + 2 * 16 * 40 * 2 * 64 * 4
 
     def bwd(ws=WS, ws_bytes=need, **kw):
         return lib.muon_attention_grad(ctypes.byref(attn_grad(**kw)), ws, ws_bytes, None)

@@ -107,3 +107,20 @@ def test_attention_takes_slices_of_one_buffer(layout):
     args = dict(tokens=40, k_tokens=40, heads_=4, kv=4, dim=64, sequences=0, layout=layout)
     for status, launches in record([("attention", args), ("attention_grad", args)]):
         assert status == 0 and launches
+
+
+@pytest.mark.parametrize("tokens,k_tokens,heads_,kv,dim,sequences,parts", [
+    (40, 4096, 4, 2, 64, 0, (16, 16, 1)), (1, 5000, 2, 1, 128, 0, (16, 16, 1)), (73, 5509, 2, 2, 80, 3, (7, 7, 1)),
+    (2500, 2500, 1, 1, 64, 0, (9, 9, 9)), (2130, 2130, 4, 1, 128, 2, (4, 4, 16)), (3000, 50, 2, 1, 40, 0, (1, 1, 16)),
+    (1500, 1400, 3, 3, 96, 0, (5, 5, 5)), (16384, 16384, 32, 8, 128, 4, (1, 1, 1)), (74, 74, 4, 4, 64, 2, (1, 1, 1))])
+def test_parts_of_attention(tokens, k_tokens, heads_, kv, dim, sequences, parts):
+    """How many parts the steps of the tested sizes are cut into: forward, dq, dk and dv; each cut has its join."""
+    args = dict(tokens=tokens, k_tokens=k_tokens, heads_=heads_, kv=kv, dim=dim, sequences=sequences, causal=0)
+    launches = [l for _, ls in record([(e, args) for e in ("attention", "attention_grad")]) for l in ls]
+    got, joins = [], 0
+    for kernel, grid, _ in launches:
+        if kernel == "k_attn_join":
+            joins += 1
+        else:
+            got.append(grid[1])
+    assert tuple(got) == parts and joins == sum(p > 1 for p in parts)
