@@ -595,7 +595,7 @@ typedef struct {
  *   zero_rest what to do with tokens behind the last sequence: 0 leaves them as they
  *             are; MUON_ATTN_ZERO_O, _LSE write zeros (-infinity to lse)
  * dim is a multiple of 8 up to 128; tokens, k_tokens 0 .. 2^30; with t the larger
- * of them (t / 128 + sequences + 2) heads <= 2^23.  Products of bf16 summed in fp32,
+ * of them (t / 128 + sequences + 2) heads <= 2^22.  Products of bf16 summed in fp32,
  * softmax in fp32; the probabilities are rounded to bf16 for the second product,
  * outputs once.  Few, long rows are cut into parts that a second launch joins.
  *   workspace muon_attention_workspace_bytes(op) bytes, 256-byte aligned (may be 0, and

@@ -138,7 +138,7 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 // Sizes and options that both directions of attention have.
 template <class Op>
 bool attention_ok(const Op* op, int32_t zero_bits) {
-  constexpr int64_t max_tokens = int64_t(1) << 30, max_blocks = int64_t(1) << 23;
+  constexpr int64_t max_tokens = int64_t(1) << 30, max_blocks = int64_t(1) << 22;
   if (!op || op->reserved || op->tokens < 0 || op->tokens > max_tokens || op->k_tokens < 0 || op->k_tokens > max_tokens ||
       op->heads < 1 || op->heads > max_blocks || op->kv_heads < 1 || op->heads % op->kv_heads || op->dim < 8 ||
       op->dim > MUON_ATTN_MAX_DIM || op->dim % 8 || !(op->scale > 0.f) || !std::isfinite(op->scale) ||
@@ -444,6 +444,7 @@ int muon_attention_grad(const muon_attention_grad_t* op, void* workspace, size_t
   if (int rc = l.open()) return rc;
   if (int rc = l.poison(workspace, p.bytes)) return rc;
   char* ws = static_cast<char*>(workspace);
+  if (p.one_launch) return l.run("attention gradient", [&](void* st) { return launch_attention_grad(in, st); });
   if (n > 0) {
     if (int rc = l.run("attention gradient, queries", [&](void* st) { return launch_attention_dq(in, p, ws, st); })) return rc;
     if (p.parts_q > 1)

@@ -90,10 +90,12 @@ int launch_attention_join(const muon_attention_t& op, const AttnPlan& p, const c
 // leaves for the one of dk and dv
 struct AttnGradPlan {
   int parts_q, parts_k;
+  bool one_launch;     // of both kernels, without a workspace
   size_t dq_off, dkv_off;
   size_t bytes;
 };
 AttnGradPlan attention_grad_plan(const muon_attention_grad_t& op);
+int launch_attention_grad(const muon_attention_grad_t& op, void* stream);
 int launch_attention_dq(const muon_attention_grad_t& op, const AttnGradPlan& p, char* ws, void* stream);
 int launch_attention_dkv(const muon_attention_grad_t& op, const AttnGradPlan& p, char* ws, void* stream);
 int launch_attention_dq_join(const muon_attention_grad_t& op, const AttnGradPlan& p, const char* ws, void* stream);

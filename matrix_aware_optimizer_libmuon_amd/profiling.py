@@ -45,7 +45,7 @@ SOURCES_OF = {"momentum_norm": _ELEMENTWISE, "normalize_cast": _ELEMENTWISE, "ap
               "act8": _COMMON + _OPS + ("muon_act8.hip",), "norm": _COMMON + _OPS + ("muon_norm.hip",),
               "embed": _COMMON + _OPS + ("muon_embed.hip",),
               "wgrad": _COMMON + _OPS + ("muon_gemm.h", "muon_wgrad.hip"),
-              "attention": _COMMON + _OPS + ("muon_attn.hip",), "losses": _COMMON + _OPS + ("muon_loss.hip",)}
+              "attention": _COMMON + _OPS + ("muon_gemm.h", "muon_attn.hip"), "losses": _COMMON + _OPS + ("muon_loss.hip",)}
 KERNEL_SOURCES = tuple(sorted({f for files in SOURCES_OF.values() for f in files}))
 TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "muon_step_transformer_d4096_hbm_traffic.md")
 MFMA_PROFILE = os.path.join(ROOT, "profiles", "muon_step_transformer_d4096_mfma_util.md")

@@ -271,7 +271,7 @@ BAD_ATTENTION = [
     dict(tokens=-1), dict(tokens=(1 << 30) + 1), dict(k_tokens=-1), dict(heads=0), dict(kv_heads=0), dict(kv_heads=3), dict(dim=0),
     dict(dim=60), dict(dim=136), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(causal=2),
     dict(zero_rest=8), dict(zero_rest=-1), dict(reserved=1), dict(k_starts=1 << 40), dict(starts=1 << 40, sequences=-1),
-    dict(starts=(1 << 40) + 2, sequences=1), dict(starts=1 << 40, sequences=1, k_tokens=39), dict(starts=1 << 40, sequences=1 << 22),
+    dict(starts=(1 << 40) + 2, sequences=1), dict(starts=1 << 40, sequences=1, k_tokens=39), dict(starts=1 << 40, sequences=1 << 21),
     dict(ld_lse=39), dict(lse=(1 << 41) + 1), dict(q=heads(data=0)), dict(k=heads(2, data=0)), dict(v=heads(2, data=(1 << 41) + 1)),
     dict(q=heads(ld_token=0)), dict(q=heads(ld_head=0)), dict(k=heads(2, ld_token=64)), dict(k=heads(2, ld_token=128, ld_head=65)),
     dict(q=heads(ld_token=1 << 60)), dict(q=heads(ld_head=1 << 60)), dict(q=heads(ld_token=-256))]
@@ -297,7 +297,7 @@ def test_attention_refuses(lib):
     # few rows over many keys are cut into parts: o and lse of each in the workspace
     long = dict(k_tokens=4096, causal=0)
     need = lib.muon_attention_workspace_bytes(ctypes.byref(attn(**long)))
-    assert need == 16 * 40 * 4 * (64 + 1) * 4 and lib.muon_attention_workspace_bytes(ctypes.byref(attn())) == 0
+    assert need == 8 * 40 * 4 * (64 + 1) * 4 and lib.muon_attention_workspace_bytes(ctypes.byref(attn())) == 0
     assert lib.muon_attention_workspace_bytes(ctypes.byref(attn(**long, dim=60))) == 0
     assert fwd(ws=None, **long) == EWORKSPACE and fwd(ws_bytes=need - 1, **long) == EWORKSPACE
     assert fwd(ws=ctypes.c_void_p((1 << 42) + 8), **long) == EWORKSPACE and fwd(lse=1 << 42, **long) == EALIAS
@@ -307,11 +307,14 @@ def test_attention_refuses(lib):
 
 def test_attention_gradient_refuses(lib):
     size = lambda **kw: lib.muon_attention_grad_workspace_bytes(ctypes.byref(attn_grad(**kw)))  # noqa: E731
-    need = size()
-    assert need == 2 * 4 * 40 * 4 and size(tokens=0) == 0 and size(dim=60) == 0 and lib.muon_attention_grad_workspace_bytes(None) == 0
-    # lse and rowsum(dout o); parts of dq over many keys; parts of dk and dv over many queries
-    assert size(k_tokens=4096, causal=0) == need + 16 * 40 * 4 * 64 * 4
-    assert size(tokens=4096, causal=0) == 2 * 4 * 4096 * 4 + 2 * 16 * 40 * 2 * 64 * 4
+    long = dict(tokens=9000, k_tokens=9000, ld_lse=9000)
+    need = size(**long)
+    # lse and rowsum(dout o), which few blocks in one launch form for themselves; three parts of dk and dv
+    assert need == 2 * 4 * 9000 * 4 + 2 * 3 * 9000 * 2 * 64 * 4 and size() == 0 and size(**dict(long, dim=60)) == 0
+    assert lib.muon_attention_grad_workspace_bytes(None) == 0
+    # parts of dq over many keys; parts of dk and dv over many queries
+    assert size(k_tokens=4096, causal=0) == 2 * 4 * 40 * 4 + 8 * 40 * 4 * 64 * 4
+    assert size(tokens=4096, ld_lse=4096, causal=0) == 2 * 4 * 4096 * 4 + 2 * 16 * 40 * 2 * 64 * 4
 
     def bwd(ws=WS, ws_bytes=need, **kw):
         return lib.muon_attention_grad(ctypes.byref(attn_grad(**kw)), ws, ws_bytes, None)
@@ -320,9 +323,10 @@ def test_attention_gradient_refuses(lib):
     for bad in [*BAD_ATTENTION, dict(lse=0), dict(dout=heads(data=0)), dict(o=heads(data=0)), dict(dq=heads(data=0)),
                 dict(dk=heads(2, data=0)), dict(dv=heads(2, ld_token=64))]:
         assert bwd(**bad) == EINVAL, bad
-    assert bwd(ws=None) == EWORKSPACE and bwd(ws_bytes=need - 1) == EWORKSPACE and bwd(ws=ctypes.c_void_p((1 << 42) + 8)) == EWORKSPACE
+    assert bwd(ws=None, **long) == EWORKSPACE and bwd(ws_bytes=need - 1, **long) == EWORKSPACE
+    assert bwd(ws=ctypes.c_void_p((1 << 42) + 8), **long) == EWORKSPACE
     p = ptr()
-    assert bwd(dq=heads(data=1 << 42)) == EALIAS and bwd(dk=heads(2, data=p), dv=heads(2, data=p)) == EALIAS
+    assert bwd(dq=heads(data=1 << 42), **long) == EALIAS and bwd(dk=heads(2, data=p), dv=heads(2, data=p)) == EALIAS
     assert bwd(q=heads(data=p), dq=heads(data=p)) == EALIAS and bwd(lse=p, dv=heads(2, data=p)) == EALIAS
     assert bwd(tokens=0, k_tokens=0, ws=None, ws_bytes=0) == 0
 

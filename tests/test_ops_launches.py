@@ -66,14 +66,11 @@ def test_weight_gradient_plans_of_the_tested_sizes():
         (6000, 520, 264): ((128, 128), "none", 16, False)}
 
 
-ATTN_MAX = 1 << 30                                # tokens of attention
-
-
 @pytest.mark.parametrize("entry", ["attention", "attention_grad"])
 @pytest.mark.parametrize("args", [
-    dict(tokens=ATTN_MAX - 128 * 3, k_tokens=ATTN_MAX - 128 * 3, heads_=1, kv=1, dim=64, sequences=0),
-    dict(tokens=1, k_tokens=1, heads_=4, kv=2, dim=128, sequences=(1 << 21) - 2),
-    dict(tokens=1 << 20, k_tokens=(1 << 20) - 5, heads_=512, kv=512, dim=80, sequences=1000),
+    dict(tokens=(1 << 29) - 128 * 3, k_tokens=(1 << 29) - 128 * 3, heads_=1, kv=1, dim=64, sequences=0),
+    dict(tokens=1, k_tokens=1, heads_=4, kv=4, dim=128, sequences=(1 << 20) - 2),
+    dict(tokens=1 << 19, k_tokens=(1 << 19) - 5, heads_=512, kv=512, dim=104, sequences=1000),
 ], ids=lambda v: "x".join(str(x) for x in v.values()))
 def test_the_largest_attention_can_be_launched(entry, args):
     (status, launches), = record([(entry, args)])
@@ -92,13 +89,23 @@ def test_the_largest_losses_can_be_launched(entry, args):
 
 
 def test_attention_kernels_by_columns_and_alignment():
-    args = dict(tokens=300, k_tokens=300, heads_=2, kv=1, sequences=0)
+    few, many = (dict(tokens=n, k_tokens=n, heads_=h, kv=h // 2, sequences=0) for n, h in ((300, 2), (20000, 32)))
     for dim, blocks in ((8, 2), (64, 2), (72, 3), (96, 3), (104, 4), (128, 4)):
         for odd in (False, True):
-            got = record([(e, dict(args, dim=dim, odd=odd)) for e in ("attention", "attention_grad")])
-            names = [kernel for _, launches in got for kernel, _, _ in launches]
             al = "false" if odd else "true"
-            assert names == [f"k_attn<{blocks}, {al}>", f"k_attn_dq<{blocks}, {al}>", f"k_attn_dkv<{blocks}, {al}>"]
+            got = record([(e, dict(args, dim=dim, odd=odd)) for args in (few, many) for e in ("attention", "attention_grad")])
+            names = [[kernel for kernel, _, _ in launches] for _, launches in got]
+            assert names == [[f"k_attn<{blocks}, {al}>"], [f"k_attn_grad<{blocks}, {al}>"],
+                             [f"k_attn<{blocks}, {al}>"], [f"k_attn_dq<{blocks}, {al}>", f"k_attn_dkv<{blocks}, {al}>"]]
+
+
+@pytest.mark.parametrize("heads_,kv,tokens,k_tokens,dim,one", [
+    (4, 4, 74, 74, 64, True), (32, 32, 1024, 1024, 64, True), (32, 32, 1025, 1024, 64, False), (32, 32, 1024, 1025, 64, False),
+    (32, 32, 1024, 1400, 128, True), (4, 4, 0, 74, 64, True), (4, 4, 74, 0, 64, True)])
+def test_few_blocks_of_the_attention_gradient_take_one_launch(heads_, kv, tokens, k_tokens, dim, one):
+    """Up to 512 blocks of 128 queries and 128 (past 96 columns 256) keys together."""
+    (status, launches), = record([("attention_grad", dict(tokens=tokens, k_tokens=k_tokens, heads_=heads_, kv=kv, dim=dim, sequences=0))])
+    assert status == 0 and [k.split("<")[0] for k, _, _ in launches] == (["k_attn_grad"] if one else ["k_attn_dq", "k_attn_dkv"])
 
 
 @pytest.mark.parametrize("layout", ["side by side", "in steps", "one after the other"])
@@ -110,9 +117,10 @@ def test_attention_takes_slices_of_one_buffer(layout):
 
 
 @pytest.mark.parametrize("tokens,k_tokens,heads_,kv,dim,sequences,parts", [
-    (40, 4096, 4, 2, 64, 0, (16, 16, 1)), (1, 5000, 2, 1, 128, 0, (16, 16, 1)), (73, 5509, 2, 2, 80, 3, (7, 7, 1)),
-    (2500, 2500, 1, 1, 64, 0, (9, 9, 9)), (2130, 2130, 4, 1, 128, 2, (4, 4, 16)), (3000, 50, 2, 1, 40, 0, (1, 1, 16)),
-    (1500, 1400, 3, 3, 96, 0, (5, 5, 5)), (16384, 16384, 32, 8, 128, 4, (1, 1, 1)), (74, 74, 4, 4, 64, 2, (1, 1, 1))])
+    (40, 4096, 4, 2, 64, 0, (8, 8, 1)), (1, 5000, 2, 1, 128, 0, (9, 9, 1)), (73, 5509, 2, 2, 80, 3, (3, 3, 1)),
+    (2500, 2500, 1, 1, 64, 0, (4, 4, 4)), (2130, 2130, 4, 1, 128, 2, (2, 2, 8)), (3000, 50, 2, 1, 40, 0, (1, 1, 11)),
+    (1500, 1400, 3, 3, 96, 0, (2, 2, 2)), (64, 1 << 16, 1, 1, 64, 0, (16, 16, 1)), (16384, 16384, 32, 8, 128, 4, (1, 1, 1)),
+    (74, 74, 4, 4, 64, 2, (1, 1))])
 def test_parts_of_attention(tokens, k_tokens, heads_, kv, dim, sequences, parts):
     """How many parts the steps of the tested sizes are cut into: forward, dq, dk and dv; each cut has its join."""
     args = dict(tokens=tokens, k_tokens=k_tokens, heads_=heads_, kv=kv, dim=dim, sequences=sequences, causal=0)
