@@ -546,28 +546,52 @@ __device__ __forceinline__ void dq_tile(const muon_attention_grad_t& op, Blocks 
     if (!(op.causal && k0 > first + 31 + offset) && first < pl.nq) {
       const bool partial = k0 + BN > pl.nk || (op.causal && k0 + BN - 1 > first + offset);
       const int last = op.causal ? min(pl.nk - 1, mine + offset) : pl.nk - 1;
+      // six phases of KS matrix instructions, a fragment of K or V each, read AHEAD of its
+      // use: S, dP of the first 32 keys, S, dP of the others, dQ from both; beside dP the
+      // exponentials, beside the next phase the rest of dS
+      constexpr int KS = G::KS, AHEAD = 3;
+      f32x16_t s[2] = {}, dp[2] = {};
+      bf16x8_t f[6 * KS], sf[4];
+      auto fetch = [&](auto i) __attribute__((always_inline)) {
+        constexpr int phase = decltype(i)::value / KS, n = decltype(i)::value % KS;
+        if constexpr (phase < 4) f[decltype(i)::value] = fr.rows(now + phase % 2 * G::TILE, 32 * (phase / 2), n);
+        else f[decltype(i)::value] = fr.cols(now, 2 * (phase - 4) + n / DB, n % DB);
+      };
+      auto phase = [&](auto ph) __attribute__((always_inline)) {
+        constexpr int P = decltype(ph)::value, kb = P < 4 ? P / 2 : P - 4;
+        static_for<KS>([&](auto nc) __attribute__((always_inline)) {
+          constexpr int n = decltype(nc)::value, at_f = P * KS + n;
+          if constexpr (at_f + AHEAD < 6 * KS) fetch(std::integral_constant<int, at_f + AHEAD>{});
+          if constexpr (P == 0 || P == 2) s[kb] = mfma(f[at_f], qf[n], s[kb]);
+          if constexpr (P == 1 || P == 3) dp[kb] = mfma(f[at_f], gf[n], dp[kb]);
+          if constexpr (P >= 4) dq[n % DB] = mfma(f[at_f], sf[2 * kb + n / DB], dq[n % DB]);
+          if constexpr (P >= 1 && P <= 4) {
+            constexpr int of = P <= 2 ? 0 : 1;
+            static_for<16 * (n + 1) / KS - 16 * n / KS>([&](auto u) __attribute__((always_inline)) {
+              constexpr int i = 16 * n / KS + decltype(u)::value;
+              if constexpr (P % 2) s[of][i] = exp2_fast(s[of][i] * c - base);
+              else s[of][i] *= dp[of][i] - delta;
+              if constexpr (P % 2 == 0 && i % 8 == 7) sf[2 * of + i / 8] = pack8(s[of], i - 7);
+            });
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      auto mask = [&](int kb) __attribute__((always_inline)) {
+        if (!partial) return;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        f32x16_t s{}, dp{};
-#pragma unroll
-        for (int ks = 0; ks < G::KS; ++ks) {
-          s = mfma(fr.rows(now, 32 * kb, ks), qf[ks], s);
-          dp = mfma(fr.rows(now + G::TILE, 32 * kb, ks), gf[ks], dp);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = exp2_fast(s[i] * c - base) * (dp[i] - delta);
-        if (partial) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (k0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 > last) s[i] = 0.f;
-        }
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const bf16x8_t sf = pack8(s, 8 * st);
-#pragma unroll
-          for (int db = 0; db < DB; ++db) dq[db] = mfma(fr.cols(now, 2 * kb + st, db), sf, dq[db]);
-        }
-      }
+        for (int i = 0; i < 16; ++i)
+          if (k0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 > last) s[kb][i] = -kInf;
+      };
+      static_for<AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(i); });
+      phase(std::integral_constant<int, 0>{});
+      mask(0);
+      phase(std::integral_constant<int, 1>{});
+      phase(std::integral_constant<int, 2>{});
+      mask(1);
+      phase(std::integral_constant<int, 3>{});
+      phase(std::integral_constant<int, 4>{});
+      phase(std::integral_constant<int, 5>{});
     }
     block_barrier();
   };
