@@ -425,11 +425,22 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint3
     const int k0 = j * BN;
     // no query of the wave sees the tile
     if (!(op.causal && k0 > first + 31 + offset) && first < pl.nq) {
+      // fragments of K are read AHEAD of their use, the first of V before the softmax
+      constexpr int KS = G::KS, AHEAD = 3, EARLY = DB;
       f32x16_t s[2] = {};
-#pragma unroll
-      for (int ks = 0; ks < G::KS; ++ks)
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) s[kb] = mfma(fr.rows(now, 32 * kb, ks), qf[ks], s[kb]);
+      bf16x8_t f[2 * KS], vf[4 * DB];
+      static_for<AHEAD>([&](auto i) __attribute__((always_inline)) { f[decltype(i)::value] = fr.rows(now, 32 * (decltype(i)::value % 2), decltype(i)::value / 2); });
+      static_for<2 * KS>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value, n = i + AHEAD;
+        if constexpr (n < 2 * KS) f[n] = fr.rows(now, 32 * (n % 2), n / 2);
+        else if constexpr (n - 2 * KS < EARLY) vf[n - 2 * KS] = fr.cols(now + G::TILE, (n - 2 * KS) / DB, (n - 2 * KS) % DB);
+        s[i % 2] = mfma(f[i], qf[i / 2], s[i % 2]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      static_for<EARLY - (AHEAD < EARLY ? AHEAD : EARLY)>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int n = AHEAD + decltype(ic)::value;
+        vf[n] = fr.cols(now + G::TILE, n / DB, n % DB);
+      });
       if (k0 + BN > pl.nk || (op.causal && k0 + BN - 1 > first + offset)) {
         const int last = op.causal ? min(pl.nk - 1, mine + offset) : pl.nk - 1;
 #pragma unroll
@@ -460,12 +471,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint3
           part[i & 3] += s[kb][i];
         }
       sum += (part[0] + part[1]) + (part[2] + part[3]);
+      bf16x8_t pf[4];
 #pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        const bf16x8_t pf = pack8(s[st / 2], 8 * (st % 2));
-#pragma unroll
-        for (int db = 0; db < DB; ++db) o[db] = mfma(fr.cols(now + G::TILE, st, db), pf, o[db]);
-      }
+      for (int st = 0; st < 4; ++st) pf[st] = pack8(s[st / 2], 8 * (st % 2));
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<4 * DB>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value, n = i + EARLY;
+        if constexpr (n < 4 * DB) vf[n] = fr.cols(now + G::TILE, n / DB, n % DB);
+        o[i % DB] = mfma(vf[i], pf[i / DB], o[i % DB]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     }
     block_barrier();
   };
