@@ -613,7 +613,7 @@ typedef struct {
   int64_t        tokens, k_tokens, sequences;
   int64_t        heads, kv_heads, dim;
   int64_t        ld_lse;
-  float          scale;      /* > 0, finite */
+  float          scale;      /* > 0, at most 1e30 */
   int32_t        causal;     /* 0 or 1 */
   int32_t        zero_rest;
   int32_t        reserved;   /* must be 0 */

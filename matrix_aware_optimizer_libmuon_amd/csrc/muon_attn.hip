@@ -313,66 +313,72 @@ struct Place {
 // Unit `unit` of the tiles of OWN queries (KEYS: keys) of all sequences; rows behind the
 // last sequence are one more, without keys (queries), if they are to be written.  Starts
 // are brought into range and order first, so that bad ones cannot lead outside the
-// tensors.  Tiles with the most work under a causal mask, the last queries and the first
-// keys, come first, over all sequences where there are fewer than 64 (4 x 4096 tokens, 8
-// heads: dK and dV 1330 us with each sequence's in turn, BALANCED with this), else sequence
-// by sequence.
+// tensors.
+//
+// Under a causal mask and with fewer than 64 sequences, units are numbered by their work, the
+// most first: the last queries and the first keys of all sequences (backward pass of 4 x
+// 4096 tokens, 32 and 8 heads of 128: 1916 us, 2306 with one sequence after the other).
+// Else tile t of sequence i, which begins at row a, is unit a / OWN + i + t: the numbers
+// rise and none is used twice, so that a search of the starts finds it, 64 at a time.
 template <bool KEYS, int OWN>
 __device__ __forceinline__ Place place_of(const int32_t* starts, const int32_t* k_starts, int64_t sequences, int tokens, int k_tokens,
-                                          bool rest, bool balance, int unit, int lane) {
+                                          bool rest, bool causal, int unit, int lane) {
+  constexpr Place none{0, 0, 0, 0, 0, false, false};
   // the tile with `work` tiles of its sequence at or behind it (KEYS: before it)
   auto tile_of = [](int tiles, int work) { return KEYS ? tiles - work : work - 1; };
+  auto tiles_of = [](int rows) { return (rows + OWN - 1) / OWN; };
   if (!starts) {
-    const int tiles = ((KEYS ? k_tokens : tokens) + OWN - 1) / OWN;
+    const int tiles = tiles_of(KEYS ? k_tokens : tokens);
     return {0, tokens, 0, k_tokens, tile_of(tiles, tiles - unit), unit < tiles, false};
   }
   if (!k_starts) k_starts = starts;
-  for (int64_t base = 0; base <= sequences; base += 64) {
-    const int64_t i = base + lane;
-    int q0 = 0, nq = 0, k0 = 0, nk = 0;
-    if (i <= sequences) {
-      const int64_t next = i < sequences ? i + 1 : i;
-      q0 = min(max(gld<int32_t>(starts + i), 0), tokens);
-      k0 = min(max(gld<int32_t>(k_starts + i), 0), k_tokens);
-      nq = min(max(gld<int32_t>(starts + next), q0), tokens) - q0;
-      nk = min(max(gld<int32_t>(k_starts + next), k0), k_tokens) - k0;
-      if (i == sequences && rest) (KEYS ? nk : nq) = KEYS ? k_tokens - k0 : tokens - q0;
+  auto q_at = [&](int64_t i) { return min(max(gld<int32_t>(starts + i), 0), tokens); };
+  auto k_at = [&](int64_t i) { return min(max(gld<int32_t>(k_starts + i), 0), k_tokens); };
+  auto sequence = [&](int64_t i) {        // its rows; the one behind the last: the rest
+    Place p = none;
+    const int64_t next = i < sequences ? i + 1 : i;
+    p.q0 = q_at(i);
+    p.k0 = k_at(i);
+    p.nq = max(q_at(next) - p.q0, 0);
+    p.nk = max(k_at(next) - p.k0, 0);
+    p.rest = i == sequences;
+    if (p.rest && rest) (KEYS ? p.nk : p.nq) = KEYS ? k_tokens - p.k0 : tokens - p.q0;
+    return p;
+  };
+  if (causal && sequences < 64) {
+    const Place p = lane <= sequences ? sequence(lane) : none;
+    const int tiles = tiles_of(KEYS ? p.nk : p.nq);
+    // the largest `work` of which fewer than unit + 1 tiles have more
+    auto above = [&](int v) { return wave_all(max(tiles - v, 0), [](int x, int y) { return x + y; }); };
+    if (above(0) <= unit) return none;
+    int lo = 0, work = wave_all(tiles, [](int x, int y) { return max(x, y); });     // above(work) == 0 <= unit
+    while (lo + 1 < work) {
+      const int mid = lo + (work - lo) / 2;
+      (above(mid) <= unit ? work : lo) = mid;
     }
-    const int tiles = ((KEYS ? nk : nq) + OWN - 1) / OWN;
-    int f, work;
-    if (balance && sequences < 64) {
-      // the largest `work` of which fewer than unit + 1 tiles have more
-      const auto add = [](int a, int b) { return a + b; };
-      auto above = [&](int v) { return wave_all(max(tiles - v, 0), add); };
-      int lo = 0, hi = wave_all(tiles, [](int a, int b) { return max(a, b); });     // above(hi) == 0 <= unit
-      if (above(0) <= unit) break;
-      while (lo + 1 < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        (above(mid) <= unit ? hi : lo) = mid;
-      }
-      work = hi;
-      uint64_t with = __ballot(tiles >= work);
-      for (int skip = unit - above(work); skip > 0; --skip) with &= with - 1;
-      f = __builtin_ctzll(with);
-    } else {
-      int upto = tiles;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(upto, o, 64);
-        if (lane >= o) upto += v;
-      }
-      const uint64_t past = __ballot(upto > unit);
-      if (!past) {
-        unit -= __builtin_amdgcn_readlane(upto, 63);
-        continue;
-      }
-      f = __builtin_ctzll(past);
-      work = __builtin_amdgcn_readlane(upto, f) - unit;
-    }
+    uint64_t with = __ballot(tiles >= work);
+    for (int skip = unit - above(work); skip > 0; --skip) with &= with - 1;
+    const int f = __builtin_ctzll(with);
     auto of = [&](int v) { return __builtin_amdgcn_readlane(v, f); };
-    return {of(q0), of(nq), of(k0), of(nk), tile_of(of(tiles), work), true, base + f == sequences};
+    return {of(p.q0), of(p.nq), of(p.k0), of(p.nk), tile_of(of(tiles), work), true, f == sequences};
   }
-  return {0, 0, 0, 0, 0, false, false};
+  int64_t at = 0, left = sequences + 1;
+  int first = 0;                            // the number of the sequence's first tile
+  while (true) {
+    const int64_t step = (left + 63) / 64, i = at + lane * step;
+    const int number = lane * step < left ? static_cast<int>((KEYS ? k_at(i) : q_at(i)) / OWN + i) : 0;
+    const uint64_t before = __ballot(lane * step < left && number <= unit);
+    if (!before) return none;
+    const int f = 63 - __builtin_clzll(before);
+    first = __builtin_amdgcn_readlane(number, f);
+    at += f * step;
+    left = min(step, left - f * step);
+    if (step == 1) break;
+  }
+  Place p = sequence(at);
+  p.tile = unit - first;
+  p.found = p.tile < tiles_of(KEYS ? p.nk : p.nq);
+  return p;
 }
 
 // The same in scalar registers, which the compiler does not see through the loop.

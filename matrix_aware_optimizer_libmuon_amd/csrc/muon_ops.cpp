@@ -141,7 +141,7 @@ bool attention_ok(const Op* op, int32_t zero_bits) {
   constexpr int64_t max_tokens = int64_t(1) << 30, max_blocks = int64_t(1) << 22;
   if (!op || op->reserved || op->tokens < 0 || op->tokens > max_tokens || op->k_tokens < 0 || op->k_tokens > max_tokens ||
       op->heads < 1 || op->heads > max_blocks || op->kv_heads < 1 || op->heads % op->kv_heads || op->dim < 8 ||
-      op->dim > MUON_ATTN_MAX_DIM || op->dim % 8 || !(op->scale > 0.f) || !std::isfinite(op->scale) ||
+      op->dim > MUON_ATTN_MAX_DIM || op->dim % 8 || !(op->scale > 0.f) || !(op->scale <= 1e30f) ||
       (op->causal != 0 && op->causal != 1) || (op->zero_rest & ~zero_bits))
     return false;
   if (!op->starts ? op->k_starts != nullptr

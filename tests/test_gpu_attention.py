@@ -165,12 +165,17 @@ def test_queries_over_other_keys(nq, nk, causal):
         q0 += a
 
 
-@pytest.mark.parametrize("count", [63, 64, 65, 200])
-def test_many_sequences(count):
-    lengths = torch.randint(0, 9, (count,), generator=gen(count)).tolist()
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("count", [62, 63, 64, 65, 127, 128, 700, 4097])
+def test_many_sequences(count, causal):
+    """Found by their work or by a search of one, two and three rounds; none of them long, a few long, many empty."""
+    lengths = torch.randint(0, 9 if count < 1000 else 2, (count,), generator=gen(count)).tolist()
+    lengths[count // 3] += 300
     lengths[-1] += 140
     n = sum(lengths)
-    check(*tensors(count, n, n, 2, 1, 32), lengths, lengths, True)
+    check(*tensors(count, n, n, 2, 1, 32), lengths, lengths, causal)
+    keys = torch.randint(0, 4, (count,), generator=gen(count + 1)).tolist()
+    check(*tensors(count, n, sum(keys), 2, 2, 32), lengths, keys, causal)
 
 
 @pytest.mark.parametrize("sharp,scale", [(20.0, None), (1.0, 1e-3), (1.0, 3.0), (0.0, None)])
@@ -285,12 +290,14 @@ def test_starts_out_of_order_or_range_stay_inside():
     """Undefined values, but nothing outside the outputs is written."""
     q, k, v = tensors(13, 100, 100, 2, 1, 64)
     do = torch.randn(q.shape, generator=gen(1)).to(BF).to(DEV)
-    for bad in ([0, 500, 100], [-9, 60, 40, 100], [90, 10, 1 << 30], [0, -5, -7], [-(1 << 31), (1 << 31) - 1]):
+    noise = torch.randint(-150, 250, (500,), generator=gen(2)).tolist()
+    for bad, causal in [(b, c) for c in (True, False) for b in (
+            [0, 500, 100], [-9, 60, 40, 100], [90, 10, 1 << 30], [0, -5, -7], [-(1 << 31), (1 << 31) - 1], noise[:30], noise, noise[::-1])]:
         st = torch.tensor(bad, dtype=torch.int32, device=DEV)
         bufs = [torch.full((t.shape[0] + 200, *t.shape[1:]), 3.0, dtype=BF, device=DEV) for t in (q, q, k, v)]
         outs = [b[100:200] for b in bufs]
-        _, lse = muon.attention(q, k, v, starts=st, out=outs[0])
-        muon.attention_grad(do, q, k, v, outs[0], lse, starts=st, dq=outs[1], dk=outs[2], dv=outs[3])
+        _, lse = muon.attention(q, k, v, starts=st, causal=causal, out=outs[0])
+        muon.attention_grad(do, q, k, v, outs[0], lse, starts=st, causal=causal, dq=outs[1], dk=outs[2], dv=outs[3])
         torch.cuda.synchronize()
         assert all((b[:100] == 3).all() and (b[200:] == 3).all() for b in bufs)
 
