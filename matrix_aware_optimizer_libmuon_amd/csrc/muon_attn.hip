@@ -546,12 +546,18 @@ __device__ __forceinline__ void dq_tile(const muon_attention_grad_t& op, Blocks 
       base = l == -kInf ? kInf : l * kLog2e;
       if (h == 0 && g.part == 0 && stats) {
         gst<float>(stats + head * op.tokens + row, base);
-        gst<float>(stats + (op.heads + head) * op.tokens + row, delta);
+        gst<float>(stats + (op.heads + head) * op.tokens + row, -delta);
       }
     }
     own_rows<DB>(op.q, pl.q0, mine, pl.nq, head, dim, h, qf);
   }
   const Frags<DB> fr(lane);
+  // dP's sums begin with -delta, where registers hold that many copies of it
+  constexpr bool LESS = DB < 4;
+  f32x16_t less{};
+  if constexpr (LESS)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) less[i] = -delta;
   f32x16_t dq[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) dq[db] = f32x16_t{};
@@ -571,7 +577,7 @@ __device__ __forceinline__ void dq_tile(const muon_attention_grad_t& op, Blocks 
       // use: S, dP of the first 32 keys, S, dP of the others, dQ from both; beside dP the
       // exponentials, beside the next phase the rest of dS
       constexpr int KS = G::KS, AHEAD = 3;
-      f32x16_t s[2] = {}, dp[2] = {};
+      f32x16_t s[2] = {}, dp[2] = {less, less};
       bf16x8_t f[6 * KS], sf[4];
       auto fetch = [&](auto i) __attribute__((always_inline)) {
         constexpr int phase = decltype(i)::value / KS, n = decltype(i)::value % KS;
@@ -591,6 +597,7 @@ __device__ __forceinline__ void dq_tile(const muon_attention_grad_t& op, Blocks 
             static_for<16 * (n + 1) / KS - 16 * n / KS>([&](auto u) __attribute__((always_inline)) {
               constexpr int i = 16 * n / KS + decltype(u)::value;
               if constexpr (P % 2) s[of][i] = exp2_fast(s[of][i] * c - base);
+              else if constexpr (LESS) s[of][i] *= dp[of][i];
               else s[of][i] *= dp[of][i] - delta;
               if constexpr (P % 2 == 0 && i % 8 == 7) sf[2 * of + i / 8] = pack8(s[of], i - 7);
             });
@@ -740,7 +747,7 @@ __device__ __forceinline__ void dkv_tile(const muon_attention_grad_t& op, Blocks
           if ((tid & 3) == 0) {
             float* stat = reinterpret_cast<float*>(to + 2 * G::TILE);
             stat[r] = l;
-            stat[BN + r] = sum;
+            stat[BN + r] = -sum;
           }
         }
       } else if (w < 2 && left > 0)
@@ -753,9 +760,9 @@ __device__ __forceinline__ void dkv_tile(const muon_attention_grad_t& op, Blocks
         const int q0 = j * BN + 32 * qb;
         // none of the queries sees a key of the wave, or there are none
         if ((op.causal && q0 + 31 + offset < first) || q0 >= pl.nq || first >= pl.nk) continue;
-        f32x16_t s[KB] = {}, dp[KB] = {};
+        f32x16_t s[KB] = {}, dp[KB];
         bf16x8_t f[4 * KS], vl[V_LDS ? KB : 1][KS], pf[KB][2], xf[KB][2];
-        f32x4_t l[4], d[4];
+        f32x4_t l[4];
         auto fetch = [&](auto i) __attribute__((always_inline)) {
           constexpr int phase = decltype(i)::value / KS, n = decltype(i)::value % KS;
           if constexpr (phase == 1 && V_LDS)
@@ -763,24 +770,31 @@ __device__ __forceinline__ void dkv_tile(const muon_attention_grad_t& op, Blocks
           if constexpr (phase < 2) f[decltype(i)::value] = fr.rows(now + phase * G::TILE, 32 * qb, n);
           else f[decltype(i)::value] = fr.cols(now + (3 - phase) * G::TILE, 2 * qb + n / DB, n % DB);
         };
-        // four rows' lse or delta, before their first use
-        auto fetch_rows = [&](f32x4_t (&to)[4], int which, int g) __attribute__((always_inline)) {
-          to[g] = *reinterpret_cast<const f32x4_t*>(now + 2 * G::TILE + which * BN * 4 + (32 * qb + 8 * g + 4 * h) * 4);
+        // four rows' lse or -delta, before their first use; dP's sums begin with the latter
+        auto stat = [&](int which, int g) __attribute__((always_inline)) {
+          return *reinterpret_cast<const f32x4_t*>(now + 2 * G::TILE + which * BN * 4 + (32 * qb + 8 * g + 4 * h) * 4);
         };
         // the j-th value of P (then of dS): four queries of each key block in turn
         auto element = [&](auto second, auto jc) __attribute__((always_inline)) {
           constexpr int jj = decltype(jc)::value, g = jj / (4 * KB), kb = jj / 4 % KB, e = jj % 4, i = 4 * g + e;
           if constexpr (!decltype(second)::value) s[kb][i] = exp2_fast(s[kb][i] * c - l[g][e]);
-          else dp[kb][i] = s[kb][i] * (dp[kb][i] - d[g][e]);
+          else dp[kb][i] *= s[kb][i];
           if constexpr (e == 3 && (g & 1)) (decltype(second)::value ? xf : pf)[kb][g / 2] = pack8(decltype(second)::value ? dp[kb] : s[kb], 8 * (g / 2));
-          if constexpr (e == 3 && kb == KB - 1 && g < 3) fetch_rows(decltype(second)::value ? d : l, decltype(second)::value, g + 1);
+          if constexpr (!decltype(second)::value && e == 3 && kb == KB - 1 && g < 3) l[g + 1] = stat(0, g + 1);
         };
         auto phase = [&](auto ph) __attribute__((always_inline)) {
           constexpr int P = decltype(ph)::value;
           static_for<KS>([&](auto nc) __attribute__((always_inline)) {
             constexpr int n = decltype(nc)::value, at_f = P * KS + n;
             if constexpr (at_f + AHEAD < 4 * KS) fetch(std::integral_constant<int, at_f + AHEAD>{});
-            if constexpr (n == KS - 2 && P < 2) fetch_rows(P ? d : l, P, 0);
+            if constexpr (P == 0 && n == KS - 2) l[0] = stat(0, 0);
+            if constexpr (P == 0 && n >= KS - 4) {
+              const f32x4_t d = stat(1, n - KS + 4);
+#pragma unroll
+              for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dp[kb][4 * (n - KS + 4) + e] = d[e];
+            }
             static_for<KB>([&](auto kc) __attribute__((always_inline)) {
               constexpr int kb = decltype(kc)::value, slot = n * KB + kb;
               if constexpr (P == 0) s[kb] = mfma(f[at_f], kf[kb][n], s[kb]);
