@@ -7,6 +7,17 @@
 // products instead of five, but no sums across blocks, so no atomics, and the same
 // bits every time.
 //
+// Rounded to bf16: P and dS as operands of the second products, whose sums are fp32 (half
+// a step, 2^-8, of each term, as the inputs have), and the outputs, once.
+//
+// 4 x 4096 tokens, 32 heads of 128 over 8 of K and V, causal: forward 553 to 589 us (930
+// to 990 TFLOP/s), backward 1720 to 1790 (770 to 800, five products counted; dQ 732 and dK,
+// dV 947); 8192 tokens of 16 heads without a mask 1052 and 858; heads of 64: 896 and 779.
+// A library product of 8192^3 reaches 1309 to 1391.  Bound by the matrix units, the
+// exponentials (a quarter of other instructions' rate; at 64 columns vector instructions
+// take as long as matrix ones) and power: 49 to 57 % of the cycles with a matrix
+// instruction, at 1.7 to 1.9 GHz.  No LDS conflicts.
+//
 // Layout.  A wave owns 32 queries (or keys), one per lane and half: it forms the
 // transposed product S^T = K Q^T with v_mfma_f32_32x32x16_bf16, whose result leaves
 // lane l with 16 of 32 keys of query l & 31.  A row's maximum and sum are then one
@@ -23,7 +34,6 @@
 // while the tile before is in work.  Rows past a sequence's end and columns past dim
 // are zeros there, so that nothing of a neighbour reaches a sum.
 #include <algorithm>
-
 #include <type_traits>
 
 #include "muon_act8.h"
@@ -390,9 +400,12 @@ __device__ __forceinline__ Place locate(Args... args) {
 }
 
 // ------------------------------------------------------------- forward pass ----
-// Rescaling is put off while no row's maximum has grown by more than 2^kSlack since the
-// last one: P then reaches 2^kSlack at most, which costs no precision, and the sums are
-// multiplied in few of the tiles instead of all.
+// The running maximum and sum are fp32, one row a lane.  Rescaling is put off while no
+// row's maximum has grown by more than 2^kSlack since the last one: P then reaches 2^kSlack
+// at most, which costs no precision, and the sums are multiplied in few of the tiles
+// instead of all.  The first load of the loop has to find nothing of the compiler's in
+// flight (`arrived`): with Q's loads pending it waited for the next tile in each step (659
+// us instead of 594 for the case above).
 constexpr float kSlack = 8.f;
 
 template <int DB, bool ALIGNED>
@@ -511,8 +524,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint3
 
 // ------------------------------------------------------------ backward: dQ ----
 // As the forward pass, with both S^T = K Q^T and dP^T = V dO^T; the row's lse and
-// rowsum(dO O) are one value a lane, left for the other kernel (rows x 2: lse in
-// powers of two, +inf where the row sees nothing, so that its P is 0).
+// rowsum(dO O) are one value a lane, left for the other kernel (lse in powers of two, +inf
+// where the row sees nothing, so that its P is 0; the sum negated, as dP begins with it).
 template <int DB, bool ALIGNED>
 __device__ __forceinline__ void dq_tile(const muon_attention_grad_t& op, Blocks g, float* stats, float* part_dq, char* smem) {
   using G = Geo<DB>;
@@ -651,16 +664,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(muon_attention_grad_t o
 //
 // The four products of a step are four phases of KS fragments of Q or dO, in a fixed
 // order: a fragment is read AHEAD of its use, the exponentials of P are spread over the
-// instructions of dP, those of dS over the ones of dV.  Sums, K and V of 128 columns are
-// more than a wave's 256 registers hold beside that: V then waits in LDS, 8 waves to a
-// block, so that two of them still share a SIMD.
+// instructions of dP, the products of dS over the ones of dV (1791 -> 1075 us for the case
+// above; left to the compiler, each matrix instruction waited for its own read).  Sums, K
+// and V of 128 columns are more than a wave's 256 registers hold beside that: V then waits
+// in LDS, 8 waves to a block, so that two of them still share a SIMD.  (64 keys a wave, one
+// wave to a SIMD, spilled: the compiler moves accumulators between the register files.)
 template <int DB>
 constexpr int kKeyWaves = DB == 4 ? 8 : 4;
 
 template <int DB>
 struct KeyLds {
   using G = Geo<DB>;
-  static constexpr int STAGE = 2 * G::TILE + 2 * BN * 4;       // Q, dO, lse, delta
+  static constexpr int STAGE = 2 * G::TILE + 2 * BN * 4;       // Q, dO, lse, -rowsum(dO O)
   static constexpr bool V = DB == 4;                           // the registers hold K alone
   static constexpr int bytes = 2 * STAGE + (V ? 32 * kKeyWaves<DB> * G::ROWB : 0);
 };
