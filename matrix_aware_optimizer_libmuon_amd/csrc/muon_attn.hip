@@ -58,14 +58,16 @@ constexpr int64_t kMaxParts = 16;  // of a block's steps
 template <int DB>
 struct Geo {
   static constexpr int KS = 2 * DB;                       // 16-column steps
-  static constexpr int COLS = DB <= 2 ? 64 : 128;         // columns of a row in LDS
+  static constexpr int COLS = 32 * DB;                    // columns of a row in LDS
   static constexpr int ROWB = COLS * 2, CPR = COLS / 8;   // its bytes and chunks
   static constexpr int TILE = BN * ROWB;
 };
 
+// What the index of a chunk of row `row` is XORed with.  Rows of 192 bytes are a quarter of
+// the banks apart by themselves.
 template <int COLS>
 __device__ __forceinline__ int swz(int row) {
-  return COLS == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+  return COLS == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : COLS == 96 ? (row >> 2) & 3 : ((row & 2) << 1) | ((row >> 2) & 3);
 }
 
 __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
@@ -144,11 +146,10 @@ struct Feed {
       : p(static_cast<const uint16_t*>(t.data) + row0 * t.ld_token + head * t.ld_head), ld(t.ld_token), rows(nrows), dim(dim_), tid(tid_) {
     w = uniform(tid >> 6);
     if constexpr (ALIGNED) {
-      const int lane = tid & 63, rr = lane / G::CPR, pos = lane % G::CPR;
 #pragma unroll
       for (int q = 0; q < LOADS; ++q) {
-        const int c = pos ^ swz<G::COLS>((w * LOADS + q) * (64 / G::CPR) + rr);
-        voff[q] = c * 8 < dim ? static_cast<uint32_t>(rr * ld * 2 + c * 16) : 0x80000000u;   // past every end
+        const int at = (w * LOADS + q) * 64 + (tid & 63), r = at / G::CPR, c = (at % G::CPR) ^ swz<G::COLS>(r);
+        voff[q] = c * 8 < dim ? static_cast<uint32_t>(r * ld * 2 + c * 16) : 0x80000000u;   // past every end
       }
     }
   }
@@ -162,8 +163,7 @@ struct Feed {
       const uint32_t to = lds_at(dst);
 #pragma unroll
       for (int q = 0; q < LOADS; ++q) {
-        const int b = w * LOADS + q;
-        dma<16>(srd, voff[q], b * (64 / G::CPR) * ldb, to + b * 1024);
+        dma<16>(srd, voff[q], 0, to + (w * LOADS + q) * 1024);
       }
     } else {
 #pragma unroll 1
@@ -198,14 +198,17 @@ struct Frags {
     t0 = row * G::ROWB + ((c ^ swz<G::COLS>(row)) << 4) + (j & 1) * 8;
   }
   __device__ __forceinline__ bf16x8_t rows(const char* tile, int rb, int ks) const {
-    return *reinterpret_cast<const bf16x8_t*>(tile + rb * G::ROWB + flip(r0, ks << 5));
+    // (rows of 192 bytes: only the two low bits of a chunk change)
+    constexpr bool low = G::COLS == 96;
+    return *reinterpret_cast<const bf16x8_t*>(tile + rb * G::ROWB + (low ? (ks >> 1) * 64 : 0) + flip(r0, (low ? ks & 1 : ks) << 5));
   }
   __device__ __forceinline__ bf16x8_t cols(const char* tile, int s, int db) const {
     // 8 rows on, bit 1 of the swizzle is set
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)(tile + s * 16 * G::ROWB + flip(t0, db << 6)));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)(tile + (s * 16 + 8) * G::ROWB + flip(t0, (db << 6) ^ 32)));
+    constexpr bool low = G::COLS == 96;
+    const char* at = tile + s * 16 * G::ROWB + (low ? db * 64 : 0);
+    const int bits = low ? 0 : db << 6;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + flip(t0, bits)));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * G::ROWB + flip(t0, bits ^ 32)));
     return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 };
@@ -409,7 +412,7 @@ __device__ __forceinline__ Place locate(Args... args) {
 constexpr float kSlack = 8.f;
 
 template <int DB, bool ALIGNED>
-__global__ __launch_bounds__(kThreads, 2) void k_attn(muon_attention_t op, uint32_t units, float* part_o, float* part_lse) {
+__global__ __launch_bounds__(kThreads, DB == 3 ? 3 : 2) void k_attn(muon_attention_t op, uint32_t units, float* part_o, float* part_lse) {
   using G = Geo<DB>;
   __shared__ __attribute__((aligned(256))) char smem[4 * G::TILE];      // K, V; K, V of the next tile
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
