@@ -4,12 +4,12 @@
 // Both need, of a token's row x = z / temperature, the softmax's maximum and sum
 // and a few single entries, and their gradient is
 //   dz = a softmax(x)  plus a value at each of those few entries.
-// A block takes a row.  Up to 131072 columns in bf16 and 65536 in fp32 the row stays in
+// A block takes a row, or, of few long ones, its share of a row's gradient.  Up to 131072 columns in bf16 and 65536 in fp32 the row stays in
 // registers, so the logits are read once and the gradient written once; a longer row is
 // read again for the gradient (from the caches, which hold the rows in work).  Bound by
 // memory: distillation 16384 x 32000 bf16 405 us (4.9 TB/s), policy loss with 30 % of the
 // rows masked 331 us (5.4); a large copy runs at 4.8.  A single row is bound by one CU's
-// exponentials, a quarter of the rate of other instructions, twice 32000 of them in 8 us.
+// exponentials, a quarter of the rate of other instructions, 32000 of them twice in 9 us.
 //
 // Numbers.  x - max is taken before the factor log2(e) / temperature, so that rows
 // of the type's lowest value stay finite; sums run in fp32, up to 128 terms a
@@ -151,7 +151,7 @@ __device__ __forceinline__ void put_scaled(T* out, int n, Vec8<T>& x, float base
 // t + j step the j-th of thread t.  All but the last lie inside the row (which has
 // (VPL - 1)^2 + VPL vectors at least), so that one scalar address and one offset a lane
 // do for them and only the last goes by its length.
-template <class T, int RT, int VPL>
+template <class T, int RT, int VPL, bool SHARED>
 struct Row {
   const T* p;
   int cols, t, step;
@@ -176,21 +176,27 @@ struct Row {
     const float m = wave_max(top_of(x));
     return {m, sum_of(x, base_of(m), k)};
   }
-  // out[c] = a 2^((x[c] - base) k)
+  // whether the block writes the vectors j of its row (uniform)
+  static __device__ __forceinline__ bool mine(int j) {
+    return !SHARED || static_cast<uint32_t>(j) * gridDim.y / VPL == blockIdx.y;
+  }
+  // out[c] = a 2^((x[c] - base) k), the block's share of it
   __device__ __forceinline__ void scaled(T* out, float base, float k, float a) {
     if (t >= step) return;
 #pragma unroll
-    for (int j = 0; j < VPL - 1; ++j) put_scaled(out + j * step * 8 + static_cast<uint32_t>(t * 8), 8, x[j], base, k, a);
-    put_scaled(out + last(), cols - last(), x[VPL - 1], base, k, a);
+    for (int j = 0; j < VPL - 1; ++j)
+      if (mine(j)) put_scaled(out + j * step * 8 + static_cast<uint32_t>(t * 8), 8, x[j], base, k, a);
+    if (mine(VPL - 1)) put_scaled(out + last(), cols - last(), x[VPL - 1], base, k, a);
   }
-  // whether this thread has written column c
-  __device__ __forceinline__ bool wrote(int c) const { return (c >> 3) % step == t; }
+  // whether this block, and of it this thread, has written column c
+  __device__ __forceinline__ bool has(int c) const { return mine((c >> 3) / step); }
+  __device__ __forceinline__ bool wrote(int c) const { return has(c) && (c >> 3) % step == t; }
 };
 
 // A row of any length, read twice: kPass vectors a thread at a time, then single ones.
 constexpr int kPass = 4;
-template <class T, int RT>
-struct Row<T, RT, 0> {
+template <class T, int RT, bool SHARED>
+struct Row<T, RT, 0, SHARED> {
   const T* p;
   int cols, t;
   Vec8<T> x[kPass];
@@ -222,22 +228,28 @@ struct Row<T, RT, 0> {
     }
     return a;
   }
+  // (passes are dealt to the row's blocks in turn)
+  static constexpr int kSpan = kPass * RT * 8;
+  __device__ __forceinline__ bool has(int c) const {
+    return !SHARED || static_cast<uint32_t>(c / kSpan) % gridDim.y == blockIdx.y;
+  }
   __device__ __forceinline__ void scaled(T* out, float base, float k, float a) {
     int at = 0;
-    for (; at + kPass * RT * 8 <= cols; at += kPass * RT * 8) {
+    for (; at + kSpan <= cols; at += kSpan) {
+      if (!has(at)) continue;
       load(at);
 #pragma unroll
       for (int j = 0; j < kPass; ++j) put_scaled(out + at + j * RT * 8 + static_cast<uint32_t>(t * 8), 8, x[j], base, k, a);
     }
 #pragma unroll 1
-    for (; at < cols; at += RT * 8) {
+    for (; at < cols && has(at); at += RT * 8) {
       const int c = at + t * 8;
       Vec8<T> v;
       load8(v, p + c, c, cols - c);
       put_scaled(out + c, cols - c, v, base, k, a);
     }
   }
-  __device__ __forceinline__ bool wrote(int c) const { return (c >> 3) % RT == t; }
+  __device__ __forceinline__ bool wrote(int c) const { return has(c) && (c >> 3) % RT == t; }
 };
 
 // Waves a SIMD, by the registers that the row takes of the 64, 80 or 128 they leave (16384
@@ -259,13 +271,13 @@ __device__ __forceinline__ void zero_row(T* out, int cols, int t) {
 // all others and then once more, behind a barrier, by the thread that has the entry:
 // softmax minus the sum of p over the entries of the same id, in their order (so
 // threads of one id write the same value).
-template <class T, int RT, int VPL>
+template <class T, int RT, int VPL, bool SHARED>
 __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_distill(muon_distill_t op) {
   constexpr int top_max = MUON_DISTILL_MAX_TOP;
   __shared__ Shared<RT> sh;
   __shared__ __attribute__((aligned(16))) int id[top_max];
   __shared__ __attribute__((aligned(16))) float pt[top_max];   // teacher logits, then p
-  const int t = static_cast<int>(threadIdx.x), wave = t >> 6, top = static_cast<int>(op.top);
+  const int t = static_cast<int>(threadIdx.x), wave = t >> 6, share = SHARED ? blockIdx.y : 0, top = static_cast<int>(op.top);
   const int padded = (top + 3) & ~3;
   const float k = kLog2e / op.temperature;
   for (int64_t row = blockIdx.x; row < op.tokens; row += gridDim.x) {
@@ -273,11 +285,11 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_distill(muon_dist
     T* out = op.dlogits ? static_cast<T*>(op.dlogits) + row * op.ld_dlogits : nullptr;
     const float weight = op.weights ? gld<float>(op.weights + row) : 1.f;
     if (weight == 0.f) {
-      if (out) zero_row<T, RT>(out, static_cast<int>(op.vocab), t);
-      if (t == 0) gst<float>(op.loss + row, 0.f);
+      if (out && share == 0) zero_row<T, RT>(out, static_cast<int>(op.vocab), t);
+      if (t == 0 && share == 0) gst<float>(op.loss + row, 0.f);
       continue;
     }
-    Row<T, RT, VPL> x(p, static_cast<int>(op.vocab), t);
+    Row<T, RT, VPL, SHARED> x(p, static_cast<int>(op.vocab), t);
     x.fetch();
     Soft teach{kNegInf, 0.f};
     for (int e = t; e < padded; e += RT) {
@@ -326,11 +338,14 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_distill(muon_dist
     if ((t & 63) == 0) sh.part[wave] = part;
     const float a = weight * op.temperature;
     if (out) {
-      if (none) zero_row<T, RT>(out, x.cols, t);
-      else x.scaled(out, base, k, a / q.s);
+      if (none) {
+        if (share == 0) zero_row<T, RT>(out, x.cols, t);
+      } else {
+        x.scaled(out, base, k, a / q.s);
+      }
     }
     __syncthreads();
-    if (t == 0) {
+    if (t == 0 && share == 0) {
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < RT / 64; ++w) sum += sh.part[w];
@@ -339,7 +354,7 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_distill(muon_dist
     if (out && !none)
       for (int e = t; e < top; e += RT) {
         const int i = id[e];
-        if (i < 0) continue;
+        if (i < 0 || !x.has(i)) continue;
         float sum = 0.f;
         for (int f = 0; f < padded; f += 4) {
           const int4 ids = *reinterpret_cast<const int4*>(id + f);
@@ -362,10 +377,10 @@ __device__ __forceinline__ float exp_less_linear(float d) {
   return d * d * (0.5f + d * (1.f / 6 + d * (1.f / 24 + d * (1.f / 120 + d * (1.f / 720 + d * (1.f / 5040))))));
 }
 
-template <class T, int RT, int VPL>
+template <class T, int RT, int VPL, bool SHARED>
 __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_policy(muon_policy_t op) {
   __shared__ Shared<RT> sh;
-  const int t = static_cast<int>(threadIdx.x), wave = t >> 6;
+  const int t = static_cast<int>(threadIdx.x), wave = t >> 6, share = SHARED ? blockIdx.y : 0;
   const float k = kLog2e / op.temperature;
   for (int64_t row = blockIdx.x; row < op.tokens; row += gridDim.x) {
     const T* p = static_cast<const T*>(op.logits) + row * op.ld_logits;
@@ -373,14 +388,14 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_policy(muon_polic
     const float weight = op.weights ? gld<float>(op.weights + row) : 1.f;
     const int64_t act = id_at(op.actions, row, op.id_bytes);
     if (weight == 0.f || act < 0 || act >= op.vocab) {
-      if (out) zero_row<T, RT>(out, static_cast<int>(op.vocab), t);
-      if (t == 0) {
+      if (out && share == 0) zero_row<T, RT>(out, static_cast<int>(op.vocab), t);
+      if (t == 0 && share == 0) {
         gst<float>(op.loss + row, 0.f);
         if (op.logp) gst<float>(op.logp + row, 0.f);
       }
       continue;
     }
-    Row<T, RT, VPL> x(p, static_cast<int>(op.vocab), t);
+    Row<T, RT, VPL, SHARED> x(p, static_cast<int>(op.vocab), t);
     x.fetch();
     const float xa = value_at(p + act), adv = gld<float>(op.advantages + row), old = gld<float>(op.old_logp + row),
                 ref = op.ref_logp ? gld<float>(op.ref_logp + row) : 0.f;
@@ -404,7 +419,7 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_policy(muon_polic
       loss += op.kl_coef * exp_less_linear(d);
       slope -= op.kl_coef * expm1f(d);
     }
-    if (t == 0) {
+    if (t == 0 && share == 0) {
       gst<float>(op.loss + row, weight * loss);
       if (op.logp) gst<float>(op.logp + row, logp);
     }
@@ -457,6 +472,19 @@ constexpr int64_t kMaxGrid = int64_t(1) << 21;   // threads of a grid stay below
 
 unsigned rows_grid(int64_t tokens) { return static_cast<unsigned>(tokens < kMaxGrid ? tokens : kMaxGrid); }
 
+// Blocks of a long row: where the chip has more CUs than there are rows, several take the
+// same one, each with statistics of its own, and share the writing of its gradient (and
+// the second exponentials): no exchange between them, and the same bits.  One row of
+// 200000 columns in bf16 27 -> 18 us, of 131072 18 -> 12, 128 of them 24 -> 22, one of
+// 32000 9 with and without; many rows would pay 1 to 2 % for the choice, so it is a
+// kernel of its own.
+constexpr bool shares(int rt, int vpl) { return rt == 1024 && (vpl == 0 || vpl >= 8); }
+unsigned share_of(int64_t rows, int vpl, bool gradient) {
+  unsigned share = 1;
+  while (gradient && 2 * share <= static_cast<unsigned>(vpl ? vpl : 8) && rows * 2 * share <= 256) share *= 2;
+  return share;
+}
+
 }  // namespace
 
 int launch_distill(const muon_distill_t& op, void* stream) {
@@ -464,7 +492,11 @@ int launch_distill(const muon_distill_t& op, void* stream) {
     using T = decltype(type);
     return by_shape<T>(op.tokens, op.vocab, [&](auto rt, auto vpl) {
       constexpr int RT = decltype(rt)::value, VPL = decltype(vpl)::value;
-      hipLaunchKernelGGL((k_distill<T, RT, VPL>), dim3(rows_grid(op.tokens)), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
+      const unsigned share = shares(RT, VPL) ? share_of(op.tokens, VPL, op.dlogits != nullptr) : 1;
+      if (share > 1)
+        hipLaunchKernelGGL((k_distill<T, RT, VPL, shares(RT, VPL)>), dim3(rows_grid(op.tokens), share), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
+      else
+        hipLaunchKernelGGL((k_distill<T, RT, VPL, false>), dim3(rows_grid(op.tokens)), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
       return static_cast<int>(hipGetLastError());
     });
   };
@@ -476,7 +508,11 @@ int launch_policy(const muon_policy_t& op, void* stream) {
     using T = decltype(type);
     return by_shape<T>(op.tokens, op.vocab, [&](auto rt, auto vpl) {
       constexpr int RT = decltype(rt)::value, VPL = decltype(vpl)::value;
-      hipLaunchKernelGGL((k_policy<T, RT, VPL>), dim3(rows_grid(op.tokens)), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
+      const unsigned share = shares(RT, VPL) ? share_of(op.tokens, VPL, op.dlogits != nullptr) : 1;
+      if (share > 1)
+        hipLaunchKernelGGL((k_policy<T, RT, VPL, shares(RT, VPL)>), dim3(rows_grid(op.tokens), share), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
+      else
+        hipLaunchKernelGGL((k_policy<T, RT, VPL, false>), dim3(rows_grid(op.tokens)), dim3(RT), 0, static_cast<hipStream_t>(stream), op);
       return static_cast<int>(hipGetLastError());
     });
   };

@@ -132,3 +132,15 @@ def test_parts_of_attention(tokens, k_tokens, heads_, kv, dim, sequences, parts)
         else:
             got.append(grid[1])
     assert tuple(got) == parts and joins == sum(p > 1 for p in parts)
+
+
+@pytest.mark.parametrize("entry", ["distill", "policy"])
+@pytest.mark.parametrize("tokens,vocab,dtype,share", [
+    (1, 32000, "bf16", 1), (1, 32769, "bf16", 8), (1, 131072, "bf16", 16), (1, 200000, "bf16", 8), (1, 65536, "f32", 8), (1, 65537, "f32", 8),
+    (16, 131072, "bf16", 16), (17, 131072, "bf16", 8), (128, 131072, "bf16", 2), (129, 131072, "bf16", 1), (128, 65536, "bf16", 2),
+    (1, 16384, "bf16", 1)])
+def test_blocks_that_share_a_long_row_of_few(entry, tokens, vocab, dtype, share):
+    """A power of two of them, no more than the row has vectors a thread, and rows times blocks up to 256."""
+    (status, ((kernel, grid, _),)), = record([(entry, dict(tokens=tokens, vocab=vocab, dtype=dtype))])
+    assert status == 0 and kernel.endswith(f", {'true' if share > 1 else 'false'}>")
+    assert grid == (tokens, share, 1)
