@@ -52,7 +52,7 @@ constexpr float kInf = __builtin_inff();
 constexpr int BN = 64;             // rows of a staged tile
 constexpr int BM = 128;            // rows that a block owns, 32 a wave
 constexpr int kThreads = 256;
-constexpr int64_t kMaxParts = 16;  // of a block's steps
+constexpr int64_t kMaxParts = 16, kMaxForwardParts = 64;  // of a block's steps
 
 // DB blocks of 32 columns are computed: dim up to 64, 96 or 128.
 template <int DB>
@@ -323,8 +323,9 @@ struct Place {
   bool rest;            // rows behind the last sequence
 };
 
-// Unit `unit` of the tiles of OWN queries (KEYS: keys) of all sequences; rows behind the
-// last sequence are one more, without keys (queries), if they are to be written.  Starts
+// Unit `unit` of the tiles of OWN queries (KEYS: keys) of all sequences, a query counted as
+// `each` rows; those behind the last sequence are one more, without keys (queries), if they
+// are to be written.  Starts
 // are brought into range and order first, so that bad ones cannot lead outside the
 // tensors.
 //
@@ -335,17 +336,17 @@ struct Place {
 // rise and none is used twice, so that a search of the starts finds it, 64 at a time.
 template <bool KEYS, int OWN>
 __device__ __forceinline__ Place place_of(const int32_t* starts, const int32_t* k_starts, int64_t sequences, int tokens, int k_tokens,
-                                          bool rest, bool causal, int unit, int lane) {
+                                          bool rest, bool causal, int unit, int lane, int each = 1) {
   constexpr Place none{0, 0, 0, 0, 0, false, false};
   // the tile with `work` tiles of its sequence at or behind it (KEYS: before it)
   auto tile_of = [](int tiles, int work) { return KEYS ? tiles - work : work - 1; };
   auto tiles_of = [](int rows) { return (rows + OWN - 1) / OWN; };
   if (!starts) {
-    const int tiles = tiles_of(KEYS ? k_tokens : tokens);
-    return {0, tokens, 0, k_tokens, tile_of(tiles, tiles - unit), unit < tiles, false};
+    const int tiles = tiles_of(KEYS ? k_tokens : tokens * each);
+    return {0, tokens * each, 0, k_tokens, tile_of(tiles, tiles - unit), unit < tiles, false};
   }
   if (!k_starts) k_starts = starts;
-  auto q_at = [&](int64_t i) { return min(max(gld<int32_t>(starts + i), 0), tokens); };
+  auto q_at = [&](int64_t i) { return min(max(gld<int32_t>(starts + i), 0), tokens) * each; };
   auto k_at = [&](int64_t i) { return min(max(gld<int32_t>(k_starts + i), 0), k_tokens); };
   auto sequence = [&](int64_t i) {        // its rows; the one behind the last: the rest
     Place p = none;
@@ -355,7 +356,7 @@ __device__ __forceinline__ Place place_of(const int32_t* starts, const int32_t* 
     p.nq = max(q_at(next) - p.q0, 0);
     p.nk = max(k_at(next) - p.k0, 0);
     p.rest = i == sequences;
-    if (p.rest && rest) (KEYS ? p.nk : p.nq) = KEYS ? k_tokens - p.k0 : tokens - p.q0;
+    if (p.rest && rest) (KEYS ? p.nk : p.nq) = KEYS ? k_tokens - p.k0 : tokens * each - p.q0;
     return p;
   };
   if (causal && sequences < 64) {
@@ -411,23 +412,35 @@ __device__ __forceinline__ Place locate(Args... args) {
 // us instead of 594 for the case above).
 constexpr float kSlack = 8.f;
 
-template <int DB, bool ALIGNED>
+//
+// PACKED: a tile's rows are the queries of all heads that share a key and value head, one
+// query after the other (row i: query i / group), so that few queries a sequence read their
+// keys and values once, and a tile spans fewer queries, which a causal mask cuts closer (us
+// with and without: 32 single queries over 4096 keys each, 32 heads of 128 over 8, 110, at
+// 4.9 TB/s, and 290; 23 sequences of 100 to 800 with 16 heads of 80 over 4, causal, 31 and
+// 41; 4 x 4096 as above 564 and 571).
+template <int DB, bool ALIGNED, bool PACKED>
 __global__ __launch_bounds__(kThreads, DB == 3 ? 3 : 2) void k_attn(muon_attention_t op, uint32_t units, float* part_o, float* part_lse) {
   using G = Geo<DB>;
   __shared__ __attribute__((aligned(256))) char smem[4 * G::TILE];      // K, V; K, V of the next tile
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), h = lane >> 5;
   const Blocks g = grid(units);
-  const auto [head, unit] = g.deal();
-  const Place pl = locate<false, BM>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, op.zero_rest != 0, op.causal != 0, unit, lane);
+  const auto [dealt, unit] = g.deal();
+  const int group = uniform(static_cast<uint32_t>(op.heads / op.kv_heads)), each = PACKED ? group : 1;
+  const Place pl = locate<false, BM>(op.starts, op.k_starts, op.sequences, op.tokens, op.k_tokens, op.zero_rest != 0, op.causal != 0, unit, lane, each);
   if (!pl.found) return;
-  const int kv = uniform(static_cast<uint32_t>(head) / static_cast<uint32_t>(op.heads / op.kv_heads)), dim = op.dim;
-  const int first = pl.tile * BM + 32 * w, mine = first + (lane & 31);   // the wave's first query, the lane's
-  const int offset = pl.nk - pl.nq;                                      // key i + offset is query i's last (causal)
-  const int block_last = min(pl.tile * BM + BM, pl.nq) - 1 + offset;
-  const int keys = op.causal ? max(0, min(pl.nk, block_last + 1)) : pl.nk;   // that any query of the block sees
+  const int kv = PACKED ? dealt : static_cast<int>(uniform(static_cast<uint32_t>(dealt) / static_cast<uint32_t>(group))), dim = op.dim;
+  auto query = [&](int row) { return PACKED ? static_cast<uint32_t>(row) / static_cast<uint32_t>(each) : static_cast<uint32_t>(row); };
+  auto query_of_all = [&](int row) { return static_cast<int>(uniform(query(row))); };
+  const int first = pl.tile * BM + 32 * w, row = first + (lane & 31);                  // the wave's first row, the lane's
+  const int lowest = query_of_all(first), highest = query_of_all(first + 31), mine = query(row);   // their queries
+  const int head = PACKED ? kv * each + row - mine * each : dealt, token = query_of_all(pl.q0) + mine;
+  const int offset = pl.nk - query_of_all(pl.nq);                                      // key i + offset is query i's last (causal)
+  const int block_last = query_of_all(min(pl.tile * BM + BM, pl.nq) - 1) + offset;
+  const int keys = op.causal ? max(0, min(pl.nk, block_last + 1)) : pl.nk;             // that any query of the block sees
 
   bf16x8_t qf[G::KS];
-  own_rows<DB>(op.q, pl.q0, mine, pl.nq, head, dim, h, qf);
+  own_rows<DB>(op.q, token - row, row, pl.nq, head, dim, h, qf);
   const Feed<DB, ALIGNED> fk(op.k, pl.k0, keys, kv, dim, tid), fv(op.v, pl.k0, keys, kv, dim, tid);
   const Frags<DB> fr(lane);
   f32x16_t o[DB];
@@ -446,7 +459,7 @@ __global__ __launch_bounds__(kThreads, DB == 3 ? 3 : 2) void k_attn(muon_attenti
     fv.load((j + 1) * BN, next + G::TILE);
     const int k0 = j * BN;
     // no query of the wave sees the tile
-    if (!(op.causal && k0 > first + 31 + offset) && first < pl.nq) {
+    if (!(op.causal && k0 > highest + offset) && first < pl.nq) {
       // fragments of K are read AHEAD of their use, the first of V before the softmax
       constexpr int KS = G::KS, AHEAD = 3, EARLY = DB;
       f32x16_t s[2] = {};
@@ -463,7 +476,7 @@ __global__ __launch_bounds__(kThreads, DB == 3 ? 3 : 2) void k_attn(muon_attenti
         constexpr int n = AHEAD + decltype(ic)::value;
         vf[n] = fr.cols(now + G::TILE, n / DB, n % DB);
       });
-      if (k0 + BN > pl.nk || (op.causal && k0 + BN - 1 > first + offset)) {
+      if (k0 + BN > pl.nk || (op.causal && k0 + BN - 1 > lowest + offset)) {
         const int last = op.causal ? min(pl.nk - 1, mine + offset) : pl.nk - 1;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
@@ -511,18 +524,18 @@ __global__ __launch_bounds__(kThreads, DB == 3 ? 3 : 2) void k_attn(muon_attenti
     if (j + 1 < j1) step(j + 1, smem + 2 * G::TILE, smem);
   }
   sum = halves_sum(sum);
-  const bool live = mine < pl.nq;
+  const bool live = row < pl.nq;
   const auto* end = late<muon_attention_t>();
   const int rest = pl.rest ? end->zero_rest : ~0;
   if (g.parts > 1) {
-    const int64_t row = (static_cast<int64_t>(g.part) * end->tokens + pl.q0 + mine) * end->heads + head;
-    store_part<DB>(part_o + row * dim, dim, h, live, o, sum == 0.f ? 0.f : 1.f / sum);
-    if (live && h == 0) gst<float>(part_lse + row, sum == 0.f ? -kInf : (top * c + __builtin_amdgcn_logf(sum)) * kLn2);
+    const int64_t at = (static_cast<int64_t>(g.part) * end->tokens + token) * end->heads + head;
+    store_part<DB>(part_o + at * dim, dim, h, live, o, sum == 0.f ? 0.f : 1.f / sum);
+    if (live && h == 0) gst<float>(part_lse + at, sum == 0.f ? -kInf : (top * c + __builtin_amdgcn_logf(sum)) * kLn2);
     return;
   }
-  store_row<DB>(copy(end->o), pl.q0 + mine, head, dim, h, live && (rest & MUON_ATTN_ZERO_O), o, sum == 0.f ? 0.f : 1.f / sum);
+  store_row<DB>(copy(end->o), token, head, dim, h, live && (rest & MUON_ATTN_ZERO_O), o, sum == 0.f ? 0.f : 1.f / sum);
   if (end->lse && live && h == 0 && (rest & MUON_ATTN_ZERO_LSE))
-    gst<float>(end->lse + head * end->ld_lse + pl.q0 + mine, sum == 0.f ? -kInf : (top * c + __builtin_amdgcn_logf(sum)) * kLn2);
+    gst<float>(end->lse + head * end->ld_lse + token, sum == 0.f ? -kInf : (top * c + __builtin_amdgcn_logf(sum)) * kLn2);
 }
 
 // ------------------------------------------------------------ backward: dQ ----
@@ -910,8 +923,10 @@ __global__ __launch_bounds__(256) void k_attn_join(Join j) {
   const bool inside = row < end;
   float v[8] = {}, top = -kInf, total = 0.f;
   if (j.part_lse)
+#pragma unroll 4
     for (int p = 0; p < j.parts; ++p) top = fmaxf(top, gld<float>(j.part_lse + (p * j.rows + row) * j.heads + head));
   const float base = top == -kInf ? 0.f : top;
+#pragma unroll 4
   for (int p = 0; p < j.parts; ++p) {
     const float* from = j.part + ((static_cast<int64_t>(p) * gridDim.y + which) * j.rows * j.heads + at) * j.dim + d;
     const f32x4_t a = gld<f32x4_t>(from), b = gld<f32x4_t>(from + 4);
@@ -959,28 +974,37 @@ int key_rows(int64_t dim) { return dim > 96 ? 32 * kKeyWaves<4> : 32 * kKeyWaves
 // that the chip's 512 places (two blocks a CU) are filled, of 8 steps at least: the join
 // costs a launch (with 4 steps 1024 tokens of 32 heads of 64 took 27 and 62 us instead of
 // 20 and 45; 32 queries over 8192 keys, 8 heads of 128: 28 and 44, without parts 139 and 200).
-int parts_of(int64_t blocks, int64_t steps) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kMaxParts, 512 / std::max<int64_t>(blocks, 1), steps / 8})));
+int parts_of(int64_t blocks, int64_t steps, int64_t most = kMaxParts) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most, 512 / std::max<int64_t>(blocks, 1), steps / 8})));
 }
 
 template <class Op>
+int64_t sequences_of(const Op& op) {
+  return std::max<int64_t>(1, op.starts ? op.sequences : 1);
+}
+
+// Steps over the queries or keys that one of `rows` keys or queries meets, in the mean.
+template <class Op>
 int64_t average_steps(const Op& op, int64_t rows) {
-  const int64_t n = rows / std::max<int64_t>(1, op.starts ? op.sequences : 1) / BN;
-  return op.causal ? n / 2 : n;
+  const int64_t q = op.tokens, k = op.k_tokens, pairs = !op.causal ? q * k : k < q ? k * k / 2 : q * (k - q / 2);
+  return pairs / std::max<int64_t>(rows, 1) / sequences_of(op) / BN;
 }
 
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
+// Blocks that own queries, `each` rows a query, in `heads` heads.
 template <class Op>
-int query_parts(const Op& op) {
-  return parts_of((op.tokens + BM - 1) / BM * op.heads, average_steps(op, op.k_tokens));
+int64_t query_blocks(const Op& op, int64_t each, int64_t heads) {
+  return std::max((op.tokens * each + BM - 1) / BM, sequences_of(op)) * heads;
 }
 
 }  // namespace
 
 AttnPlan attention_plan(const muon_attention_t& op) {
   AttnPlan p{};
-  p.parts = query_parts(op);
+  p.packed = op.heads > op.kv_heads;      // (tokens x heads fit 32 bits)
+  const int64_t each = p.packed ? op.heads / op.kv_heads : 1;
+  p.parts = parts_of(query_blocks(op, each, op.heads / each), average_steps(op, op.tokens), kMaxForwardParts);
   if (p.parts > 1) {
     const size_t rows = static_cast<size_t>(p.parts) * op.tokens * op.heads;
     p.lse_off = rounded(rows * op.dim * sizeof(float));
@@ -992,9 +1016,9 @@ AttnPlan attention_plan(const muon_attention_t& op) {
 AttnGradPlan attention_grad_plan(const muon_attention_grad_t& op) {
   AttnGradPlan p{};
   const size_t q = static_cast<size_t>(op.tokens) * op.heads, k = static_cast<size_t>(op.k_tokens) * op.kv_heads;
-  p.parts_q = query_parts(op);
+  p.parts_q = parts_of(query_blocks(op, 1, op.heads), average_steps(op, op.tokens));
   const int own = key_rows(op.dim);
-  p.parts_k = parts_of((op.k_tokens + own - 1) / own * op.kv_heads, op.heads / op.kv_heads * average_steps(op, op.tokens));
+  p.parts_k = parts_of((op.k_tokens + own - 1) / own * op.kv_heads, op.heads / op.kv_heads * average_steps(op, op.k_tokens));
   const bool ragged = op.starts != nullptr;
   // (2 x 37 tokens, 4 heads of 64: 12.5 us, two launches 17.4; 512 tokens, 8 heads: 21, 32)
   p.one_launch = p.parts_q == 1 && p.parts_k == 1 &&
@@ -1007,12 +1031,17 @@ AttnGradPlan attention_grad_plan(const muon_attention_grad_t& op) {
 }
 
 int launch_attention(const muon_attention_t& op, const AttnPlan& p, char* ws, void* stream) {
-  const uint32_t units = units_of(op.tokens, op.sequences, op.starts != nullptr);
+  const int64_t each = p.packed ? op.heads / op.kv_heads : 1;
+  const uint32_t units = units_of(op.tokens * each, op.sequences, op.starts != nullptr);
+  const dim3 grid(units * static_cast<uint32_t>(op.heads / each), p.parts);
   return by_shape(op.dim, aligned16(op.k) && aligned16(op.v), [&](auto db, auto al) {
-    hipLaunchKernelGGL((k_attn<decltype(db)::value, decltype(al)::value>), dim3(units * static_cast<uint32_t>(op.heads), p.parts),
-                       dim3(kThreads), 0, static_cast<hipStream_t>(stream), op, units, reinterpret_cast<float*>(ws),
-                       reinterpret_cast<float*>(ws + p.lse_off));
-    return static_cast<int>(hipGetLastError());
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), op, units, reinterpret_cast<float*>(ws),
+                         reinterpret_cast<float*>(ws + p.lse_off));
+      return static_cast<int>(hipGetLastError());
+    };
+    return p.packed ? launch(k_attn<decltype(db)::value, decltype(al)::value, true>)
+                    : launch(k_attn<decltype(db)::value, decltype(al)::value, false>);
   });
 }
 

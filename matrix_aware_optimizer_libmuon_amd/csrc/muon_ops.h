@@ -79,6 +79,7 @@ int launch_embed_join(const muon_embed_grad_t& op, const EmbedSortPlan& p, char*
 // muon_attn.hip.  Workspace: where few blocks have long rows, their steps are cut into
 // parts whose results a further launch joins.
 struct AttnPlan {
+  bool packed;         // heads that share keys and values in one block
   int parts;
   size_t lse_off;      // each part's lse, behind its o
   size_t bytes;

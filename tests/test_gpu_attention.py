@@ -192,6 +192,28 @@ def test_single_queries_over_long_keys():
 
 
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,kv,dim", [(4, 1, 64), (6, 2, 80), (5, 1, 128), (32, 8, 40), (48, 1, 64), (200, 1, 24)])
+@pytest.mark.parametrize("nq,nk", [([1], [1]), ([1, 1, 1], [70, 1, 300]), ([3, 0, 2], [64, 9, 700]), ([1, 150, 2, 0, 4], [200, 150, 1, 33, 3]),
+                                   ([11], [2000]), ([1] * 70, [3] * 70), ([64], [64]), ([5, 2], [0, 1])])
+def test_few_queries_of_heads_that_share_keys(nq, nk, heads, kv, dim, causal):
+    """A block takes the queries of all heads of a key head, most of its rows empty."""
+    out = check(*tensors(heads, sum(nq), sum(nk), heads, kv, dim), nq, nk, causal)
+    q, k, v = tensors(heads, sum(nq) + 3, sum(nk) + 5, heads, kv, dim)
+    st = dict(starts=starts_of(nq), k_starts=starts_of(nk), causal=causal)
+    kept, (fresh, lse) = torch.full_like(q, 7.0), muon.attention(q, k, v, **st)
+    muon.attention(q, k, v, out=kept, **st)
+    n = sum(nq)
+    assert (kept[n:] == 7).all() and not fresh[n:].any() and torch.equal(kept[:n], fresh[:n]) and (lse[:, n:] == -float("inf")).all()
+    assert out[0].shape == (n, heads, dim)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_layouts_of_few_queries(layout, causal):
+    check(*tensors(3, 12, 312, 4, 2, 72, layout), [7, 1, 0, 4], [7, 200, 5, 100], causal, layout=layout)
+
+
+@pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("nq,nk,heads,kv,dim", [([40], [4096], 4, 2, 64), ([1], [5000], 2, 1, 128), ([3, 0, 70], [3000, 9, 2500], 2, 2, 80),
                                                 ([2500], [2500], 1, 1, 64), ([2100, 30], [2100, 30], 4, 1, 128), ([3000], [50], 2, 1, 40),
                                                 ([1500], [1400], 3, 3, 96)])

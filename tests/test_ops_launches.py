@@ -95,8 +95,8 @@ def test_attention_kernels_by_columns_and_alignment():
             al = "false" if odd else "true"
             got = record([(e, dict(args, dim=dim, odd=odd)) for args in (few, many) for e in ("attention", "attention_grad")])
             names = [[kernel for kernel, _, _ in launches] for _, launches in got]
-            assert names == [[f"k_attn<{blocks}, {al}>"], [f"k_attn_grad<{blocks}, {al}>"],
-                             [f"k_attn<{blocks}, {al}>"], [f"k_attn_dq<{blocks}, {al}>", f"k_attn_dkv<{blocks}, {al}>"]]
+            assert names == [[f"k_attn<{blocks}, {al}, true>"], [f"k_attn_grad<{blocks}, {al}>"],
+                             [f"k_attn<{blocks}, {al}, true>"], [f"k_attn_dq<{blocks}, {al}>", f"k_attn_dkv<{blocks}, {al}>"]]
 
 
 @pytest.mark.parametrize("heads_,kv,tokens,k_tokens,dim,one", [
@@ -119,7 +119,7 @@ def test_attention_takes_slices_of_one_buffer(layout):
 @pytest.mark.parametrize("tokens,k_tokens,heads_,kv,dim,sequences,parts", [
     (40, 4096, 4, 2, 64, 0, (8, 8, 1)), (1, 5000, 2, 1, 128, 0, (9, 9, 1)), (73, 5509, 2, 2, 80, 3, (3, 3, 1)),
     (2500, 2500, 1, 1, 64, 0, (4, 4, 4)), (2130, 2130, 4, 1, 128, 2, (2, 2, 8)), (3000, 50, 2, 1, 40, 0, (1, 1, 11)),
-    (1500, 1400, 3, 3, 96, 0, (2, 2, 2)), (64, 1 << 16, 1, 1, 64, 0, (16, 16, 1)), (16384, 16384, 32, 8, 128, 4, (1, 1, 1)),
+    (1500, 1400, 3, 3, 96, 0, (2, 2, 2)), (64, 1 << 16, 1, 1, 64, 0, (64, 16, 1)), (16384, 16384, 32, 8, 128, 4, (1, 1, 1)),
     (74, 74, 4, 4, 64, 2, (1, 1))])
 def test_parts_of_attention(tokens, k_tokens, heads_, kv, dim, sequences, parts):
     """How many parts the steps of the tested sizes are cut into: forward, dq, dk and dv; each cut has its join."""
@@ -132,6 +132,16 @@ def test_parts_of_attention(tokens, k_tokens, heads_, kv, dim, sequences, parts)
         else:
             got.append(grid[1])
     assert tuple(got) == parts and joins == sum(p > 1 for p in parts)
+
+
+@pytest.mark.parametrize("tokens,k_tokens,heads_,kv,sequences,packed,grid", [
+    (32, 32 * 4096, 32, 8, 32, True, (34 * 8, 2, 1)), (1, 65536, 32, 8, 0, True, (8, 64, 1)), (1, 65536, 8, 8, 0, False, (8, 64, 1)),
+    (64, 64, 6, 2, 0, True, (4, 1, 1)), (65, 65, 6, 6, 0, False, (6, 1, 1)), (640, 9000, 10, 2, 10, True, (36 * 2, 1, 1)),
+    (641, 9000, 10, 10, 10, False, (17 * 10, 1, 1)), (3, 3000, 4, 1, 2, True, (4, 2, 1))])
+def test_heads_that_share_keys_go_together(tokens, k_tokens, heads_, kv, sequences, packed, grid):
+    """Forward pass: a block has the rows of all heads of a key head."""
+    (status, launches), = record([("attention", dict(tokens=tokens, k_tokens=k_tokens, heads_=heads_, kv=kv, dim=64, sequences=sequences))])
+    assert status == 0 and launches[0][0] == f"k_attn<2, true, {'true' if packed else 'false'}>" and launches[0][1] == grid
 
 
 @pytest.mark.parametrize("entry", ["distill", "policy"])
