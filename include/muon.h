@@ -686,8 +686,8 @@ int muon_distill(const muon_distill_t* op, hipStream_t stream);
  * with A the advantage.  A token of weight 0, or whose action is outside 0 .. vocab - 1,
  * has loss and logp 0 and a gradient of zeros, whatever its logits hold.
  *   logits      dtype, tokens x vocab;  actions  int32 or int64 [tokens]
- *   old_logp, advantages, ref_logp, weights  fp32 [tokens]; ref_logp NULL: no KL term;
- *               weights NULL: 1
+ *   old_logp, advantages, ref_logp, weights  fp32 [tokens]; no KL term where ref_logp
+ *               is NULL or kl_coef 0; weights NULL: 1
  *   loss, logp  fp32 [tokens]; logp may be NULL
  *   dlogits     dtype, NULL: not wanted */
 typedef struct {

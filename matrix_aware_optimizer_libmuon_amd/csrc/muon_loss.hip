@@ -414,7 +414,8 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_policy(muon_polic
     const float held = fminf(fmaxf(ratio, 1.f - op.clip_low), 1.f + op.clip_high) * adv;
     // a comparison that NaN fails lets it through
     float loss = held < free ? -held : -free, slope = held < free ? 0.f : -free;
-    if (op.ref_logp) {
+    // a coefficient of 0 has no part either, whatever the reference (exp(d) may be infinite)
+    if (op.ref_logp && op.kl_coef != 0.f) {
       const float d = ref - logp;
       loss += op.kl_coef * exp_less_linear(d);
       slope -= op.kl_coef * expm1f(d);

@@ -199,7 +199,8 @@ def policy_loss(logits, actions, old_logp, advantages, *, ref_logp=None, clip: f
         loss = weight * (-min(r A, clamp(r, 1 - clip, 1 + clip_high) A) + kl_coef (exp(d) - d - 1))
 
     float32 per token, and ``dlogits`` the gradient of loss.sum(), in the logits' type
-    (None if not wanted).  No KL term without ``ref_logp``; ``clip_high``: clip if None.
+    (None if not wanted).  No KL term without ``ref_logp`` or at a ``kl_coef`` of 0;
+    ``clip_high``: clip if None.
     ``weights``: float32 per token; a token of weight 0, or whose action is outside
     the vocabulary, has loss and logp 0, and its logits are not read."""
     return tuple(_run("policy_loss", logits, stream, logits, actions, old_logp, advantages, ref_logp, weights, out, float(clip),

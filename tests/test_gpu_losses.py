@@ -330,3 +330,17 @@ def test_refusals_name_the_argument():
         with pytest.raises(muon.LibMuonError) as e:
             call()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids_of)
+def test_a_kl_coefficient_of_zero_takes_no_part(dtype):
+    """Whatever the reference: exp(d) past the largest number, an action that cannot be."""
+    z = torch.randn(4, 900, generator=gen(2))
+    z[0, 3], z[1, 3] = -float("inf"), -200.0
+    actions, adv = torch.full((4,), 3, device=DEV), torch.tensor([1.0, -1.0, 0.5, 0.0]).to(DEV)
+    old, ref = torch.full((4,), -7.0, device=DEV), torch.tensor([-1.0, 0.0, -5.0, float("inf")]).to(DEV)
+    z = z.to(dtype).to(DEV)
+    with_ref = muon.policy_loss(z, actions, old, adv, ref_logp=ref)
+    without = muon.policy_loss(z, actions, old, adv)
+    for a, b in zip(with_ref, without):
+        assert torch.equal(a, b) and not torch.isnan(a).any()
