@@ -344,3 +344,24 @@ def test_a_kl_coefficient_of_zero_takes_no_part(dtype):
     without = muon.policy_loss(z, actions, old, adv)
     for a, b in zip(with_ref, without):
         assert torch.equal(a, b) and not torch.isnan(a).any()
+
+
+@pytest.mark.parametrize("temperature", [1.0, 1.25, 2.0, 4.0])
+@pytest.mark.parametrize("dtype", TYPES, ids=ids_of)
+def test_entries_on_a_column_of_the_lowest_value(dtype, temperature):
+    """A column masked with the type's lowest value has a log-probability of about -3e38 / temperature, not of -infinity.
+    Relative to it: the difference, the quotient by the temperature (two roundings), the log's subtraction, a product and
+    the weight's: 8 u; the log of the sum is 2^-120 of it."""
+    low = torch.finfo(dtype).min
+    z = torch.randn(2, 700, generator=gen(4)).to(dtype)
+    z[:, 5] = low
+    want = (O.log_softmax(np64(z) / temperature))[:, 5]
+    off = 8 * U * np.abs(want)
+    zero = torch.zeros(2, device=DEV)
+    loss, logp, grad = muon.policy_loss(z.to(DEV), torch.full((2,), 5, device=DEV), zero - 1, zero + 1, temperature=temperature)
+    assert (np.abs(np64(logp) - want) <= off).all() and not loss.any() and not grad.any()
+    # a quarter of the teacher's mass on it
+    loss, grad = muon.distill_loss(z.to(DEV), torch.tensor([[5, 6, 7, 8]] * 2, device=DEV), torch.zeros(2, 4, device=DEV), temperature=temperature,
+                                   weights=zero + 1 / 8)
+    want = -want / 4 * temperature ** 2 / 8
+    assert (np.abs(np64(loss) - want) <= (8 + 30) * U * want).all() and torch.isfinite(grad).all()
