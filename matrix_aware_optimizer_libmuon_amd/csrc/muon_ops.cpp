@@ -6,6 +6,7 @@
 #include <cmath>
 #include <initializer_list>
 #include <string>
+#include <utility>
 
 #include "muon.h"
 #include "muon_internal.h"
@@ -23,21 +24,47 @@ size_t type_size(int32_t dtype) { return dtype == MUON_BF16 ? 2 : 4; }
 bool type_ok(int32_t dtype) { return dtype == MUON_F32 || dtype == MUON_BF16; }
 bool size_ok(int64_t rows, int64_t cols) { return rows >= 0 && rows <= kMaxRows && cols >= 1 && cols <= MUON_MAX_DIM; }
 
-// The bytes of a strided matrix: `rows` pieces of `width` bytes, `stride` apart.
+// The bytes of a strided tensor: `rows` rows, `stride` apart, of `n` pieces of `width`
+// bytes, `step` apart.  A row's pieces span a stride at most (n is 1 for a matrix).
 struct Span {
   uintptr_t begin = 0;
-  uint64_t rows = 0, width = 0, stride = 0;
-  uintptr_t end() const { return begin + (rows - 1) * stride + width; }
+  uint64_t rows = 0, width = 0, stride = 0, n = 1, step = 0;
+  uint64_t extent() const { return (n - 1) * step + width; }
+  uintptr_t end() const { return begin + (rows - 1) * stride + extent(); }
+  // the same bytes with each piece a row, where rows follow each other in steps of one length
+  bool even() const { return n > 1 && stride == n * step; }
+  Span flat() const { return {begin, rows * n, width, step, 1, 0}; }
 };
+
+// Whether a piece of a row of b, which begins `at` bytes behind one of a, meets one of a:
+// some j has -b.width < at + j step < a.width.
+bool rows_meet(const Span& a, const Span& b, int64_t at) {
+  const int64_t wa = static_cast<int64_t>(a.width), wb = static_cast<int64_t>(b.width), step = static_cast<int64_t>(a.n > 1 ? a.step : b.step);
+  if (a.n == 1 && b.n == 1) return at < wa && at + wb > 0;
+  if (a.n > 1 && b.n > 1 && a.step != b.step)   // (as if they had no gaps)
+    return at < static_cast<int64_t>(a.extent()) && at + static_cast<int64_t>(b.extent()) > 0;
+  const int64_t over = -wb - at, first = (over >= 0 ? over / step : -((-over + step - 1) / step)) + 1;   // the least j past the left bound
+  const int64_t j = first > 1 - static_cast<int64_t>(a.n) ? first : 1 - static_cast<int64_t>(a.n);
+  return j < static_cast<int64_t>(b.n) && at + j * step < wa;
+}
+
+// Slices of one buffer, rows of the same stride: the rows of b begin d + r stride bytes
+// behind those of a, 0 <= d < stride, and only r = 0 and r = -1 can meet.
+bool slices_meet(const Span& a, const Span& b) {
+  const int64_t s = static_cast<int64_t>(a.stride), by = static_cast<int64_t>(b.begin - a.begin);
+  const int64_t m = by >= 0 ? by / s : -((-by + s - 1) / s), d = by - m * s;
+  // the row of b that lies r strides behind some row of a: its number less that row's is r - m
+  auto there = [&](int64_t r) { return r - m > -static_cast<int64_t>(a.rows) && r - m < static_cast<int64_t>(b.rows); };
+  return (there(0) && rows_meet(a, b, d)) || (there(-1) && rows_meet(a, b, d - s));
+}
 
 bool overlap(const Span& a, const Span& b) {
   if (!a.rows || !b.rows || a.end() <= b.begin || b.end() <= a.begin) return false;
-  // slices of one buffer: apart where their columns are, modulo the row stride
-  if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {
-    const uint64_t d = b.begin >= a.begin ? (b.begin - a.begin) % a.stride
-                                          : (a.stride - (a.begin - b.begin) % a.stride) % a.stride;
-    return !(d >= a.width && d + b.width <= a.stride);
-  }
+  auto alike = [](const Span& x, const Span& y) { return x.rows > 1 && y.rows > 1 && x.stride == y.stride; };
+  if (alike(a, b)) return slices_meet(a, b);
+  if (a.even() && alike(a.flat(), b)) return slices_meet(a.flat(), b);
+  if (b.even() && alike(a, b.flat())) return slices_meet(a, b.flat());
+  if (a.even() && b.even() && alike(a.flat(), b.flat())) return slices_meet(a.flat(), b.flat());
   return true;
 }
 
@@ -54,7 +81,7 @@ class Args {
     s.rows = static_cast<uint64_t>(rows);
     s.width = static_cast<uint64_t>(cols) * esize;
     s.stride = rows > 1 ? static_cast<uint64_t>(ld) * esize : s.width;
-    (written ? out_ : in_)[written ? n_out_++ : n_in_++] = s;
+    note(s, written);
     return true;
   }
   bool act8(const muon_act8_t& a, int64_t rows, int64_t cols, bool written, bool need = true) {
@@ -63,19 +90,24 @@ class Args {
     return mat(a.codes, rows, cols, a.ld_codes, 1, written) &&
            mat(a.scales, rows, (cols + MUON_ACT8_GROUP - 1) / MUON_ACT8_GROUP, a.ld_scales, 1, written);
   }
-  // A tokens x heads x dim tensor of bf16.  As rows that `overlap` can tell apart
-  // where its axes allow it (heads side by side, in steps of one stride, or one after
-  // the other); else as everything from its first byte to its last.
+  // A tokens x heads x dim tensor of bf16: each token's heads lie within a token's stride,
+  // or each head's tokens within a head's.
   bool heads(const muon_heads_t& t, int64_t tokens, int64_t heads, int64_t dim, bool written) {
     const int64_t lt = t.ld_token, lh = t.ld_head;
     if (tokens == 0 || heads == 1) return mat(t.data, tokens, dim, lt, 2, written);
     if (tokens == 1) return mat(t.data, heads, dim, lh, 2, written);
-    if (lt < dim || lh < dim || lt > kMaxSpan / tokens || lh > kMaxSpan / heads) return false;
+    if (!t.data || !is_aligned(t.data, 2) || lt < dim || lh < dim || lt > kMaxSpan / tokens || lh > kMaxSpan / heads) return false;
+    const bool by_token = lt >= (heads - 1) * lh + dim;
+    if (!by_token && lh < (tokens - 1) * lt + dim) return false;
     if (lh == dim) return mat(t.data, tokens, heads * dim, lt, 2, written);
-    if (lt == heads * lh) return mat(t.data, tokens * heads, dim, lh, 2, written);
-    if (lh == tokens * lt) return mat(t.data, tokens * heads, dim, lt, 2, written);
-    if (lt < (heads - 1) * lh + dim && lh < (tokens - 1) * lt + dim) return false;
-    return mat(t.data, 1, (tokens - 1) * lt + (heads - 1) * lh + dim, 0, 2, written);
+    Span s{reinterpret_cast<uintptr_t>(t.data), static_cast<uint64_t>(tokens), static_cast<uint64_t>(dim) * 2, static_cast<uint64_t>(lt) * 2,
+           static_cast<uint64_t>(heads), static_cast<uint64_t>(lh) * 2};
+    if (!by_token) {
+      std::swap(s.rows, s.n);
+      std::swap(s.stride, s.step);
+    }
+    note(s, written);
+    return true;
   }
   bool vec(const void* p, int64_t n, size_t esize, bool written, bool need) { return n == 0 || mat(p, 1, n, n, esize, written, need); }
   bool clash() const {
@@ -89,6 +121,7 @@ class Args {
   }
 
  private:
+  void note(const Span& s, bool written) { (written ? out_ : in_)[written ? n_out_++ : n_in_++] = s; }
   Span in_[12], out_[10];   // more than any call notes
   int n_in_ = 0, n_out_ = 0;
 };

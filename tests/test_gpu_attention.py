@@ -394,3 +394,34 @@ def test_refusals_name_the_argument():
         with pytest.raises(muon.LibMuonError) as e:
             call()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("pad", [8, 5])
+@pytest.mark.parametrize("form", ["heads of a kind apart", "heads side by side", "padded columns"])
+def test_slices_of_a_padded_buffer(form, pad):
+    """q, k, v in one buffer, dq, dk, dv in one, q and o in one: the same bits as in tensors of their own."""
+    lengths, h, d = [70, 1, 130], 4, 64
+    n = sum(lengths)
+
+    def three():
+        if form == "padded columns":
+            x = torch.full((n, 3 * h, d + pad), 7.0, device=DEV, dtype=BF)
+            return x, [x[:, i * h:(i + 1) * h, :d] for i in range(3)]
+        x = torch.full((n, 3 * h * d + pad), 7.0, device=DEV, dtype=BF)
+        parts = x[:, :3 * h * d].unflatten(1, (3, h, d) if form == "heads of a kind apart" else (h, 3, d))
+        return x, [parts[:, i] if form == "heads of a kind apart" else parts[:, :, i] for i in range(3)]
+    plain = tensors(21, n, n, h, h, d)
+    _, qkv = three()
+    for a, b in zip(qkv, plain):
+        a.copy_(b)
+    st = dict(starts=starts_of(lengths))
+    o, lse = muon.attention(*plain, **st)
+    do = torch.randn(o.shape, generator=gen(1)).to(BF).to(DEV)
+    want = muon.attention_grad(do, *plain, o, lse, **st)
+    whole, grads = three()
+    muon.attention_grad(do, *qkv, o, lse, dq=grads[0], dk=grads[1], dv=grads[2], **st)
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
+    assert int((whole == 7).sum()) == whole.numel() - sum(int((g != 7).sum()) for g in grads)
+    _, (q, out, _) = three()
+    q.copy_(plain[0])
+    assert torch.equal(muon.attention(q, plain[1], plain[2], out=out, **st)[0], o)

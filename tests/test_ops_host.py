@@ -375,3 +375,64 @@ def test_binding_of_attention_and_losses_refuses_cpu_tensors(lib):
                  lambda: muon.policy_loss(x, i, v, v)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def bytes_of(t, tokens, n, dim):
+    return {t.data + 2 * (i * t.ld_token + h * t.ld_head) + b for i in range(tokens) for h in range(n) for b in range(2 * dim)}
+
+
+def attention_of(q, o, n_q, n_kv, tokens, dim, lib, **kw):
+    far = lambda n: heads(n, dim)  # noqa: E731
+    op = with_(L.MuonAttention(q=q, k=far(n_kv), v=far(n_kv), o=o, tokens=tokens, k_tokens=tokens, heads=n_q, kv_heads=n_kv, dim=dim,
+                               ld_lse=tokens, scale=1.0), **kw)
+    return lib.muon_attention(ctypes.byref(op), WS, 1 << 40, None)
+
+
+def test_slices_of_a_padded_buffer_do_not_overlap(lib):
+    """Heads in steps whose tokens have a stride of their own: side by side in every head, padded columns, unlike numbers of heads."""
+    p, tokens, n, dim = ptr(), 40, 4, 64
+    for lt, lh, apart in ((3 * n * dim + dim, 3 * dim, dim), (3 * n * dim + 8, 3 * dim, 2 * dim), (3 * n * (dim + 8), dim + 8, n * (dim + 8)),
+                          (3 * dim, 3 * dim * (tokens + 2), dim), (dim, dim * (3 * tokens + 1), dim * tokens)):
+        one = L.MuonHeads(p, lt, lh)
+        mine, seen = bytes_of(one, tokens, n, dim), set()
+        for at in (apart, apart - 8, apart - 16, apart + 8, apart - dim, 0):
+            other = L.MuonHeads(p + 2 * at, lt, lh)
+            meet = bool(mine & bytes_of(other, tokens, n, dim))
+            assert not (meet and at == apart)
+            for q, o in ((one, other), (other, one)):
+                got = attention_of(q, o, n, n, tokens, dim, lib)
+                assert got == EALIAS if meet else got not in (EALIAS, EINVAL), (lt, lh, at)
+            seen.add(meet)
+        assert seen == {False, True}
+    # q of 4 heads and dk, dv of 2 behind them, all in steps of padded columns
+    at = lambda head: L.MuonHeads(p + 2 * head * 72, 8 * 72, 72)  # noqa: E731
+    op = attn_grad(dq=at(0), dk=at(4), dv=at(6))
+    assert lib.muon_attention_grad(ctypes.byref(op), WS, 1 << 40, None) not in (EALIAS, EINVAL)
+    for bad in (dict(dk=at(3)), dict(dv=at(5)), dict(dq=at(1))):
+        assert lib.muon_attention_grad(ctypes.byref(with_(attn_grad(dq=at(0), dk=at(4), dv=at(6)), **bad)), WS, 1 << 40, None) == EALIAS
+
+
+def test_overlap_of_heads_against_sets_of_bytes(lib):
+    """Random strides: a call whose output shares a byte with an input is always refused; one whose tensors have the same
+    strides only then."""
+    rng, apart, shared = random.Random(5), 0, 0
+    for _ in range(4000):
+        tokens, n, dim = rng.randint(1, 5), rng.randint(1, 4), rng.choice([8, 16])
+        inner = rng.choice([dim, dim + 8, 2 * dim, 3 * dim, 3 * dim + 8])
+
+        def strides():
+            if rng.random() < 0.5:
+                return rng.choice([n * inner, n * inner + 8, 3 * n * inner, (n - 1) * inner + dim]), inner
+            return inner, rng.choice([tokens * inner, tokens * inner + 8, 3 * tokens * inner, (tokens - 1) * inner + dim])
+        (lt, lh), p = strides(), ptr()
+        other = strides() if rng.random() < 0.3 else (lt, lh)
+        q, o = L.MuonHeads(p, lt, lh), L.MuonHeads(p + 2 * rng.randint(-8 * inner, 8 * inner), *other)
+        got = attention_of(q, o, n, n, tokens, dim, lib)
+        meet = bool(bytes_of(q, tokens, n, dim) & bytes_of(o, tokens, n, dim))
+        assert got != EINVAL and (got == EALIAS if meet else True), (tokens, n, dim, lt, lh, other, o.data - p)
+        if other == (lt, lh) and not meet:
+            inside = max(bytes_of(q, tokens, n, dim)) >= o.data and max(bytes_of(o, tokens, n, dim)) >= p
+            assert got != EALIAS, (tokens, n, dim, lt, lh, o.data - p)
+            apart += inside
+        shared += meet
+    assert apart > 200 and shared > 500
