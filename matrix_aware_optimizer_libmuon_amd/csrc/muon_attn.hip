@@ -448,6 +448,9 @@ __global__ __launch_bounds__(kThreads, DB == 3 ? 3 : 2) void k_attn(muon_attenti
   for (int db = 0; db < DB; ++db) o[db] = f32x16_t{};
   float top = -kInf, sum = 0.f;                // top: the maximum that P is taken against; sum: of this half's keys
   const float c = op.scale * kLog2e;
+  // kSlack in units of the scores; finite, as top is -inf at first and no NaN may arise (the
+  // file is compiled as if there were none)
+  const float slack = __uint_as_float(uniform(__float_as_uint(fminf(kSlack / c, 1e38f))));
 
   const auto [j0, j1] = g.range((keys + BN - 1) / BN);
   fk.load(j0 * BN, smem);
@@ -488,7 +491,7 @@ __global__ __launch_bounds__(kThreads, DB == 3 ? 3 : 2) void k_attn(muon_attenti
 #pragma unroll
       for (int i = 1; i < 16; ++i) m = fmaxf(m, fmaxf(s[0][i], s[1][i]));
       m = halves_max(m);
-      if (__any((m - top) * c > kSlack)) {     // (-inf - -inf is NaN: no)
+      if (__any(m > top + slack)) {
         const float grown = fmaxf(m, top);
         const float f = grown == -kInf ? 0.f : exp2_fast((top - grown) * c);
         top = grown;
