@@ -154,3 +154,41 @@ def test_blocks_that_share_a_long_row_of_few(entry, tokens, vocab, dtype, share)
     (status, ((kernel, grid, _),)), = record([(entry, dict(tokens=tokens, vocab=vocab, dtype=dtype))])
     assert status == 0 and kernel.endswith(f", {'true' if share > 1 else 'false'}>")
     assert grid == (tokens, share, 1)
+
+
+def loss_shape(rows, cols, f32):
+    """(threads, vectors of 8 columns a thread) of a row; 0 vectors: read twice."""
+    if cols <= 512:
+        return 64, 1
+    if rows <= 512:
+        few = [(2048, 256, 1), (8192, 1024, 1), (16384, 1024, 2), (32768, 1024, 4), (65536, 1024, 8)]
+        for most, threads, vectors in few:
+            if cols <= most:
+                return threads, vectors
+    many = [(2048, 64, 4), (8192, 256, 4), (16384, 512, 4), (32768, 512, 8)]
+    many += [(65536, 1024, 8)] if f32 else [(65536, 512, 16), (131072, 1024, 16)]
+    for most, threads, vectors in many:
+        if cols <= most:
+            return threads, vectors
+    return 1024, 0
+
+
+@pytest.mark.parametrize("entry", ["distill", "policy"])
+def test_loss_kernels_of_the_tested_sizes(entry):
+    """Every kernel that a size can take is one that tests/test_gpu_losses.py or test_gpu_losses_rows.py compares with the oracle."""
+    from tests.test_gpu_losses import COLS
+    from tests.test_gpu_losses_rows import CASES
+    sizes = [(3, cols, t) for cols in COLS for t in ("f32", "bf16")]
+    sizes += [(rows, cols, "f32" if str(t) == "torch.float32" else "bf16") for rows, cols, t in CASES]
+    tested = set()
+    for (rows, cols, t), (status, ((kernel, _, block),)) in zip(sizes, record([(entry, dict(tokens=r, vocab=c, dtype=t)) for r, c, t in sizes])):
+        threads, vectors = loss_shape(rows, cols, t == "f32")
+        name = f"k_{entry}<{'float' if t == 'f32' else 'unsigned short'}, {threads}, {vectors}, "
+        assert status == 0 and kernel.startswith(name) and block == (threads, 1, 1), (rows, cols, t, kernel)
+        tested.add(kernel)
+    reached = set()
+    grid = [(rows, cols, t) for rows in (1, 16, 100, 128, 129, 512, 513, 1 << 20) for t in ("f32", "bf16")
+            for cols in (1, 512, 513, 2048, 2049, 8192, 8193, 16384, 16385, 32768, 32769, 65536, 65537, 131072, 131073, 1 << 20)]
+    for _, ((kernel, _, _),) in record([(entry, dict(tokens=r, vocab=c, dtype=t)) for r, c, t in grid]):
+        reached.add(kernel)
+    assert reached == tested
