@@ -192,3 +192,16 @@ def test_loss_kernels_of_the_tested_sizes(entry):
     for _, ((kernel, _, _),) in record([(entry, dict(tokens=r, vocab=c, dtype=t)) for r, c, t in grid]):
         reached.add(kernel)
     assert reached == tested
+
+
+def test_unaligned_backward_passes_of_the_tested_sizes():
+    """tests/test_gpu_attention_paths.py: two launches without wide loads, cut into parts and whole."""
+    from tests.test_gpu_attention_paths import PARTS, WHOLE
+    for cases, cut in ((PARTS, True), (WHOLE, False)):
+        for nq, nk, heads_, kv, dim in cases:
+            (status, launches), = record([("attention_grad", dict(tokens=sum(nq), k_tokens=sum(nk), heads_=heads_, kv=kv, dim=dim,
+                                                                  sequences=len(nq), odd=True, causal=0))])
+            blocks = 2 if dim <= 64 else 3 if dim <= 96 else 4
+            names = [k for k, _, _ in launches if k != "k_attn_join"]
+            assert status == 0 and names == [f"k_attn_dq<{blocks}, false>", f"k_attn_dkv<{blocks}, false>"], (nq[:3], dim, launches)
+            assert any(grid[1] > 1 for k, grid, _ in launches if k != "k_attn_join") == cut, (nq[:3], dim, launches)
