@@ -12,8 +12,8 @@
 // exponentials, a quarter of the rate of other instructions, 32000 of them twice in 9 us.
 //
 // Numbers.  x - max is taken before the factor log2(e) / temperature, so that rows
-// of the type's lowest value stay finite, and log-probabilities are (x - max) / temperature
-// - log(sum), so that single columns of it do; sums run in fp32, up to 128 terms a
+// of the type's lowest value stay finite, and a single log2 of a probability is
+// halved, so that it does for a column of that value; sums run in fp32, up to 128 terms a
 // thread, then over the wave and the waves in a fixed order.  The gradient is
 // rounded once, to the logits' type.
 #include <type_traits>
@@ -44,6 +44,12 @@ __device__ __forceinline__ float base_of(float m) { return m == kNegInf ? 0.f : 
 // of nothing but -inf is 0 and stays it).
 __device__ __forceinline__ float shrink(float from, float to, float k) {
   return from == kNegInf ? 0.f : exp2_fast((from - to) * k);
+}
+
+// Half of log2 of v's probability, (v - base) k - log2(sum): v may be the type's lowest value,
+// which log2(e) takes past the largest number, and the half is as exact.
+__device__ __forceinline__ float half_log2(float v, float base, float k, float log2_sum) {
+  return (v - base) * 0.5f * k - 0.5f * log2_sum;
 }
 
 // Maximum and sum of 2^((v - m) k) over some values.
@@ -323,8 +329,7 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_distill(muon_dist
     const Soft q = block_join<RT>(sh, 0, k);
     teach = block_join<RT>(sh, 1, k);
     const bool none = teach.s == 0.f;               // no entry, no loss
-    const float base = base_of(q.m), lq = log2_fast(q.s) * kLn2, lt = log2_fast(teach.s), tbase = base_of(teach.m);
-    const float cool = 1.f / op.temperature;
+    const float base = base_of(q.m), lq = log2_fast(q.s), lt = log2_fast(teach.s), tbase = base_of(teach.m);
     float part = 0.f;
     for (int e = t; e < padded; e += RT) {
       const int i = id[e];
@@ -332,8 +337,7 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_distill(muon_dist
       if (i >= 0) {
         const float le = (pt[e] - tbase) * k - lt;   // log2 of p
         pe = exp2_fast(le);
-        // (in natural units, in which a column of the type's lowest value is a number)
-        if (pe != 0.f) part += pe * (le * kLn2 - ((value_at(p + i) - base) * cool - lq));
+        if (pe != 0.f) part += pe * (le * 0.5f - half_log2(value_at(p + i), base, k, lq));
       }
       pt[e] = pe;
     }
@@ -352,7 +356,7 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_distill(muon_dist
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < RT / 64; ++w) sum += sh.part[w];
-      gst<float>(op.loss + row, none ? 0.f : a * op.temperature * sum);
+      gst<float>(op.loss + row, none ? 0.f : a * op.temperature * (2 * kLn2) * sum);
     }
     if (out && !none)
       for (int e = t; e < top; e += RT) {
@@ -410,8 +414,7 @@ __global__ __launch_bounds__(RT, (occupancy<T, VPL>())) void k_policy(muon_polic
     __syncthreads();
     const Soft q = block_join<RT>(sh, 0, k);
     const float base = base_of(q.m), la = (xa - base) * k;
-    // from the difference, which times k would be infinite where xa is the type's lowest value
-    const float logp = (xa - base) * (1.f / op.temperature) - log2_fast(q.s) * kLn2;
+    const float logp = half_log2(xa, base, k, log2_fast(q.s)) * (2 * kLn2);
     const float ratio = expf(logp - old);
     // an advantage of 0 has no part, whatever the ratio
     const float free = adv == 0.f ? 0.f : ratio * adv;

@@ -350,8 +350,8 @@ def test_a_kl_coefficient_of_zero_takes_no_part(dtype):
 @pytest.mark.parametrize("dtype", TYPES, ids=ids_of)
 def test_entries_on_a_column_of_the_lowest_value(dtype, temperature):
     """A column masked with the type's lowest value has a log-probability of about -3e38 / temperature, not of -infinity.
-    Relative to it: the difference, the quotient by the temperature (two roundings), the log's subtraction, a product and
-    the weight's: 8 u; the log of the sum is 2^-120 of it."""
+    Relative to it: the difference, log2(e) / temperature (two roundings), the product with it, the log's subtraction and the
+    product with ln 2 (two): 8 u; the log of the sum is 2^-120 of it."""
     low = torch.finfo(dtype).min
     z = torch.randn(2, 700, generator=gen(4)).to(dtype)
     z[:, 5] = low
