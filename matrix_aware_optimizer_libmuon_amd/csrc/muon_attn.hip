@@ -10,13 +10,14 @@
 // Rounded to bf16: P and dS as operands of the second products, whose sums are fp32 (half
 // a step, 2^-8, of each term, as the inputs have), and the outputs, once.
 //
-// 4 x 4096 tokens, 32 heads of 128 over 8 of K and V, causal: forward 553 to 589 us (930
-// to 990 TFLOP/s), backward 1720 to 1790 (770 to 800, five products counted; dQ 732 and dK,
-// dV 947); 8192 tokens of 16 heads without a mask 1052 and 858; heads of 64: 896 and 779.
-// A library product of 8192^3 reaches 1309 to 1391.  Bound by the matrix units, the
-// exponentials (a quarter of other instructions' rate; at 64 columns vector instructions
-// take as long as matrix ones) and power: 49 to 57 % of the cycles with a matrix
-// instruction, at 1.7 to 1.9 GHz.  No LDS conflicts.
+// 4 x 4096 tokens, 32 heads of 128 over 8 of K and V, causal: forward 553 to 590 us (930
+// to 990 TFLOP/s), backward 1720 to 1810 (760 to 800, five products counted; dQ 728 and dK,
+// dV 958); 8192 tokens of 16 heads without a mask 1020 and 841; heads of 64: 904 and 764.
+// A library product of 8192^3 reaches 1309 to 1409.  50 to 57 % of the cycles have a matrix
+// instruction (38 at 64 columns, where vector instructions take as long as matrix ones; the
+// exponentials run at a quarter of other instructions' rate).  Two waves share a SIMD, and in
+// the forward pass each spends 37 % of its time ready but not issued and 21 % at waits and
+// barriers: the softmax of a step stands between its two products.  No LDS conflicts.
 //
 // Layout.  A wave owns 32 queries (or keys), one per lane and half: it forms the
 // transposed product S^T = K Q^T with v_mfma_f32_32x32x16_bf16, whose result leaves
@@ -409,16 +410,16 @@ __device__ __forceinline__ Place locate(Args... args) {
 // at most, which costs no precision, and the sums are multiplied in few of the tiles
 // instead of all.  The first load of the loop has to find nothing of the compiler's in
 // flight (`arrived`): with Q's loads pending it waited for the next tile in each step (659
-// us instead of 594 for the case above).
+// us instead of 594 for the case above, when it was found).
 constexpr float kSlack = 8.f;
 
 //
 // PACKED: a tile's rows are the queries of all heads that share a key and value head, one
 // query after the other (row i: query i / group), so that few queries a sequence read their
 // keys and values once, and a tile spans fewer queries, which a causal mask cuts closer (us
-// with and without: 32 single queries over 4096 keys each, 32 heads of 128 over 8, 110, at
-// 4.9 TB/s, and 290; 23 sequences of 100 to 800 with 16 heads of 80 over 4, causal, 31 and
-// 41; 4 x 4096 as above 564 and 571).
+// with and without: 32 single queries over 4096 keys each, 32 heads of 128 over 8, 104, at
+// 5.2 TB/s, and 217; 23 sequences of 8 to 1843 with 16 heads of 80 over 4, causal, 48 and
+// 61; 8192 with 16 heads of 64 over 2 175 and 193; 4 x 4096 as above 566 and 575).
 template <int DB, bool ALIGNED, bool PACKED>
 __global__ __launch_bounds__(kThreads, DB == 3 ? 3 : 2) void k_attn(muon_attention_t op, uint32_t units, float* part_o, float* part_lse) {
   using G = Geo<DB>;
@@ -890,8 +891,9 @@ __global__ __launch_bounds__(64 * kKeyWaves<DB>, 2) void k_attn_dkv(muon_attenti
   dkv_tile<DB, ALIGNED, true>(op, grid(units), stats, part_dkv, smem);
 }
 
-// Both in one launch, where the chip has a place for every block: the first q_blocks make dQ, the
-// others dK and dV, with rowsum(dO O) for themselves.
+// Both in one launch, for few blocks: the first q_blocks make dQ, the others dK and dV, with
+// rowsum(dO O) for themselves.  Past 96 columns a block has a CU's LDS to itself, so that there
+// 257 and more take two rounds.
 template <int DB, bool ALIGNED>
 __global__ __launch_bounds__(64 * kKeyWaves<DB>, 2) void k_attn_grad(muon_attention_grad_t op, uint32_t units, uint32_t q_blocks, uint32_t k_units) {
   constexpr int bytes = KeyLds<DB>::bytes > 4 * Geo<DB>::TILE ? KeyLds<DB>::bytes : 4 * Geo<DB>::TILE;
@@ -973,10 +975,15 @@ int by_shape(int64_t dim, bool aligned, F&& f) {
 
 int key_rows(int64_t dim) { return dim > 96 ? 32 * kKeyWaves<4> : 32 * kKeyWaves<2>; }   // that a block of k_attn_dkv owns
 
-// Parts that the steps of `blocks` blocks are cut into, `steps` each on average: so many
-// that the chip's 512 places (two blocks a CU) are filled, of 8 steps at least: the join
-// costs a launch (with 4 steps 1024 tokens of 32 heads of 64 took 27 and 62 us instead of
-// 20 and 45; 32 queries over 8192 keys, 8 heads of 128: 28 and 44, without parts 139 and 200).
+// Parts that the steps of `blocks` blocks are cut into, `steps` each on average: up to 512
+// blocks, of 8 steps at least: the join costs a launch.  Forward and backward, us, with parts
+// of 8 steps, of 4, and whole: 32 queries over 8192 keys, 8 heads of 128, 25 and 40, 28 and
+// 40, 137 and 156; causal, 1024 tokens of 32 heads of 64, 20 and 45, 27 and 63, 20 and 45;
+// 2048 of 8 heads of 64 27 and 64, -, 31 and 65.  (512 is two blocks a CU.  k_attn_dkv<4>, whose
+// LDS allows one, would do with half: 4096 causal tokens of 8 heads of 128 over 2 take 244 us
+// backward, with 256 215.  And two parts cost more than they give where the whole would be one
+// launch: 1024 tokens of 8 heads of 64 without a mask 42 us backward, whole 35.  The average is
+// all that the host knows of the sequences: one long one among many short is not cut.)
 int parts_of(int64_t blocks, int64_t steps, int64_t most = kMaxParts) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most, 512 / std::max<int64_t>(blocks, 1), steps / 8})));
 }
@@ -1023,7 +1030,8 @@ AttnGradPlan attention_grad_plan(const muon_attention_grad_t& op) {
   const int own = key_rows(op.dim);
   p.parts_k = parts_of((op.k_tokens + own - 1) / own * op.kv_heads, op.heads / op.kv_heads * average_steps(op, op.k_tokens));
   const bool ragged = op.starts != nullptr;
-  // (2 x 37 tokens, 4 heads of 64: 12.5 us, two launches 17.4; 512 tokens, 8 heads: 21, 32)
+  // (us, and in two launches: 2 x 37 tokens, 4 heads of 64, 13, 18; 512, 8 of 64, 21, 29; 1024, 16
+  // of 64, 36, 45; 1024, 28 of 128, 76, 87; 32 of 128 88, 87; but 4 x 256, 32 of 128 over 8, 89, 75)
   p.one_launch = p.parts_q == 1 && p.parts_k == 1 &&
                  units_of(op.tokens, op.sequences, ragged) * op.heads + units_of(op.k_tokens, op.sequences, ragged, own) * op.kv_heads <= 512;
   if (p.one_launch) return p;

@@ -4,18 +4,20 @@
 // Both need, of a token's row x = z / temperature, the softmax's maximum and sum
 // and a few single entries, and their gradient is
 //   dz = a softmax(x)  plus a value at each of those few entries.
-// A block takes a row, or, of few long ones, its share of a row's gradient.  Up to 131072 columns in bf16 and 65536 in fp32 the row stays in
-// registers, so the logits are read once and the gradient written once; a longer row is
-// read again for the gradient (from the caches, which hold the rows in work).  Bound by
-// memory: distillation 16384 x 32000 bf16 405 us (4.9 TB/s), policy loss with 30 % of the
-// rows masked 331 us (5.4); a large copy runs at 4.8.  A single row is bound by one CU's
+// A block takes a row, or, of few long ones, its share of a row's gradient.  Up to 131072
+// columns in bf16 and 65536 in fp32 the row stays in registers, so the logits are read once
+// and the gradient written once; a longer row is read again for the gradient (from the
+// caches, which hold the rows in work).  Bound by memory: distillation 16384 x 32000 bf16
+// 409 us (4.9 TB/s), policy loss with 30 % of the rows masked 331 us (5.4); a large copy
+// runs at 4.7 to 4.8.  A single row is bound by one CU's
 // exponentials, a quarter of the rate of other instructions, 32000 of them twice in 9 us.
 //
 // Numbers.  x - max is taken before the factor log2(e) / temperature, so that rows
 // of the type's lowest value stay finite, and a single log2 of a probability is
-// halved, so that it does for a column of that value; sums run in fp32, up to 128 terms a
-// thread, then over the wave and the waves in a fixed order.  The gradient is
-// rounded once, to the logits' type.
+// halved, so that it does for a column of that value.  Sums run in fp32, in trees: a term
+// goes through 19 roundings at most in a thread whose row is in registers, through 80 where
+// it is read twice, then through the wave's and the waves' in a fixed order.  The gradient
+// is rounded once, to the logits' type.
 #include <type_traits>
 
 #include "muon_act8.h"
@@ -259,8 +261,10 @@ struct Row<T, RT, 0, SHARED> {
   __device__ __forceinline__ bool wrote(int c) const { return has(c) && (c >> 3) % RT == t; }
 };
 
-// Waves a SIMD, by the registers that the row takes of the 64, 80 or 128 they leave (16384
-// x 32000 in bf16: 6 waves 338 us, 8 with some of the row spilled 359, 4 521).
+// Waves a SIMD, by the registers that the row takes of the 64, 80 or 128 they leave (policy
+// loss, 16384 x 32000 in bf16: 6 waves 338 us, 8 with some of the row spilled 359, 4 521).
+// Also as it is some instances keep up to 8 values besides the row in scratch, written and
+// read once a row; k_distill<*, 64, *> has 5 waves, for its LDS.
 template <class T, int VPL>
 constexpr int occupancy() {
   constexpr int row = (VPL ? VPL : kPass) * static_cast<int>(sizeof(T)) * 2;
@@ -483,9 +487,9 @@ unsigned rows_grid(int64_t tokens) { return static_cast<unsigned>(tokens < kMaxG
 // Blocks of a long row: where the chip has more CUs than there are rows, several take the
 // same one, each with statistics of its own, and share the writing of its gradient (and
 // the second exponentials): no exchange between them, and the same bits.  One row of
-// 200000 columns in bf16 27 -> 18 us, of 131072 18 -> 12, 128 of them 24 -> 22, one of
-// 32000 9 with and without; many rows would pay 1 to 2 % for the choice, so it is a
-// kernel of its own.
+// 200000 columns in bf16 27 us alone, 18 shared, of 131072 18, 12, 128 of them 24, 22, 20 of
+// 200000 in fp32 35, 20, one of 32000 9 with and without; many rows would pay 1 to 2 % for
+// the choice, so it is a kernel of its own.
 constexpr bool shares(int rt, int vpl) { return rt == 1024 && (vpl == 0 || vpl >= 8); }
 unsigned share_of(int64_t rows, int vpl, bool gradient) {
   unsigned share = 1;
