@@ -163,7 +163,8 @@ def attention(q, k, v, *, starts=None, k_starts=None, causal: bool = True, scale
     ``scale``: 1 / sqrt(dim) if None.  lse (float32, (heads, tokens)) is each row's log
     of the sum of exponentials, for the backward pass; a query that sees no key gets
     zeros and -infinity.  Tokens behind the last sequence: left as they are in
-    ``out``, zeros in a new tensor; their lse is -infinity."""
+    ``out``, zeros in a new tensor; their lse is -infinity.  A value that is not finite
+    may reach every row of its sequence and head, masked or not, but no other sequence."""
     return tuple(_run("attention", q, stream, q, k, v, starts, k_starts, bool(causal), None if scale is None else float(scale), out))
 
 
@@ -200,7 +201,7 @@ def policy_loss(logits, actions, old_logp, advantages, *, ref_logp=None, clip: f
 
     float32 per token, and ``dlogits`` the gradient of loss.sum(), in the logits' type
     (None if not wanted).  No KL term without ``ref_logp`` or at a ``kl_coef`` of 0;
-    ``clip_high``: clip if None.
+    ``clip``: 0 .. 1; ``clip_high``: clip if None.
     ``weights``: float32 per token; a token of weight 0, or whose action is outside
     the vocabulary, has loss and logp 0, and its logits are not read."""
     return tuple(_run("policy_loss", logits, stream, logits, actions, old_logp, advantages, ref_logp, weights, out, float(clip),

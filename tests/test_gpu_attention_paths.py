@@ -51,3 +51,15 @@ def test_outputs_in_every_layout(layout, nq, nk, heads, kv, dim):
         assert torch.equal(view, w)
         around = torch.empty(0, device=DEV, dtype=BF).set_(view.untyped_storage())
         assert int(torch.isfinite(around).sum()) == view.numel()
+
+
+@pytest.mark.parametrize("n,heads,kv", [(90, 4, 2), (2400, 4, 1), (1100, 32, 32)])
+def test_lse_with_rows_of_a_wider_buffer(n, heads, kv):
+    """One launch, two with parts, two without: the same bits, whatever lies behind a row."""
+    q, k, v = tensors(2, n, n, heads, kv, 64)
+    o, lse = muon.attention(q, k, v)
+    do = placed(torch.randn(q.shape, generator=gen(1)).to(BF), "plain")
+    wide = torch.full((heads, n + 13), float("nan"), device=DEV)
+    wide[:, 5:5 + n] = lse
+    for a, b in zip(muon.attention_grad(do, q, k, v, o, lse), muon.attention_grad(do, q, k, v, o, wide[:, 5:5 + n])):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
